@@ -281,6 +281,99 @@ FORGE_API forge_status_t forge_dequantize_state_block(const void* codes, const f
                                                       int32_t is_signed, int32_t block,
                                                       void* stream);
 
+/* ---------------------------------------------------------------------------
+ * The operators around the linear step: the norm that makes X, and the
+ * optimizer step of the parameters that are not a linear's weight.
+ * ------------------------------------------------------------------------- */
+
+/* Gradient dtypes of forge_multi_opt_step. */
+typedef enum forge_g_dtype { FORGE_G_FP32 = 0, FORGE_G_BF16 = 1 } forge_g_dtype_t;
+
+/* One tensor of forge_multi_opt_step: n elements, contiguous, in any shape. */
+typedef struct forge_tensor {
+  int64_t n;          /* elements; any length, 0 included                     */
+  const void* grad;   /* g_dtype, or NULL for a zero gradient                  */
+  void* W;            /* w_dtype, updated in place                             */
+  void* s1;           /* s_dtype, as in forge_state_t                          */
+  void* s2;
+  float* s1_scale;    /* INT8: one absmax per block, ceil(n / B) of them       */
+  float* s2_scale;
+} forge_tensor_t;
+
+/* One step of rule `opt_kind` on `count` tensors whose gradients exist:
+ * norms, embeddings, biases, gates.  Per element the arithmetic is that of
+ * forge_unfused_opt_step; all tensors share the dtypes, hyper-parameters and
+ * step (call once per group).  INT8 blocks run along the flattened tensor;
+ * its last block may be short.  BF16 weights round stochastically with the
+ * element's index in its tensor and the seed `seed` + i for tensors[i], so one
+ * tensor steps as forge_unfused_opt_step steps it with that seed.  Every
+ * pairing of w_dtype and s_dtype is supported.  One launch per 480 tensors
+ * that are not empty; the table travels with the launch, so `tensors` may be
+ * freed on return. */
+FORGE_API forge_status_t forge_multi_opt_step(const forge_tensor_t* tensors, int32_t count,
+                                              int32_t w_dtype, int32_t g_dtype, int32_t s_dtype,
+                                              int32_t opt_kind, const forge_hparams_t* hp,
+                                              int64_t step, uint64_t seed, void* stream);
+
+/* Root-mean-square norm of T tokens of K columns (K % 8 == 0, 8 <= K <= 16384):
+ *   h = bf16(x + residual), or x where residual is NULL;
+ *   rstd = 1 / sqrt(mean_k h^2 + eps);   y = h * rstd * w.
+ * Statistics and y are float32 from the rounded h, so that the gradient, which
+ * reads h, is that of the function computed.  Outputs that are not NULL:
+ *   h         bf16 [T x K], needed with a residual; may be x or residual itself
+ *   rstd      [T]
+ *   y         bf16 [T x K]
+ *   yq        E4M3 codes [T x K] with one scale per token in yq_scale [T]:
+ *             scale = max_k |y| / 448, code = E4M3(y / scale); a zero row has
+ *             scale 0 and zero codes; a row with a value that is not finite
+ *             has NaN scale and codes
+ *   yt        E4M3 codes [K x T] (token-contiguous, as forge_linear_bwd_step_fp8
+ *             reads X) of y / yt_scale, saturating at +-448; T % 16 == 0
+ *   amax      [1], with yt: max |y| over the tensor (NaN if any row has a value
+ *             that is not finite), from which the caller forms the next step's
+ *             yt_scale */
+typedef struct forge_rmsnorm {
+  int64_t T, K;
+  const void* x;         /* bf16 [T x K]                                     */
+  const void* residual;  /* bf16 [T x K] or NULL                             */
+  const void* w;         /* bf16 [K]                                         */
+  float eps;
+  float yt_scale;        /* finite and > 0 (its reciprocal too) when yt is set */
+  void* h;
+  float* rstd;
+  void* y;
+  void* yq;
+  float* yq_scale;
+  void* yt;
+  float* amax;
+} forge_rmsnorm_t;
+FORGE_API forge_status_t forge_rmsnorm_fwd(const forge_rmsnorm_t* norm, void* stream);
+
+/* Its gradient: with n = h * rstd and g = dy * w,
+ *   dx = rstd * (g - n * mean_k(g * n)) + dh     bf16 [T x K]
+ *   dw = sum_t dy * n                            float32 [K]
+ * dx is the gradient of x and of the residual alike; dh, the gradient that
+ * reaches h along the residual stream, may be NULL; dx may be dy or dh itself.
+ * The sum over tokens goes through `workspace`
+ * (forge_rmsnorm_bwd_workspace(T, K) floats, contents irrelevant) in a fixed
+ * order: the same inputs give the same bits on the same device. */
+typedef struct forge_rmsnorm_grad {
+  int64_t T, K;
+  const void* dy;        /* bf16 [T x K]                                     */
+  const void* h;         /* bf16 [T x K]: what the forward normalised          */
+  const void* w;         /* bf16 [K]                                         */
+  const float* rstd;     /* [T]                                              */
+  const void* dh;        /* bf16 [T x K] or NULL                             */
+  void* dx;
+  float* dw;
+  float* workspace;
+} forge_rmsnorm_grad_t;
+FORGE_API forge_status_t forge_rmsnorm_bwd(const forge_rmsnorm_grad_t* grad, void* stream);
+
+/* Floats of workspace that forge_rmsnorm_bwd needs on the current device; -1
+ * (with a message) when the shape is not supported or there is no device. */
+FORGE_API int64_t forge_rmsnorm_bwd_workspace(int64_t T, int64_t K);
+
 /* Synchronises `stream`, then returns and clears the current device's status
  * word: FORGE_OK, FORGE_ERR_TIMEOUT (a bounded wait expired in a kernel) or
  * FORGE_ERR_CUDA (the stream reported a CUDA error). */

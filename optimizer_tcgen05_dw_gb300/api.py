@@ -25,6 +25,7 @@ STATE_FP32, STATE_INT8_B64, STATE_BF16 = 0, 1, 2
 STATE_INT8_B32, STATE_INT8_B128, STATE_INT8_B256 = 3, 4, 5
 INT8_STATE_OF_BLOCK = {32: STATE_INT8_B32, 64: STATE_INT8_B64, 128: STATE_INT8_B128,
                        256: STATE_INT8_B256}
+G_FP32, G_BF16 = 0, 1
 USES_S1 = {"adamw", "nadam", "radam", "lion", "sgd_momentum"}
 USES_S2 = {"adamw", "nadam", "radam", "rmsprop", "adagrad"}
 
@@ -50,6 +51,24 @@ class ForgeState(ctypes.Structure):
 class ForgeHparams(ctypes.Structure):
     _fields_ = [(n, c_float) for n in ("lr", "beta1", "beta2", "eps", "weight_decay", "alpha",
                                        "momentum")]
+
+
+class ForgeTensor(ctypes.Structure):
+    _fields_ = [("n", c_int64), ("grad", c_void_p), ("W", c_void_p), ("s1", c_void_p), ("s2", c_void_p),
+                ("s1_scale", c_void_p), ("s2_scale", c_void_p)]
+
+
+class ForgeRmsnorm(ctypes.Structure):
+    _fields_ = [("T", c_int64), ("K", c_int64), ("x", c_void_p), ("residual", c_void_p), ("w", c_void_p),
+                ("eps", c_float), ("yt_scale", c_float), ("h", c_void_p), ("rstd", c_void_p),
+                ("y", c_void_p), ("yq", c_void_p), ("yq_scale", c_void_p), ("yt", c_void_p),
+                ("amax", c_void_p)]
+
+
+class ForgeRmsnormGrad(ctypes.Structure):
+    _fields_ = [("T", c_int64), ("K", c_int64), ("dy", c_void_p), ("h", c_void_p), ("w", c_void_p),
+                ("rstd", c_void_p), ("dh", c_void_p), ("dx", c_void_p), ("dw", c_void_p),
+                ("workspace", c_void_p)]
 
 
 HPARAM_DEFAULTS = dict(lr=1e-3, beta1=0.9, beta2=0.999, eps=1e-8, weight_decay=0.0, alpha=0.99,
@@ -91,6 +110,12 @@ _SIGNATURES = {
                                              c_int32, c_void_p]),
     "forge_dequantize_state_block": (c_int32, [c_void_p, c_void_p, c_void_p, c_int64, c_int64, c_int32,
                                                c_int32, c_void_p]),
+    "forge_multi_opt_step": (c_int32, [ctypes.POINTER(ForgeTensor), c_int32, c_int32, c_int32, c_int32,
+                                       c_int32, ctypes.POINTER(ForgeHparams), c_int64, c_uint64,
+                                       c_void_p]),
+    "forge_rmsnorm_fwd": (c_int32, [ctypes.POINTER(ForgeRmsnorm), c_void_p]),
+    "forge_rmsnorm_bwd": (c_int32, [ctypes.POINTER(ForgeRmsnormGrad), c_void_p]),
+    "forge_rmsnorm_bwd_workspace": (c_int64, [c_int64, c_int64]),
     "forge_get_device_status": (c_int32, [c_void_p]),
     "forge_set_wait_limit_ns": (c_int32, [c_uint64]),
     "forge_debug_skip_loads": (c_int32, [c_int32]),
@@ -367,6 +392,165 @@ def forge_dequantize_state(codes, absmax, x, is_signed: bool, stream=None, block
     _need(absmax, "absmax", torch.float32, (rows, cols // block))
     _check(lib().forge_dequantize_state_block(_ptr(codes), _ptr(absmax), _ptr(x), rows, cols,
                                               1 if is_signed else 0, int(block), _stream(stream)))
+
+
+class ForgeTensors:
+    """The tensor table of forge_multi_opt_step (make_tensors builds it): the C
+    array of pointers, and the tensors themselves so that they stay alive."""
+
+    __slots__ = ("table", "count", "w_dtype", "g_dtype", "s_dtype", "kept")
+
+
+def _one_dtype(tensors, name, allowed):
+    """The dtype that the tensors share (None when there are none)."""
+    found = {t.dtype for t in tensors if t is not None}
+    if len(found) > 1:
+        raise TypeError(f"{name}: one dtype a call, got {sorted(map(str, found))}; make one table per dtype")
+    if not found:
+        return None
+    d = found.pop()
+    if d not in allowed:
+        raise TypeError(f"{name}: expected one of {', '.join(map(str, allowed))}, got {d}")
+    return d
+
+
+def _need_flat(t, name, dtype, n):
+    if t.dtype != dtype:
+        raise TypeError(f"{name}: expected {dtype}, got {t.dtype}")
+    if t.numel() != n:
+        raise ValueError(f"{name}: expected {n} elements, got {t.numel()}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+
+
+def make_tensors(weights, grads, s1=None, s2=None, s1_scale=None, s2_scale=None, block: int = 64) -> ForgeTensors:
+    """The table of one forge_multi_opt_step group, built once and used step
+    after step: lists of equal length of weights (float32 or bfloat16),
+    gradients (float32 or bfloat16; None entries mean a zero gradient) and
+    states (float32, bfloat16, or int8 s1 / uint8 s2 codes with float32 absmax
+    of ceil(n / block) blocks of the flattened tensor), any shapes and lengths,
+    contiguous.  The gradients' values may change between steps, their storage
+    may not: build a table again after replacing a tensor."""
+    weights, grads = list(weights), list(grads)
+    n = len(weights)
+
+    def listed(v, name):
+        v = [None] * n if v is None else list(v)
+        if len(v) != n:
+            raise ValueError(f"{name}: expected {n} tensors, got {len(v)}")
+        return v
+
+    grads, s1, s2 = listed(grads, "grads"), listed(s1, "s1"), listed(s2, "s2")
+    s1_scale, s2_scale = listed(s1_scale, "s1_scale"), listed(s2_scale, "s2_scale")
+    if any(w is None for w in weights):
+        raise ValueError("weights: every entry must be a tensor")
+    f32, b16 = torch.float32, torch.bfloat16
+    wd = _one_dtype(weights, "weights", (f32, b16)) or f32
+    gd = _one_dtype(grads, "grads", (f32, b16)) or f32
+    d1 = _one_dtype(s1, "s1", (f32, b16, torch.int8))
+    d2 = _one_dtype(s2, "s2", (f32, b16, torch.uint8))
+    int8 = d1 == torch.int8 or d2 == torch.uint8
+    if d1 is not None and d2 is not None and (d1 == torch.int8) != (d2 == torch.uint8) \
+            or not int8 and None not in (d1, d2) and d1 != d2:
+        raise TypeError(f"s1 and s2 must be kept alike, got {d1} and {d2}")
+    if int8 and block not in INT8_STATE_OF_BLOCK:
+        raise ValueError("block must be 32, 64, 128 or 256")
+    out = ForgeTensors()
+    out.count = n
+    out.w_dtype = W_FP32 if wd == f32 else W_BF16_SR
+    out.g_dtype = G_FP32 if gd == f32 else G_BF16
+    out.s_dtype = (INT8_STATE_OF_BLOCK[block] if int8 else STATE_BF16 if b16 in (d1, d2) else STATE_FP32)
+    out.table = (ForgeTensor * max(1, n))()
+    for i, (w, g, a, b, sa, sb) in enumerate(zip(weights, grads, s1, s2, s1_scale, s2_scale)):
+        e = w.numel()
+        _need_flat(w, f"weights[{i}]", wd, e)
+        for t, name, d in ((g, "grads", gd), (a, "s1", d1), (b, "s2", d2)):
+            if t is not None:
+                _need_flat(t, f"{name}[{i}]", d, e)
+        if int8:
+            for t, sc, name in ((a, sa, "s1_scale"), (b, sb, "s2_scale")):
+                if t is not None:
+                    if sc is None:
+                        raise ValueError(f"{name}[{i}] is required with INT8 states")
+                    _need_flat(sc, f"{name}[{i}]", f32, (e + block - 1) // block)
+        out.table[i] = ForgeTensor(e, _ptr(g), _ptr(w), _ptr(a), _ptr(b), _ptr(sa) if int8 else None,
+                                   _ptr(sb) if int8 else None)
+    out.kept = (weights, grads, s1, s2, s1_scale, s2_scale)
+    return out
+
+
+def forge_multi_opt_step(tensors: ForgeTensors, opt: str, hp: dict, step: int, seed: int, stream=None):
+    """One optimizer step over every tensor of the table (make_tensors), in
+    place; bf16 weights of tensor i round with the seed `seed + i`."""
+    _check(lib().forge_multi_opt_step(tensors.table, tensors.count, tensors.w_dtype, tensors.g_dtype,
+                                      tensors.s_dtype, OPT_KINDS[opt], ctypes.byref(_hparams_of(hp)),
+                                      int(step), int(seed) & 0xFFFFFFFFFFFFFFFF, _stream(stream)))
+
+
+def _rows(t, name):
+    if t.dim() != 2:
+        raise ValueError(f"{name}: expected a [T, K] tensor, got {tuple(t.shape)}")
+    return t.shape
+
+
+def forge_rmsnorm_fwd(x, w, eps: float, residual=None, h=None, rstd=None, y=None, yq=None, yq_scale=None,
+                      yt=None, yt_scale: float = 1.0, amax=None, stream=None):
+    """Root-mean-square norm of x [T, K] bf16 (+ residual) with weight w [K]
+    bf16.  Writes the outputs given: h (the sum, bf16; may be x or residual), rstd [T], y
+    [T, K] bf16, yq [T, K] E4M3 with yq_scale [T], yt [K, T] E4M3 of y /
+    yt_scale with amax [1]."""
+    T, K = shape = _rows(x, "x")
+    _need(x, "x", torch.bfloat16, shape)
+    _need(w, "w", torch.bfloat16, (K,))
+    if residual is not None:
+        _need(residual, "residual", torch.bfloat16, shape)
+    if h is not None:
+        _need(h, "h", torch.bfloat16, shape)
+    if rstd is not None:
+        _need(rstd, "rstd", torch.float32, (T,))
+    if y is not None:
+        _need(y, "y", torch.bfloat16, shape)
+    if yq is not None:
+        _need(yq, "yq", torch.float8_e4m3fn, shape)
+        _need(yq_scale, "yq_scale", torch.float32, (T,))
+    if yt is not None:
+        _need(yt, "yt", torch.float8_e4m3fn, (K, T))
+    if amax is not None:
+        _need(amax, "amax", torch.float32, (1,))
+    p = ForgeRmsnorm(T, K, x.data_ptr(), _ptr(residual), w.data_ptr(), eps, yt_scale, _ptr(h), _ptr(rstd), _ptr(y),
+                     _ptr(yq), _ptr(yq_scale), _ptr(yt), _ptr(amax))
+    _check(lib().forge_rmsnorm_fwd(ctypes.byref(p), _stream(stream)))
+
+
+def forge_rmsnorm_bwd_workspace(T: int, K: int) -> int:
+    """Floats of workspace that forge_rmsnorm_bwd needs for [T, K]."""
+    n = lib().forge_rmsnorm_bwd_workspace(int(T), int(K))
+    if n < 0:
+        raise ForgeError(1, lib().forge_last_error_message().decode(errors="replace"))
+    return int(n)
+
+
+def forge_rmsnorm_bwd(dy, h, w, rstd, dx, dw, workspace, dh=None, stream=None):
+    """Gradient of forge_rmsnorm_fwd: dx [T, K] bf16 (of x and the residual
+    alike; dh, the gradient reaching h itself, is added) and dw [K] float32.
+    workspace: float32, forge_rmsnorm_bwd_workspace(T, K) elements or more."""
+    T, K = shape = _rows(dy, "dy")
+    _need(dy, "dy", torch.bfloat16, shape)
+    _need(h, "h", torch.bfloat16, shape)
+    _need(w, "w", torch.bfloat16, (K,))
+    _need(rstd, "rstd", torch.float32, (T,))
+    _need(dx, "dx", torch.bfloat16, shape)
+    _need(dw, "dw", torch.float32, (K,))
+    if dh is not None:
+        _need(dh, "dh", torch.bfloat16, shape)
+    _need(workspace, "workspace", torch.float32, workspace.shape)
+    if workspace.numel() < forge_rmsnorm_bwd_workspace(T, K):
+        raise ValueError(f"workspace: need {forge_rmsnorm_bwd_workspace(T, K)} elements, got {workspace.numel()}")
+    p = ForgeRmsnormGrad(T, K, dy.data_ptr(), h.data_ptr(), w.data_ptr(), rstd.data_ptr(), _ptr(dh), dx.data_ptr(),
+                         dw.data_ptr(), workspace.data_ptr())
+    _check(lib().forge_rmsnorm_bwd(ctypes.byref(p), _stream(stream)))
 
 
 def forge_get_device_status(stream=None):

@@ -17,6 +17,7 @@
 
 #include "forge.h"
 #include "common.h"
+#include "host.h"
 #include "launch.h"
 
 namespace forge {
@@ -39,9 +40,9 @@ __device__ uint32_t g_dx_done[kMaxDxBlocks + 2];  // + the residency gate's two 
 constexpr int kStaticScratchWords = 1024;
 static __device__ __align__(256) uint32_t g_static_scratch[kStaticScratchWords + 2];
 
-namespace {
+static thread_local char g_msg[512] = "";
 
-thread_local char g_msg[512] = "";
+void clear_message() { g_msg[0] = '\0'; }
 
 forge_status_t fail(forge_status_t st, const char* fmt, ...) {
   va_list ap;
@@ -55,26 +56,20 @@ forge_status_t cuda_fail(cudaError_t e, const char* what) {
   return fail(FORGE_ERR_CUDA, "%s: %s", what, cudaGetErrorString(e));
 }
 
-std::atomic<uint64_t> g_wait_limit_ns{2000000000ull};
-std::atomic<int32_t> g_skip_loads{0};
-std::atomic<int32_t> g_step_fusion{1};
+static std::atomic<uint64_t> g_wait_limit_ns{2000000000ull};
+static std::atomic<int32_t> g_skip_loads{0};
+static std::atomic<int32_t> g_step_fusion{1};
+
+uint64_t wait_limit_ns() { return g_wait_limit_ns.load(); }
+bool skip_loads() { return g_skip_loads.load() != 0; }
 
 // ---------------------------------------------------------------- per device
 
 constexpr int kMaxDevices = 64;
 
-struct DeviceInfo {
-  int num_sms = 0;
-  uint32_t* status = nullptr;
-  uint32_t* dx_done = nullptr;
-  uint32_t* static_scratch = nullptr;  // g_static_scratch on this device
-  int step_pairs[kNumKernelSdt] = {};  // resident one-launch-step pairs, by kernel state dtype
-  int cc_major = 0, cc_minor = 0;
-};
-
-std::mutex g_dev_mu;
-DeviceInfo g_dev[kMaxDevices];
-bool g_dev_ready[kMaxDevices] = {};
+static std::mutex g_dev_mu;
+static DeviceInfo g_dev[kMaxDevices];
+static bool g_dev_ready[kMaxDevices] = {};
 
 forge_status_t device_info(DeviceInfo* out) {
   int dev = 0;
@@ -120,7 +115,7 @@ using EncodeFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, voi
                               CUtensorMapInterleave, CUtensorMapSwizzle, CUtensorMapL2promotion,
                               CUtensorMapFloatOOBfill);
 
-forge_status_t encode_fn(EncodeFn* fn) {
+static forge_status_t encode_fn(EncodeFn* fn) {
   static std::once_flag once;
   static EncodeFn cached = nullptr;
   static cudaError_t err = cudaSuccess;
@@ -157,6 +152,23 @@ forge_status_t tensor_map(CUtensorMap* m, const void* base, CUtensorMapDataType 
   if (r != CUDA_SUCCESS)
     return fail(FORGE_ERR_CUDA, "cuTensorMapEncodeTiled failed (%d) for [%lld x %lld]", static_cast<int>(r),
                 static_cast<long long>(outer), static_cast<long long>(inner));
+  return FORGE_OK;
+}
+
+// The same for any rank up to 5 (dims innermost first; strides in bytes of
+// dims 1 ..).
+forge_status_t tensor_map_nd(CUtensorMap* m, const void* base, CUtensorMapDataType dtype, int rank,
+                             const cuuint64_t* dims, const cuuint64_t* strides, const cuuint32_t* box,
+                             CUtensorMapSwizzle swizzle) {
+  EncodeFn fn;
+  forge_status_t st = encode_fn(&fn);
+  if (st != FORGE_OK) return st;
+  const cuuint32_t estr[5] = {1, 1, 1, 1, 1};
+  CUresult r = fn(m, dtype, static_cast<cuuint32_t>(rank), const_cast<void*>(base), dims, strides, box, estr,
+                  CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r != CUDA_SUCCESS)
+    return fail(FORGE_ERR_CUDA, "cuTensorMapEncodeTiled (%d-D) failed (%d)", rank, static_cast<int>(r));
   return FORGE_OK;
 }
 
@@ -670,7 +682,6 @@ forge_status_t bwd_step(const forge_linear_t* lin, const forge_state_t* state, i
   return FORGE_OK;
 }
 
-}  // namespace
 }  // namespace forge
 
 using namespace forge;
@@ -680,14 +691,14 @@ extern "C" {
 forge_status_t forge_linear_bwd_step(const forge_linear_t* lin, const forge_state_t* state,
                                      int32_t opt_kind, const forge_hparams_t* hp, int64_t step,
                                      uint64_t seed, void* stream) {
-  g_msg[0] = '\0';
+  clear_message();
   return bwd_step(lin, state, opt_kind, hp, step, seed, 0, stream);
 }
 
 forge_status_t forge_linear_bwd_step_shard(const forge_linear_t* lin, const forge_state_t* state,
                                            int32_t opt_kind, const forge_hparams_t* hp, int64_t step,
                                            uint64_t seed, int64_t row_offset, void* stream) {
-  g_msg[0] = '\0';
+  clear_message();
   if (row_offset < 0) return fail(FORGE_ERR_INVALID_ARG, "row_offset must be >= 0 (got %lld)", (long long)row_offset);
   if (lin != nullptr && row_offset > (int64_t{1} << 31) - 1 - lin->N)
     return fail(FORGE_ERR_UNSUPPORTED, "row_offset + N must fit in 31 bits");
@@ -697,7 +708,7 @@ forge_status_t forge_linear_bwd_step_shard(const forge_linear_t* lin, const forg
 forge_status_t forge_linear_bwd_step_static(const forge_linear_t* lin, const forge_state_t* state,
                                             int32_t opt_kind, const forge_hparams_t* hp,
                                             int64_t step, uint64_t seed, void* stream) {
-  g_msg[0] = '\0';
+  clear_message();
   forge_status_t st;
   if ((st = check_linear(lin, true)) != FORGE_OK) return st;
   if ((st = check_hp(opt_kind, hp, step)) != FORGE_OK) return st;
@@ -722,7 +733,7 @@ forge_status_t forge_linear_bwd_step_static(const forge_linear_t* lin, const for
 forge_status_t forge_linear_bwd_step_fp8(const forge_linear_fp8_t* lin, const forge_state_t* state,
                                          int32_t opt_kind, const forge_hparams_t* hp, int64_t step,
                                          uint64_t seed, void* stream) {
-  g_msg[0] = '\0';
+  clear_message();
   forge_status_t st;
   if (lin == nullptr) return fail(FORGE_ERR_INVALID_ARG, "lin is NULL");
   const int64_t T = lin->T, N = lin->N, K = lin->K;
@@ -805,7 +816,7 @@ forge_status_t forge_linear_bwd_step_fp8(const forge_linear_fp8_t* lin, const fo
 void forge_set_step_fusion(int32_t enable) { g_step_fusion.store(enable != 0 ? 1 : 0); }
 
 forge_status_t forge_linear_dgrad(const forge_linear_t* lin, const void* W, int32_t w_dtype, void* stream) {
-  g_msg[0] = '\0';
+  clear_message();
   forge_status_t st;
   if ((st = check_linear(lin, false)) != FORGE_OK) return st;
   if (w_dtype != FORGE_W_FP32 && w_dtype != FORGE_W_BF16_SR) return fail(FORGE_ERR_INVALID_ARG, "w_dtype %d", w_dtype);
@@ -819,7 +830,7 @@ forge_status_t forge_linear_dgrad(const forge_linear_t* lin, const void* W, int3
 }
 
 forge_status_t forge_unfused_wgrad(const forge_linear_t* lin, float* dW, void* stream) {
-  g_msg[0] = '\0';
+  clear_message();
   forge_status_t st;
   if ((st = check_linear(lin, true)) != FORGE_OK) return st;
   if (lin->N == 0 || lin->K == 0) return FORGE_OK;
@@ -851,7 +862,7 @@ forge_status_t forge_unfused_wgrad(const forge_linear_t* lin, float* dW, void* s
 forge_status_t forge_unfused_opt_step(const float* dW, const forge_state_t* state, int64_t N, int64_t K,
                                       int32_t opt_kind, const forge_hparams_t* hp, int64_t step,
                                       uint64_t seed, void* stream) {
-  g_msg[0] = '\0';
+  clear_message();
   forge_status_t st;
   if (N < 0 || K < 0 || K % 8 != 0) return fail(FORGE_ERR_INVALID_ARG, "need N >= 0 and K %% 8 == 0");
   if ((st = check_hp(opt_kind, hp, step)) != FORGE_OK) return st;
@@ -889,7 +900,7 @@ static forge_status_t quant_common(const void* a, const void* b, const float* ab
 
 forge_status_t forge_quantize_state_block(const float* x, void* codes, float* absmax, int64_t rows,
                                           int64_t cols, int32_t is_signed, int32_t block, void* stream) {
-  g_msg[0] = '\0';
+  clear_message();
   forge_status_t st;
   if ((st = quant_common(x, codes, absmax, rows, cols, block)) != FORGE_OK) return st;
   if (rows * cols == 0) return FORGE_OK;
@@ -906,7 +917,7 @@ forge_status_t forge_quantize_state_block(const float* x, void* codes, float* ab
 
 forge_status_t forge_dequantize_state_block(const void* codes, const float* absmax, float* x, int64_t rows,
                                             int64_t cols, int32_t is_signed, int32_t block, void* stream) {
-  g_msg[0] = '\0';
+  clear_message();
   forge_status_t st;
   if ((st = quant_common(x, codes, absmax, rows, cols, block)) != FORGE_OK) return st;
   if (rows * cols == 0) return FORGE_OK;
@@ -933,7 +944,7 @@ forge_status_t forge_dequantize_state(const void* codes, const float* absmax, fl
 }
 
 forge_status_t forge_get_device_status(void* stream) {
-  g_msg[0] = '\0';
+  clear_message();
   forge_status_t st;
   DeviceInfo d;
   if ((st = device_info(&d)) != FORGE_OK) return st;

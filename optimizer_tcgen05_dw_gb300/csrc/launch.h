@@ -68,4 +68,59 @@ cudaError_t launch_dequantize(const ElemParams& p, int num_sms, cudaStream_t s);
 cudaError_t launch_dgrad_fp32w(const void* dY, const float* W, void* dX, int64_t T, int64_t N,
                                int64_t K, int num_sms, cudaStream_t s);
 
+
+// One tensor of a many-tensor optimizer step.
+struct MultiItem {
+  const void* g;     // gradient (nullptr = zero)
+  void* W;
+  void* s1;
+  void* s2;
+  float* s1_scale;
+  float* s2_scale;
+  int64_t n;         // elements
+  uint32_t first;    // its first tile in the launch
+  uint32_t index;    // its place in the caller's list: added to the rounding seed
+};
+// Tensors a launch carries in its parameters (64 bytes each): the short form
+// fits the 4 KB that every launch can pass at no extra cost.
+constexpr int kMultiShort = 56, kMultiLong = 480;
+constexpr int kMultiTile = 2048;  // elements per block
+template <int CAP>
+struct MultiParams {
+  OptScalars sc;
+  uint64_t seed, step;
+  int32_t count;     // tensors
+  int32_t qblock;    // INT8 states: elements per absmax block
+  MultiItem items[CAP];
+};
+// multi.cu: the rule over `tiles` tiles of p.count tensors, one block a tile.
+cudaError_t launch_multi(int wdt, int sdt, int gdt, const MultiParams<kMultiLong>& p, uint32_t tiles,
+                         cudaStream_t s);
+
+// Root-mean-square norm (norm.cu).
+struct NormParams {
+  const void* x;         // [T x K] bf16 input (bwd: the stream h the norm read)
+  const void* res;       // [T x K] bf16 residual, or nullptr
+  const void* w;         // [K] bf16
+  void* h;               // [T x K] bf16: x + residual, or nullptr
+  float* rstd;           // [T] (bwd: input), or nullptr
+  void* y;               // [T x K] bf16, or nullptr (bwd: dx)
+  void* q;               // [T x K] E4M3, or nullptr
+  float* q_scale;        // [T]
+  void* qt;              // [K x T] E4M3, or nullptr
+  float* amax;           // [1], or nullptr
+  const void* dy;        // bwd: [T x K] bf16
+  const void* dh;        // bwd: [T x K] bf16, or nullptr
+  float* dw;             // bwd: [K]
+  float* partial;        // bwd: [blocks x K]
+  int64_t T;
+  int32_t K;
+  float eps;
+  float inv_scale;       // qt: 1 / its scale
+};
+cudaError_t launch_norm_fwd(const NormParams& p, int num_sms, cudaStream_t s);
+cudaError_t launch_norm_bwd(const NormParams& p, int num_sms, cudaStream_t s);
+// Rows of p.partial that launch_norm_bwd uses.
+int64_t norm_bwd_blocks(int64_t T, int K, int num_sms);
+
 }  // namespace forge
