@@ -282,9 +282,48 @@ FORGE_API forge_status_t forge_dequantize_state_block(const void* codes, const f
                                                       void* stream);
 
 /* ---------------------------------------------------------------------------
- * The operators around the linear step: the norm that makes X, and the
- * optimizer step of the parameters that are not a linear's weight.
+ * The operators around the linear step: linears grouped by expert, the norm
+ * that makes X, and the optimizer step of the parameters that are not a
+ * linear's weight.
  * ------------------------------------------------------------------------- */
+
+/* Linears grouped by expert: token rows offsets[e] .. offsets[e + 1] - 1 of X,
+ * dY, Y and dX belong to expert e, whose weight W_e is [N x K]; the experts'
+ * weights (and states) lie one after the other: W is [groups x N x K].
+ *   - offsets is a DEVICE array of groups + 1 ascending int32 in [0, T], read
+ *     by the kernels when they run (nothing waits for it on the host).  A
+ *     group may be empty, of one row, or hold every row.  Offsets that
+ *     decrease or leave [0, T] are clamped and reported by
+ *     forge_get_device_status as FORGE_ERR_INVALID_ARG.
+ *   - N % 8 == 0, K % 8 == 0, groups <= 1024; T, K and groups * N within 31
+ *     bits; all tensors bf16. */
+typedef struct forge_grouped {
+  int64_t T, N, K;          /* tokens, out-features, in-features of one expert */
+  int32_t groups;
+  const int32_t* offsets;
+  const void* X;            /* [T x K]                                         */
+  const void* dY;           /* [T x N]                                         */
+  void* Y;                  /* [T x N]                                         */
+  void* dX;                 /* [T x K]                                         */
+} forge_grouped_t;
+
+/* Y_t = W_e X_t for every token t of every expert e (FP32 accumulation, one
+ * rounding to bf16).  Rows of Y that belong to no group become zero. */
+FORGE_API forge_status_t forge_grouped_linear(const forge_grouped_t* g, const void* W, void* stream);
+
+/* dX_t = W_e^T dY_t, as forge_grouped_linear. */
+FORGE_API forge_status_t forge_grouped_dgrad(const forge_grouped_t* g, const void* W, void* stream);
+
+/* forge_linear_bwd_step for every expert: dX (if g->dX is set) from the weights
+ * before the update, then dW_e = sum over e's tokens of dY_t X_t^T and the rule
+ * `opt_kind` on every W_e and its states, no gradient ever written.  `state`
+ * is that of one [groups * N x K] matrix (bf16 weights; FP32, BF16 or INT8
+ * states of any width): stochastic rounding draws the bits of index
+ * (e * N + n) * K + k, and an expert without tokens takes a step on a zero
+ * gradient.  FP32 weights return FORGE_ERR_UNSUPPORTED. */
+FORGE_API forge_status_t forge_grouped_bwd_step(const forge_grouped_t* g, const forge_state_t* state,
+                                                int32_t opt_kind, const forge_hparams_t* hp, int64_t step,
+                                                uint64_t seed, void* stream);
 
 /* Gradient dtypes of forge_multi_opt_step. */
 typedef enum forge_g_dtype { FORGE_G_FP32 = 0, FORGE_G_BF16 = 1 } forge_g_dtype_t;
@@ -375,7 +414,8 @@ FORGE_API forge_status_t forge_rmsnorm_bwd(const forge_rmsnorm_grad_t* grad, voi
 FORGE_API int64_t forge_rmsnorm_bwd_workspace(int64_t T, int64_t K);
 
 /* Synchronises `stream`, then returns and clears the current device's status
- * word: FORGE_OK, FORGE_ERR_TIMEOUT (a bounded wait expired in a kernel) or
+ * word: FORGE_OK, FORGE_ERR_TIMEOUT (a bounded wait expired in a kernel),
+ * FORGE_ERR_INVALID_ARG (group offsets out of order or range) or
  * FORGE_ERR_CUDA (the stream reported a CUDA error). */
 FORGE_API forge_status_t forge_get_device_status(void* stream);
 

@@ -53,6 +53,11 @@ class ForgeHparams(ctypes.Structure):
                                        "momentum")]
 
 
+class ForgeGrouped(ctypes.Structure):
+    _fields_ = [("T", c_int64), ("N", c_int64), ("K", c_int64), ("groups", c_int32), ("offsets", c_void_p),
+                ("X", c_void_p), ("dY", c_void_p), ("Y", c_void_p), ("dX", c_void_p)]
+
+
 class ForgeTensor(ctypes.Structure):
     _fields_ = [("n", c_int64), ("grad", c_void_p), ("W", c_void_p), ("s1", c_void_p), ("s2", c_void_p),
                 ("s1_scale", c_void_p), ("s2_scale", c_void_p)]
@@ -110,6 +115,10 @@ _SIGNATURES = {
                                              c_int32, c_void_p]),
     "forge_dequantize_state_block": (c_int32, [c_void_p, c_void_p, c_void_p, c_int64, c_int64, c_int32,
                                                c_int32, c_void_p]),
+    "forge_grouped_linear": (c_int32, [ctypes.POINTER(ForgeGrouped), c_void_p, c_void_p]),
+    "forge_grouped_dgrad": (c_int32, [ctypes.POINTER(ForgeGrouped), c_void_p, c_void_p]),
+    "forge_grouped_bwd_step": (c_int32, [ctypes.POINTER(ForgeGrouped), ctypes.POINTER(ForgeState), c_int32,
+                                         ctypes.POINTER(ForgeHparams), c_int64, c_uint64, c_void_p]),
     "forge_multi_opt_step": (c_int32, [ctypes.POINTER(ForgeTensor), c_int32, c_int32, c_int32, c_int32,
                                        c_int32, ctypes.POINTER(ForgeHparams), c_int64, c_uint64,
                                        c_void_p]),
@@ -392,6 +401,67 @@ def forge_dequantize_state(codes, absmax, x, is_signed: bool, stream=None, block
     _need(absmax, "absmax", torch.float32, (rows, cols // block))
     _check(lib().forge_dequantize_state_block(_ptr(codes), _ptr(absmax), _ptr(x), rows, cols,
                                               1 if is_signed else 0, int(block), _stream(stream)))
+
+
+def _experts(W, offsets):
+    """(groups, N, K) of W [groups, N, K] bf16, and the offsets' check."""
+    if W.dim() != 3:
+        raise ValueError(f"W: expected [groups, N, K], got {tuple(W.shape)}")
+    E, N, K = W.shape
+    _need(W, "W", torch.bfloat16, (E, N, K))
+    _need(offsets, "offsets", torch.int32, (E + 1,))
+    return E, N, K
+
+
+def forge_grouped_linear(X, W, offsets, Y, stream=None):
+    """Y[t] = W[e] X[t] for the rows offsets[e] .. offsets[e+1]-1 of X [T, K] of
+    every expert e: W [groups, N, K], Y [T, N], all bf16; offsets [groups + 1]
+    int32 on the device.  Rows of no group become zero."""
+    E, N, K = _experts(W, offsets)
+    T = X.shape[0]
+    _need(X, "X", torch.bfloat16, (T, K))
+    _need(Y, "Y", torch.bfloat16, (T, N))
+    g = ForgeGrouped(T, N, K, E, offsets.data_ptr(), X.data_ptr(), None, Y.data_ptr(), None)
+    _check(lib().forge_grouped_linear(ctypes.byref(g), W.data_ptr(), _stream(stream)))
+
+
+def forge_grouped_dgrad(dY, W, offsets, dX, stream=None):
+    """dX[t] = W[e]^T dY[t], as forge_grouped_linear."""
+    E, N, K = _experts(W, offsets)
+    T = dY.shape[0]
+    _need(dY, "dY", torch.bfloat16, (T, N))
+    _need(dX, "dX", torch.bfloat16, (T, K))
+    g = ForgeGrouped(T, N, K, E, offsets.data_ptr(), None, dY.data_ptr(), None, dX.data_ptr())
+    _check(lib().forge_grouped_dgrad(ctypes.byref(g), W.data_ptr(), _stream(stream)))
+
+
+def forge_grouped_bwd_step(X, dY, W, offsets, opt: str, hp: dict, step: int, seed: int, s1=None, s2=None,
+                           s1_scale=None, s2_scale=None, dX=None, stream=None):
+    """The FORGE step on every expert's weight W[e] (bf16, with the states of
+    forge_linear_bwd_step in the same [groups, N, K] layout; INT8 scales
+    [groups, N, K / B]): W and the states are updated in place, dX, if given,
+    comes from the weights before the update."""
+    E, N, K = _experts(W, offsets)
+    T = X.shape[0]
+    _need(X, "X", torch.bfloat16, (T, K))
+    _need(dY, "dY", torch.bfloat16, (T, N))
+    if dX is not None:
+        _need(dX, "dX", torch.bfloat16, (T, K))
+    rows = [t if t is None else _flat_rows(t, name, E, N) for t, name in
+            ((s1, "s1"), (s2, "s2"), (s1_scale, "s1_scale"), (s2_scale, "s2_scale"))]
+    st = make_state(W.view(E * N, K), *rows)
+    g = ForgeGrouped(T, N, K, E, offsets.data_ptr(), X.data_ptr(), dY.data_ptr(), None, _ptr(dX))
+    _check(lib().forge_grouped_bwd_step(ctypes.byref(g), ctypes.byref(st), OPT_KINDS[opt],
+                                        ctypes.byref(_hparams_of(hp)), int(step), int(seed) & 0xFFFFFFFFFFFFFFFF,
+                                        _stream(stream)))
+
+
+def _flat_rows(t, name, E, N):
+    if t.dim() != 3 or t.shape[0] != E or t.shape[1] != N:
+        raise ValueError(f"{name}: expected [groups, N, ..] = [{E}, {N}, ..], got {tuple(t.shape)}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return t.view(E * N, t.shape[2])
 
 
 class ForgeTensors:

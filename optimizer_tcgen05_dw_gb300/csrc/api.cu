@@ -959,6 +959,8 @@ forge_status_t forge_get_device_status(void* stream) {
     if ((e = cudaMemcpy(d.status, &zero, sizeof(zero), cudaMemcpyHostToDevice)) != cudaSuccess)
       return cuda_fail(e, "clear status word");
     if (word == kStatusTimeout) return fail(FORGE_ERR_TIMEOUT, "a pipeline wait in a kernel expired");
+    if (word == kStatusInvalid)
+      return fail(FORGE_ERR_INVALID_ARG, "group offsets decrease or leave [0, T] (they were clamped)");
     return fail(FORGE_ERR_DEVICE, "device status %u", word);
   }
   return FORGE_OK;

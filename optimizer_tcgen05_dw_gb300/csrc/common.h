@@ -28,7 +28,7 @@ constexpr int kNumKernelSdt = 6;
 constexpr int64_t kStageWeightsMaxT = 8192;
 
 // Device-side status codes (values match forge_status_t).
-enum DeviceStatus : uint32_t { kStatusOk = 0, kStatusTimeout = 4 };
+enum DeviceStatus : uint32_t { kStatusOk = 0, kStatusInvalid = 1, kStatusTimeout = 4 };
 
 // Per-step scalars of a rule, formed on the host in double from the float
 // hyper-parameters and the step number and rounded once to float.  Field use
@@ -92,7 +92,8 @@ enum GemmMode : int32_t {
   kModeWgradStore = 1, // dW tile -> fp32 store (unfused pass 1)
   kModeDgrad = 2,      // dX tile -> bf16 store
   kModeStep = 3,       // one launch: the dX tiles, then the dW tiles -> optimizer epilogue
-  kModeFusedFp8 = 4    // the FORGE step from E4M3 operands (token-contiguous, scaled)
+  kModeFusedFp8 = 4,   // the FORGE step from E4M3 operands (token-contiguous, scaled)
+  kModeGrouped = 5     // the FORGE step of many experts' weights over ragged token groups
 };
 
 // Column blocks (of kTileN) whose dX-completion counters the one-launch step
@@ -154,6 +155,32 @@ struct GemmParams {
   // INT8 states: elements per absmax block along a row (32, 64, 128 or 256;
   // the scale arrays are [M x Ncols / qblock]) and its base-2 logarithm.
   int32_t qblock, qshift;
+  // kModeGrouped: W and the states hold `groups` experts' [M x Ncols] in
+  // sequence; expert e's gradient sums over token rows offsets[e] ..
+  // offsets[e + 1] - 1 of the operands' `tokens` rows.
+  const int32_t* offsets;
+  int32_t groups, group_tiles, tokens;
+};
+
+
+// Products grouped by expert: rows offsets[e] .. offsets[e + 1] - 1 of the
+// token operands belong to group e.
+constexpr int kMaxGroups = 1024;
+
+// Parameters of a grouped product: out[t, f] = sum_r W_e(f, r) tok[t, r].
+struct GroupedParams {
+  const int32_t* offsets;    // [groups + 1]
+  int32_t groups;
+  int32_t T;                 // token rows
+  int32_t F;                 // output features (forward: N; dX: K)
+  int32_t w_rows;            // rows of one expert's weight (N)
+  int32_t num_kb;            // reduction blocks of 64
+  int32_t tiles_f;           // 256-feature tiles
+  int32_t w3d;               // dX: the weight map has single-copy column blocks
+  void* out;                 // bf16 [T x F]
+  uint64_t wait_limit_ns;
+  uint32_t* status;
+  int32_t skip_loads;
 };
 
 }  // namespace forge

@@ -69,6 +69,18 @@ cudaError_t launch_dgrad_fp32w(const void* dY, const float* W, void* dX, int64_t
                                int64_t K, int num_sms, cudaStream_t s);
 
 
+// tc_grouped.cu: the FORGE step of every expert (mode kModeGrouped, bf16
+// weights): a, b the operands with a stage's rows as a dimension (see
+// producer_role), s1, s2, w with the experts as a third.
+cudaError_t launch_tc_grouped(int sdt, const CUtensorMap& a, const CUtensorMap& b, const CUtensorMap& s1,
+                              const CUtensorMap& s2, const CUtensorMap& w, const GemmParams& p, int grid,
+                              cudaStream_t s);
+// grouped.cu: the grouped forward product (dgrad false) or dX (true).  w: the
+// weights' map; tok[i]: the token operand in boxes of 64 columns x (16 << i)
+// rows.
+cudaError_t launch_grouped(bool dgrad, const CUtensorMap& w, const CUtensorMap (&tok)[4],
+                           const GroupedParams& p, int grid, cudaStream_t s);
+
 // One tensor of a many-tensor optimizer step.
 struct MultiItem {
   const void* g;     // gradient (nullptr = zero)

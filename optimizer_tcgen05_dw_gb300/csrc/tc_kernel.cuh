@@ -97,7 +97,7 @@ struct KCfg {
   // the staged epilogue: every FORGE step with bf16 weights, and the fused
   // step with fp32 weights and fp32 states
   static constexpr bool kTmaEpi =
-      ((MODE == kModeFusedOpt || MODE == kModeStep || kFp8) && WDT == kWBf16) ||
+      ((MODE == kModeFusedOpt || MODE == kModeStep || MODE == kModeGrouped || kFp8) && WDT == kWBf16) ||
       (MODE == kModeFusedOpt && WDT == kWFp32 && SDT == kSFp32);
   static constexpr bool kStageW = kTmaEpi && stages_weights(SDT);
   static constexpr int kBK =
@@ -131,7 +131,8 @@ static_assert(KCfg<kModeFusedFp8, kWBf16, kSInt8WX>::kSmem <= 232448, "dynamic s
 
 // Bounded wait on an mbarrier phase.  Returns false if the CTA is aborting
 // or the wait expired (the first expiry records the timeout).
-__device__ __forceinline__ bool bounded_wait(uint64_t* bar, uint32_t parity, const GemmParams& p,
+template <typename P>  // GemmParams or GroupedParams
+__device__ __forceinline__ bool bounded_wait(uint64_t* bar, uint32_t parity, const P& p,
                                              SharedState* ss, bool honour_abort = true) {
   if (ptx::mbar_try_wait(bar, parity)) return true;
   const uint64_t t0 = ptx::global_timer_ns();
@@ -172,6 +173,26 @@ __device__ __forceinline__ void unit_coords(int u, const GemmParams& p, int& tm,
   half = split ? ((u - p.split_from) & 1) : -1;
   tile_coords(split ? p.split_from + ((u - p.split_from) >> 1) : u, p, tm, tn);
 }
+
+// Grouped step: units are whole tiles, expert by expert; unit u's expert and
+// its tile inside that expert's weight.
+__device__ __forceinline__ int group_tile(int u, const GemmParams& p, int& tm, int& tn) {
+  const int e = u / p.group_tiles;
+  tile_coords_of(u - e * p.group_tiles, p.tiles_m, p.tiles_n, tm, tn);
+  return e;
+}
+// Token rows [begin, begin + count) of expert e; offsets that decrease or
+// leave [0, tokens] are clamped (and reported, once a launch finds one).
+__device__ __forceinline__ void group_rows(int e, const GemmParams& p, int& begin, int& count) {
+  const int a = p.offsets[e], b = p.offsets[e + 1];
+  begin = min(max(a, 0), p.tokens);
+  const int end = min(max(b, begin), p.tokens);
+  count = end - begin;
+  if (a < 0 || b < a || b > p.tokens) atomicCAS(p.status, 0u, static_cast<uint32_t>(kStatusInvalid));
+}
+// Stages of an expert's reduction: at least one, which an expert without
+// tokens fills with zeros (its gradient).
+__device__ __forceinline__ int group_stages(int count, int bk) { return count > 0 ? (count + bk - 1) / bk : 1; }
 
 // ------------------------------------------------------------------ roles
 
@@ -231,6 +252,43 @@ __device__ void producer_role(const CUtensorMap* mA, const CUtensorMap* mB, cons
           last_parity = (last_parity & ~(1u << s)) | (ph << s);
         }
       }
+    }
+    if constexpr (MODE == kModeGrouped) {
+      // Ragged reductions: the operands' maps have the 64 rows of a stage as a
+      // dimension of their own ahead of the row it starts from.  A full stage
+      // is read from row 0 of that dimension; an expert's last stage of n < 64
+      // rows starts n - 64 rows before it, so those read as zeros (in both
+      // operands: nothing of the next expert's tokens can reach the sum, a NaN
+      // among them neither) and its n rows follow.
+      for (int u = pair_id(); u < p.num_units; u += num_pairs()) {
+        int tm, tn, begin, count;
+        group_rows(group_tile(u, p, tm, tn), p, begin, count);
+        const int m0 = tm * kPairM + static_cast<int>(rank) * kTileM;
+        const int n0 = tn * kTileN + static_cast<int>(rank) * (kTileN / 2);
+        const int stages = group_stages(count, BK);
+        for (int kb = 0; kb < stages; ++kb, ++it) {
+          const int s = static_cast<int>(it % STG);
+          const uint32_t ph = (it / STG) & 1u;
+          if (!bounded_wait(&ss->empty[s], ph ^ 1u, p, ss)) goto drain;
+          const uint32_t bar = full0 + static_cast<uint32_t>(s) * 8u;
+          if (rank == 0) ptx::mbar_arrive_expect_tx(&ss->full[s], 2u * (kA + kB));
+          const int r0 = min(count - kb * BK, BK) - BK, t0 = begin + kb * BK;
+          uint8_t* a = smA + s * kA;
+          uint8_t* b = smB + s * kB;
+          if (p.op3d) {
+            ptx::tma_load_4d_pair(mA, bar, a, 0, r0, m0 / 64, t0);
+            ptx::tma_load_4d_pair(mB, bar, b, 0, r0, n0 / 64, t0);
+          } else {
+            ptx::tma_load_3d_pair(mA, bar, a, m0, r0, t0);
+            ptx::tma_load_3d_pair(mA, bar, a + 64 * BK * 2, m0 + 64, r0, t0);
+            ptx::tma_load_3d_pair(mB, bar, b, n0, r0, t0);
+            ptx::tma_load_3d_pair(mB, bar, b + 64 * BK * 2, n0 + 64, r0, t0);
+          }
+          issued_mask |= 1u << s;
+          last_parity = (last_parity & ~(1u << s)) | (ph << s);
+        }
+      }
+      goto drain;
     }
     for (int u = pair_id(); u < p.num_units; u += num_pairs()) {
       int tm, tn, half;
@@ -342,8 +400,15 @@ __device__ void mma_role(const GemmParams& p, uint8_t* smA, uint8_t* smB, Shared
     for (int i = 0; i < ndx; ++i)
       if (!run_tile(p.dx_num_kb, true, kTileN)) goto done;
   }
-  for (int u = pair_id(); u < p.num_units; u += num_pairs())  // a half unit: N = 128
-    if (!run_tile(p.num_kb, MODE == kModeDgrad, u < p.split_from ? kTileN : kTileN / 2)) goto done;
+  for (int u = pair_id(); u < p.num_units; u += num_pairs()) {  // a half unit: N = 128
+    int num_kb = p.num_kb;
+    if (MODE == kModeGrouped) {
+      int begin, count;
+      group_rows(u / p.group_tiles, p, begin, count);
+      num_kb = group_stages(count, BK);
+    }
+    if (!run_tile(num_kb, MODE == kModeDgrad, u < p.split_from ? kTileN : kTileN / 2)) goto done;
+  }
 done:
   // Tensor memory may be released only after every issued MMA has finished.
   ptx::mma_commit_pair_multicast(&ss->mma_done, 0x1);
@@ -1023,7 +1088,7 @@ __device__ __forceinline__ void epi_chunk_int8(uint32_t taddr, uint8_t* buf, int
 // regions (`amax` and `amax_other`), [state][block b of the unit][row]: two
 // blocks of 128 in a whole unit, else one.
 template <int KIND, bool SCALE>
-__device__ __forceinline__ void int8_wide_absmax(uint32_t tunit, int64_t row, int col0, int nch, int r,
+__device__ __forceinline__ void int8_wide_absmax(uint32_t tunit, int64_t row, bool row_ok, int col0, int nch, int r,
                                                  int sub, int qs, float* amax, float* amax_other,
                                                  int nthreads, const GemmParams& p) {
   const int64_t K = p.Ncols;
@@ -1036,7 +1101,7 @@ __device__ __forceinline__ void int8_wide_absmax(uint32_t tunit, int64_t row, in
     ptx::tmem_ld_issue(tunit + static_cast<uint32_t>(c * 64 + sub * 16), gr);
     uint4 q1 = make_uint4(0, 0, 0, 0), q2 = make_uint4(0, 0, 0, 0), w0 = q1, w1 = q1;
     float a1 = 0.f, a2 = 0.f;
-    if (row < p.M && col < K) {
+    if (row_ok && col < K) {
       const int64_t e0 = row * K + col, sidx = row * (K >> qs) + (col >> qs);
       if (uses_s1(KIND)) {
         q1 = *reinterpret_cast<const uint4*>(static_cast<const int8_t*>(p.s1) + e0);
@@ -1160,14 +1225,17 @@ struct StagedGeom {
 // Units are whole tiles (kChunks chunks) or, for a pair's last unit only,
 // 128-column halves (kChunks / 2 chunks): chunk j belongs to unit j / kChunks,
 // and `total` counts the pair's chunks.
-template <int kChunks>
+// Grouped step: rows are those of the tile's expert, kept beside them.
+template <int kChunks, bool GROUPED>
 struct TileWalk {
   int cur_tile = 0, cur_row0 = 0, cur_col0 = 0, nxt_row0 = 0, nxt_col0 = 0;
+  int cur_e = 0, nxt_e = 0;
   int my_tiles = 0, total = 0;
   __device__ __forceinline__ void origin(int i, const GemmParams& p, uint32_t rank, int& row0,
-                                         int& col0) const {
-    int tm, tn, half;
-    unit_coords(pair_id() + i * num_pairs(), p, tm, tn, half);
+                                         int& col0, int& e) const {
+    int tm, tn, half = -1;
+    if (GROUPED) e = group_tile(pair_id() + i * num_pairs(), p, tm, tn);
+    else unit_coords(pair_id() + i * num_pairs(), p, tm, tn, half);
     row0 = tm * kPairM + static_cast<int>(rank) * kTileM;
     col0 = tn * kTileN + (half > 0 ? kTileN / 2 : 0);
   }
@@ -1175,20 +1243,25 @@ struct TileWalk {
     my_tiles = p.num_units > pair_id() ? (p.num_units - 1 - pair_id()) / num_pairs() + 1 : 0;
     total = my_tiles * kChunks;
     if (my_tiles > 0 && pair_id() + (my_tiles - 1) * num_pairs() >= p.split_from) total -= kChunks / 2;
-    if (my_tiles > 0) origin(0, p, rank, cur_row0, cur_col0);
-    if (my_tiles > 1) origin(1, p, rank, nxt_row0, nxt_col0);
+    if (my_tiles > 0) origin(0, p, rank, cur_row0, cur_col0, cur_e);
+    if (my_tiles > 1) origin(1, p, rank, nxt_row0, nxt_col0, nxt_e);
   }
   // Tile `local` (> 0) becomes the one in hand.
   __device__ __forceinline__ void advance(int local, const GemmParams& p, uint32_t rank) {
     cur_tile = local;
     cur_row0 = nxt_row0;
     cur_col0 = nxt_col0;
-    if (local + 1 < my_tiles) origin(local + 1, p, rank, nxt_row0, nxt_col0);
+    if (GROUPED) cur_e = nxt_e;
+    if (local + 1 < my_tiles) origin(local + 1, p, rank, nxt_row0, nxt_col0, nxt_e);
   }
   __device__ __forceinline__ void where(int j, int kCC, int& row0, int& col0) const {
     const bool next = (j / kChunks) != cur_tile;
     row0 = next ? nxt_row0 : cur_row0;
     col0 = (next ? nxt_col0 : cur_col0) + (j % kChunks) * kCC;
+  }
+  // Chunk j's expert (grouped step; else 0).
+  __device__ __forceinline__ int expert(int j) const {
+    return GROUPED ? ((j / kChunks) != cur_tile ? nxt_e : cur_e) : 0;
   }
 };
 
@@ -1283,8 +1356,8 @@ __device__ void epilogue_io_role(const CUtensorMap* mS1, const CUtensorMap* mS2,
                                  const CUtensorMap* mDX, const CUtensorMap* mW, const GemmParams& p,
                                  SharedState* ss, uint8_t* epi, int lane, uint32_t rank) {
   using G = StagedGeom<KIND, SDT>;
-  constexpr bool STEP = MODE == kModeStep;
-  TileWalk<G::kChunks> walk;
+  constexpr bool STEP = MODE == kModeStep, GROUPED = MODE == kModeGrouped;
+  TileWalk<G::kChunks, GROUPED> walk;
   walk.init(p, rank);
   const int total = walk.total;
   const bool io = (lane == 0);
@@ -1297,12 +1370,26 @@ __device__ void epilogue_io_role(const CUtensorMap* mS1, const CUtensorMap* mS2,
     uint8_t* buf = epi + (j & 1) * G::kBuf;
     uint64_t* bar = &ss->epi_full[j & 1];
     ptx::mbar_arrive_expect_tx(bar, G::kTxAll);
+    if constexpr (GROUPED) {  // the maps have the experts as a third dimension
+      const int e = walk.expert(j);
+      if (G::U1) ptx::tma_load_3d_hint(mS1, bar, buf + G::kOffS1, col0, row0, e, pol);
+      if (G::U2) ptx::tma_load_3d_hint(mS2, bar, buf + G::kOffS2, col0, row0, e, pol);
+      if (G::WST) ptx::tma_load_3d_hint(mW, bar, buf + G::kOffW, col0, row0, e, pol);
+      return;
+    }
     if (G::U1) ptx::tma_load_2d_hint(mS1, bar, buf + G::kOffS1, col0, row0, pol);
     if (G::U2) ptx::tma_load_2d_hint(mS2, bar, buf + G::kOffS2, col0, row0, pol);
     if (G::WST) ptx::tma_load_2d_hint(mW, bar, buf + G::kOffW, col0, row0, pol);
   };
-  auto store_at = [&](int j, int row0, int col0) {
+  auto store_at = [&](int j, int row0, int col0, int e) {
     const uint8_t* buf = epi + (j & 1) * G::kBuf;
+    if constexpr (GROUPED) {  // rows past the expert's last are out of the map's range, not the next expert's
+      if (G::U1) ptx::tma_store_3d_hint(mS1, buf + G::kOffS1, col0, row0, e, pol);
+      if (G::U2) ptx::tma_store_3d_hint(mS2, buf + G::kOffS2, col0, row0, e, pol);
+      if (G::WST) ptx::tma_store_3d_hint(mW, buf + G::kOffW, col0, row0, e, pol);
+      ptx::bulk_commit_group();
+      return;
+    }
     if (G::U1) ptx::tma_store_2d_hint(mS1, buf + G::kOffS1, col0, row0, pol);
     if (G::U2) ptx::tma_store_2d_hint(mS2, buf + G::kOffS2, col0, row0, pol);
     if (G::WST) ptx::tma_store_2d_hint(mW, buf + G::kOffW, col0, row0, pol);
@@ -1373,6 +1460,7 @@ __device__ void epilogue_io_role(const CUtensorMap* mS1, const CUtensorMap* mS2,
   for (int j = 0; j < total && !stop; ++j) {
     int srow, scol;
     walk.where(j, G::kCC, srow, scol);  // chunk j's origin, before the walk moves on
+    const int sexp = walk.expert(j);
     const bool more = j + 1 < total;
     if (io && more) {
       ptx::bulk_wait_group_read0();  // chunk j-1's stores have read buffer (j+1)&1
@@ -1381,10 +1469,10 @@ __device__ void epilogue_io_role(const CUtensorMap* mS1, const CUtensorMap* mS2,
     }
     if (more && (j + 1) % G::kChunks != 0) {
       stop = ptx::bar_red_or(kEpiBarrier, G::kNB, !ready(j + 1));
-      if (io) store_at(j, srow, scol);
+      if (io) store_at(j, srow, scol, sexp);
     } else {
       ptx::bar_sync(kEpiBarrier, G::kNB);  // chunk j is back in shared memory
-      if (io) store_at(j, srow, scol);
+      if (io) store_at(j, srow, scol, sexp);
       if (more) stop = ptx::bar_red_or(kEpiBarrier, G::kNB, !ready(j + 1));
     }
     if (!stop && more) consumed = j + 2;
@@ -1404,14 +1492,14 @@ template <int KIND, int WDT, int SDT, int MODE>
 __device__ void epilogue_compute_role(const GemmParams& p, SharedState* ss, uint8_t* epi,
                                       int warp, int lane, uint32_t rank) {
   using G = StagedGeom<KIND, SDT>;
-  constexpr bool STEP = MODE == kModeStep, SCALE = MODE == kModeFusedFp8;
+  constexpr bool STEP = MODE == kModeStep, SCALE = MODE == kModeFusedFp8, GROUPED = MODE == kModeGrouped;
   constexpr bool F32W = WDT == kWFp32;
   constexpr int kCC = G::kCC, kChunks = G::kChunks, kWPerThread = G::kWPerThread;
   constexpr int kWV = kWPerThread * (F32W ? 4 : 2) / 16;  // 16-byte words of weights per thread and chunk
   const int quarter = warp & 3, sub = (warp - 2) >> 2;  // TMEM lane quarter, column quarter
   const int r = quarter * 32 + lane;
   const int64_t K = p.Ncols;
-  TileWalk<kChunks> walk;
+  TileWalk<kChunks, GROUPED> walk;
   walk.init(p, rank);
   const int total = walk.total;
   const uint32_t empty0 = ptx::mapa(ptx::smem_addr(&ss->tmem_empty[0]), 0);
@@ -1430,9 +1518,9 @@ __device__ void epilogue_compute_role(const GemmParams& p, SharedState* ss, uint
   auto prefetch = [&](int j, uint4 (&v)[kWV], float& o1, float& o2) {
     int row0, col0;
     walk.where(j, kCC, row0, col0);
-    const int64_t row = static_cast<int64_t>(row0) + r;
+    const int64_t row = static_cast<int64_t>(row0) + r + static_cast<int64_t>(walk.expert(j)) * p.M;
     const int col = col0 + sub * kWPerThread;
-    const bool ok = row < p.M && col < K;
+    const bool ok = row0 + r < p.M && col < K;
     if (!G::WST) {
       const uint8_t* q = static_cast<const uint8_t*>(p.W) + (row * K + col) * (F32W ? 4 : 2);
 #pragma unroll
@@ -1444,7 +1532,7 @@ __device__ void epilogue_compute_role(const GemmParams& p, SharedState* ss, uint
     // chunk one quarter loads a row's old scales and hands them to the other
     // three, unless every thread loads its own (`own`)
     if (G::I8 && (j == 0 || sub == 0 || own)) {
-      const bool okb = row < p.M && col < K;
+      const bool okb = ok;
       const int64_t sidx = row * (K >> qs) + (col >> qs);
       if (G::U1) o1 = okb ? p.s1_scale[sidx] : 0.f;
       if (G::U2) o2 = okb ? p.s2_scale[sidx] : 0.f;
@@ -1487,7 +1575,8 @@ __device__ void epilogue_compute_role(const GemmParams& p, SharedState* ss, uint
     const int c = j % kChunks;
     int row0, col0;
     walk.where(j, kCC, row0, col0);
-    const int64_t row = static_cast<int64_t>(row0) + r;
+    const bool row_ok = row0 + r < p.M;
+    const int64_t row = static_cast<int64_t>(row0) + r + static_cast<int64_t>(walk.expert(j)) * p.M;  // of all experts'
     uint4 wcur[kWV];
     uint8_t* buf = epi + (j & 1) * G::kBuf;
     float o1 = o1next, o2 = o2next;
@@ -1524,7 +1613,7 @@ __device__ void epilogue_compute_role(const GemmParams& p, SharedState* ss, uint
         if (c == 0) {  // a new unit
           const uint32_t tunit = ss->tmem_base + (static_cast<uint32_t>(quarter * 32) << 16) +
                                  static_cast<uint32_t>(acc * kTileN);
-          int8_wide_absmax<KIND, SCALE>(tunit, row, col0, min(kChunks, total - j), r, sub, qs,
+          int8_wide_absmax<KIND, SCALE>(tunit, row, row_ok, col0, min(kChunks, total - j), r, sub, qs,
                                         reinterpret_cast<float*>(buf + G::kOffAmax),
                                         reinterpret_cast<float*>(epi + ((j + 1) & 1) * G::kBuf + G::kOffAmax),
                                         G::kNC, p);
@@ -1567,7 +1656,7 @@ __device__ void epilogue_compute_role(const GemmParams& p, SharedState* ss, uint
     // come after this fence, so that it has no global write in flight to
     // wait for: they are ordered by nothing in this CTA.
     ptx::fence_proxy_async_smem();
-    if (!G::WST && row < p.M && col < K) {
+    if (!G::WST && row_ok && col < K) {
       uint8_t* q = static_cast<uint8_t*>(p.W) + e0 * (F32W ? 4 : 2);
 #pragma unroll
       for (int h = 0; h < kWV; ++h) *reinterpret_cast<uint4*>(q + 16 * h) = wcur[h];
@@ -1575,7 +1664,7 @@ __device__ void epilogue_compute_role(const GemmParams& p, SharedState* ss, uint
     // INT8: the thread with the block's last 16 columns stores the block's
     // new absmax; a block wider than a chunk keeps its old one until its last
     // chunk has read it (the next chunks' old scales are loaded a chunk ahead)
-    if (G::I8 && (col & (qb - 1)) == qb - 16 && row < p.M && col < K) {
+    if (G::I8 && (col & (qb - 1)) == qb - 16 && row_ok && col < K) {
       const int64_t sidx = row * (K >> qs) + (col >> qs);
       if (G::U1) p.s1_scale[sidx] = n1;
       if (G::U2) p.s2_scale[sidx] = n2;
