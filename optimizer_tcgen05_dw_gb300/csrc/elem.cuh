@@ -1,6 +1,6 @@
 // Groups of eight consecutive elements of a weight, gradient or state tensor:
-// vector loads and stores, and the INT8 code of a block shared by the lanes
-// that hold it.  Used by the elementwise kernels (elementwise.cu, multi.cu).
+// vector loads and stores, the INT8 code of a block shared by the lanes that
+// hold it, and the stochastic rounding of eight weights.
 #pragma once
 
 #include <cstdint>
@@ -27,26 +27,48 @@ __device__ __forceinline__ float group_max(float a, int lanes) {
   return a;
 }
 
+// Codes are formed and read without the conversion unit (int <-> float casts
+// and rint run there at a quarter of the float rate): code_f32, and
+// code_round_fast with all eight redone from the exact quotient when one lies
+// near a half-integer or is not finite.  The values are dequant's and quant's.
 template <bool SIGNED>
-__device__ __forceinline__ void load_codes8(const void* base, int64_t e0, float a, float (&v)[8]) {
-  const uint2 c = *reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(base) + e0);
-  const uint32_t w[2] = {c.x, c.y};
+__device__ __forceinline__ void decode8(uint2 c, float a, float (&v)[8]) {
+  const float s = dev::dvd(a, SIGNED ? 127.f : 255.f);
+#pragma unroll
+  for (int j = 0; j < 8; ++j) v[j] = dev::mul(dev::code_f32<SIGNED>(j < 4 ? c.x : c.y, j & 3), s);
+}
+
+template <bool SIGNED>
+__device__ __forceinline__ uint2 encode8(const float (&v)[8], float a) {
+  if (a == 0.f) return make_uint2(0u, 0u);
+  const float st = dev::dvd(a, SIGNED ? 127.f : 255.f), inv = dev::dvd(1.f, st);
+  uint32_t k[8];  // the low byte of each is the code
+  bool any = !(fabsf(inv) <= 3.0e38f);
 #pragma unroll
   for (int j = 0; j < 8; ++j) {
-    const uint32_t b = (w[j >> 2] >> (8 * (j & 3))) & 0xFFu;
-    const int code = SIGNED ? static_cast<int>(static_cast<int8_t>(b)) : static_cast<int>(b);
-    v[j] = dev::dequant<SIGNED>(code, a);
+    bool redo;
+    k[j] = dev::code_round_fast<SIGNED>(dev::mul(v[j], inv), redo);
+    any |= redo;
   }
+  if (any) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      bool near;
+      k[j] = static_cast<uint32_t>(dev::code_round<SIGNED>(dev::dvd(v[j], st), near));
+    }
+  }
+  return make_uint2(__byte_perm(__byte_perm(k[0], k[1], 0x0040u), __byte_perm(k[2], k[3], 0x0040u), 0x5410u),
+                    __byte_perm(__byte_perm(k[4], k[5], 0x0040u), __byte_perm(k[6], k[7], 0x0040u), 0x5410u));
+}
+
+template <bool SIGNED>
+__device__ __forceinline__ void load_codes8(const void* base, int64_t e0, float a, float (&v)[8]) {
+  decode8<SIGNED>(*reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(base) + e0), a, v);
 }
 
 template <bool SIGNED>
 __device__ __forceinline__ void store_codes8(void* base, int64_t e0, float a, const float (&v)[8]) {
-  uint32_t w[2] = {0u, 0u};
-  const float st = dev::dvd(a, SIGNED ? 127.f : 255.f), inv = dev::dvd(1.f, st);
-#pragma unroll
-  for (int j = 0; j < 8; ++j)
-    w[j >> 2] |= (static_cast<uint32_t>(dev::quant_recip<SIGNED>(v[j], a, st, inv)) & 0xFFu) << (8 * (j & 3));
-  *reinterpret_cast<uint2*>(static_cast<uint8_t*>(base) + e0) = make_uint2(w[0], w[1]);
+  *reinterpret_cast<uint2*>(static_cast<uint8_t*>(base) + e0) = encode8<SIGNED>(v, a);
 }
 
 __device__ __forceinline__ void load_bf16x8(const void* base, int64_t e0, float (&v)[8]) {
@@ -64,6 +86,30 @@ __device__ __forceinline__ void store_bf16x8_rne(void* base, int64_t e0, const f
 #pragma unroll
   for (int j = 0; j < 4; ++j) o[j] = dev::bf16_rne(v[2 * j]) | (dev::bf16_rne(v[2 * j + 1]) << 16);
   *reinterpret_cast<uint4*>(static_cast<uint16_t*>(base) + e0) = make_uint4(o[0], o[1], o[2], o[3]);
+}
+
+// Eight weights to bf16 by stochastic rounding (dev::bf16_sr), packed in
+// pairs.  When all eight are finite (w * 0 is then 0; an infinite or NaN w
+// makes the sum NaN), each is its bit pattern plus its 16 random bits, upper
+// half kept: the two halves of a word come from one byte permutation.
+__device__ __forceinline__ uint4 pack_sr_bf16x8(const float* w, uint4 rnd) {
+  float probe = 0.f;
+#pragma unroll
+  for (int j = 0; j < 8; ++j) probe = __fmaf_rn(w[j], 0.f, probe);
+  const uint32_t rw[4] = {rnd.x, rnd.y, rnd.z, rnd.w};
+  uint32_t o[4];
+  if (probe == probe) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      o[j] = __byte_perm(__float_as_uint(w[2 * j]) + (rw[j] & 0xFFFFu),
+                         __float_as_uint(w[2 * j + 1]) + (rw[j] >> 16), 0x7632u);
+  } else {
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      o[j] = dev::bf16_sr(w[2 * j], dev::sr_bits(rnd, 2 * j)) |
+             (dev::bf16_sr(w[2 * j + 1], dev::sr_bits(rnd, 2 * j + 1)) << 16);
+  }
+  return make_uint4(o[0], o[1], o[2], o[3]);
 }
 
 }  // namespace forge

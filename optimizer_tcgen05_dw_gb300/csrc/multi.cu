@@ -56,40 +56,47 @@ __device__ __forceinline__ void load_b16(const void* base, int64_t e0, int cnt, 
     for (int j = 0; j < 8; ++j) v[j] = j < cnt ? dev::bf16_to_f32(p[j]) : 0.f;
   }
 }
-__device__ __forceinline__ void store_b16(void* base, int64_t e0, int cnt, const uint32_t (&b)[8]) {
+// Eight bf16 values packed in pairs.
+__device__ __forceinline__ void store_b16(void* base, int64_t e0, int cnt, uint4 v) {
   uint16_t* p = static_cast<uint16_t*>(base) + e0;
   if (cnt == 8) {
-    *reinterpret_cast<uint4*>(p) = make_uint4(b[0] | (b[1] << 16), b[2] | (b[3] << 16), b[4] | (b[5] << 16),
-                                              b[6] | (b[7] << 16));
+    *reinterpret_cast<uint4*>(p) = v;
   } else {
+    const uint32_t a[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
     for (int j = 0; j < 8; ++j)
-      if (j < cnt) p[j] = static_cast<uint16_t>(b[j]);
+      if (j < cnt) p[j] = static_cast<uint16_t>(a[j >> 1] >> (16 * (j & 1)));
   }
+}
+__device__ __forceinline__ uint4 rne_bf16x8(const float (&v)[8]) {
+  uint32_t o[4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) o[j] = dev::bf16_rne(v[2 * j]) | (dev::bf16_rne(v[2 * j + 1]) << 16);
+  return make_uint4(o[0], o[1], o[2], o[3]);
 }
 template <bool SIGNED>
 __device__ __forceinline__ void load_c8(const void* base, int64_t e0, int cnt, float a, float (&v)[8]) {
+  const uint8_t* p = static_cast<const uint8_t*>(base) + e0;
+  uint2 c = make_uint2(0u, 0u);
   if (cnt == 8) {
-    load_codes8<SIGNED>(base, e0, a, v);
+    c = *reinterpret_cast<const uint2*>(p);
   } else {
-    const uint8_t* p = static_cast<const uint8_t*>(base) + e0;
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const int b = j < cnt ? p[j] : 0;
-      v[j] = dev::dequant<SIGNED>(SIGNED ? static_cast<int>(static_cast<int8_t>(b)) : b, a);
-    }
+    for (int j = 0; j < 8; ++j)
+      if (j < cnt) (j < 4 ? c.x : c.y) |= static_cast<uint32_t>(p[j]) << (8 * (j & 3));
   }
+  decode8<SIGNED>(c, a, v);
 }
 template <bool SIGNED>
 __device__ __forceinline__ void store_c8(void* base, int64_t e0, int cnt, float a, const float (&v)[8]) {
+  uint8_t* p = static_cast<uint8_t*>(base) + e0;
+  const uint2 c = encode8<SIGNED>(v, a);
   if (cnt == 8) {
-    store_codes8<SIGNED>(base, e0, a, v);
+    *reinterpret_cast<uint2*>(p) = c;
   } else {
-    uint8_t* p = static_cast<uint8_t*>(base) + e0;
-    const float st = dev::dvd(a, SIGNED ? 127.f : 255.f), inv = dev::dvd(1.f, st);
 #pragma unroll
     for (int j = 0; j < 8; ++j)
-      if (j < cnt) p[j] = static_cast<uint8_t>(dev::quant_recip<SIGNED>(v[j], a, st, inv));
+      if (j < cnt) p[j] = static_cast<uint8_t>((j < 4 ? c.x : c.y) >> (8 * (j & 3)));
   }
 }
 
@@ -122,11 +129,7 @@ __device__ __forceinline__ void multi_group(const MultiItem& it, const OptScalar
 #pragma unroll
     for (int j = 0; j < 8; ++j) dev::rule<KIND>(w[j], g[j], s1[j], s2[j], sc);
     if (WDT == kWBf16) {
-      const uint4 r = dev::sr_words(static_cast<uint64_t>(e0) >> 3, seed + it.index, step);
-      uint32_t b[8];
-#pragma unroll
-      for (int j = 0; j < 8; ++j) b[j] = dev::bf16_sr(w[j], dev::sr_bits(r, j));
-      store_b16(it.W, e0, cnt, b);
+      store_b16(it.W, e0, cnt, pack_sr_bf16x8(w, dev::sr_words(static_cast<uint64_t>(e0) >> 3, seed + it.index, step)));
     } else {
       store_f32(it.W, e0, cnt, w);
     }
@@ -134,17 +137,8 @@ __device__ __forceinline__ void multi_group(const MultiItem& it, const OptScalar
       if (uses_s1(KIND)) store_f32(it.s1, e0, cnt, s1);
       if (uses_s2(KIND)) store_f32(it.s2, e0, cnt, s2);
     } else if (SDT == kSBf16) {
-      uint32_t b[8];
-      if (uses_s1(KIND)) {
-#pragma unroll
-        for (int j = 0; j < 8; ++j) b[j] = dev::bf16_rne(s1[j]);
-        store_b16(it.s1, e0, cnt, b);
-      }
-      if (uses_s2(KIND)) {
-#pragma unroll
-        for (int j = 0; j < 8; ++j) b[j] = dev::bf16_rne(s2[j]);
-        store_b16(it.s2, e0, cnt, b);
-      }
+      if (uses_s1(KIND)) store_b16(it.s1, e0, cnt, rne_bf16x8(s1));
+      if (uses_s2(KIND)) store_b16(it.s2, e0, cnt, rne_bf16x8(s2));
     }
   }
   if (SDT == kSInt8) {

@@ -11,14 +11,14 @@
 // bf16 (nearest even) and codes to E4M3 (nearest even, saturating) once.
 //
 // The floor of each is its traffic: x, residual, h, y 2 B an element each,
-// codes 1 B.  So a row is read once and held in registers between its
-// reduction and its output (the token-contiguous codes are the exception: a
-// block's 32 rows outlive the registers and are read back from L2).
+// codes 1 B.  So a row is read once and held in registers (or, for the token-contiguous
+// codes, shared memory between its reduction and its output.
 #include <cuda_bf16.h>
 #include <cuda_fp8.h>
 
 #include "launch.h"
 #include "optim.cuh"
+#include "ptx.cuh"
 
 namespace forge {
 
@@ -73,12 +73,6 @@ __device__ __forceinline__ float warp_max(float v) {
 // 1 / sqrt(sum / K + eps)
 __device__ __forceinline__ float inv_rms(float sum, int K, float eps) {
   return __frsqrt_rn(__fdiv_rn(sum, static_cast<float>(K)) + eps);
-}
-
-// Atomic maximum of non-negative floats (their bit patterns order as they do;
-// a NaN, above infinity, wins).  The order of the atomics changes nothing.
-__device__ __forceinline__ void atomic_max_pos(float* p, float v) {
-  atomicMax(reinterpret_cast<unsigned int*>(p), __float_as_uint(v));
 }
 
 // ---------------------------------------------------------------- forward
@@ -183,36 +177,53 @@ __global__ void __launch_bounds__(512) norm_fwd_kernel(const NormParams p) {
   }
 }
 
-// Token-contiguous codes [K x T]: a block takes 32 tokens.  First its warps
-// reduce the rows (writing h), then each thread takes two columns at a time
-// down the block's tokens and writes 32 consecutive codes of each: a whole
-// 32-byte sector, where one token's codes alone would be single bytes a row
-// apart.  The second reading comes from L2 (h was written there a moment ago).
+// Token-contiguous codes [K x T].  One token's codes are single bytes a row
+// apart, so a cluster of blocks takes 32 tokens at a time, each block a
+// segment of the columns, and keeps its h in shared memory between the two
+// passes: rows are read (and h written) along K, reduced in the block and then
+// across the cluster through distributed shared memory; then each thread
+// takes two columns down the 32 tokens and writes 32 consecutive codes of
+// each, a whole sector.  Nothing is read from global memory twice: 7 B an
+// element with a residual.
 constexpr int kTransTokens = 32;
+constexpr int kTransCols = 2048;  // of a segment, at most: 128 KiB of shared memory
+
+// A float of the same shared variable in block `rank` of the cluster.
+__device__ __forceinline__ float cluster_float(const float* p, uint32_t rank) {
+  float v;
+  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(ptx::mapa(ptx::smem_addr(p), rank)) : "memory");
+  return v;
+}
+
 template <bool RES>
-__global__ void __launch_bounds__(256) norm_fwd_t_kernel(const NormParams p) {
-  __shared__ float s_rstd[kTransTokens];
-  __shared__ float s_top[8];
+__global__ void __launch_bounds__(256) norm_fwd_t_kernel(const NormParams p, const int cluster, const int seg) {
+  extern __shared__ __align__(16) uint4 s_h[];  // [32][seg / 8]
+  __shared__ float s_sum[kTransTokens], s_top[kTransTokens], s_rstd[kTransTokens];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int V = p.K >> 3;
-  const int64_t t0 = static_cast<int64_t>(blockIdx.x) * kTransTokens;
+  const int V = p.K >> 3, SV = seg >> 3;
+  const int rank = static_cast<int>(ptx::cluster_ctarank());
+  const int v0 = rank * SV;
+  const int mine = min(SV, V - v0);  // vectors of this block's segment (at least one: host)
+  const int64_t t0 = static_cast<int64_t>(blockIdx.x / cluster) * kTransTokens;
   const int rows = static_cast<int>(p.T - t0 < kTransTokens ? p.T - t0 : kTransTokens);  // 16 or 32
-  float best = 0.f;
+  const uint4* w = static_cast<const uint4*>(p.w) + v0;
   for (int r = warp; r < rows; r += 8) {
-    const uint4* x = static_cast<const uint4*>(p.x) + (t0 + r) * V;
-    const uint4* res = static_cast<const uint4*>(p.res) + (t0 + r) * V;
-    uint4* ho = static_cast<uint4*>(p.h) + (t0 + r) * V;
+    const int64_t at = (t0 + r) * V + v0;
+    const uint4* x = static_cast<const uint4*>(p.x) + at;
+    const uint4* res = static_cast<const uint4*>(p.res) + at;
+    uint4* ho = static_cast<uint4*>(p.h) + at;
     float sum = 0.f, top = 0.f;
 #pragma unroll 4
-    for (int v = lane; v < V; v += 32) {
+    for (int v = lane; v < mine; v += 32) {
       uint4 h = x[v];
       if (RES) {
         h = add_bf16x8(h, res[v]);
         ho[v] = h;
       }
+      s_h[r * SV + v] = h;
       float f[8], g[8];
       unpack8(h, f);
-      unpack8(static_cast<const uint4*>(p.w)[v], g);
+      unpack8(w[v], g);
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
         sum = __fmaf_rn(f[j], f[j], sum);
@@ -221,41 +232,49 @@ __global__ void __launch_bounds__(256) norm_fwd_t_kernel(const NormParams p) {
     }
     sum = warp_sum(sum);
     top = warp_max(top);
-    const float rstd = inv_rms(sum, p.K, p.eps);
-    const float amax = top * rstd;
-    best = amax > best || amax != amax ? amax : best;  // a NaN stays
-    if (best != best) best = __int_as_float(0x7FC00000);
     if (lane == 0) {
-      s_rstd[r] = rstd;
-      if (p.rstd != nullptr) p.rstd[t0 + r] = rstd;
+      s_sum[r] = sum;
+      s_top[r] = top;
     }
   }
-  if (lane == 0) s_top[warp] = best;
-  __syncthreads();  // also orders this block's h for its own reads below
-  if (tid == 0 && p.amax != nullptr) {
-    unsigned int m = 0u;
-    for (int i = 0; i < 8; ++i) m = max(m, __float_as_uint(s_top[i]));
-    atomic_max_pos(p.amax, __uint_as_float(m));
+  ptx::cluster_sync();  // every block's shares are there
+  if (tid < rows) {     // each block adds them in the same order
+    float sum = 0.f, top = 0.f;
+    for (int c = 0; c < cluster; ++c) {
+      sum += cluster_float(&s_sum[tid], c);
+      top = fmaxf(top, cluster_float(&s_top[tid], c));
+    }
+    const float rstd = inv_rms(sum, p.K, p.eps);
+    s_rstd[tid] = rstd;
+    if (rank == 0) {
+      if (p.rstd != nullptr) p.rstd[t0 + tid] = rstd;
+      if (p.amax != nullptr) {
+        const float amax = top * rstd;
+        const uint32_t bits = amax == amax ? __float_as_uint(amax) : 0x7FC00000u;  // a NaN wins
+        const uint32_t most = __reduce_max_sync(rows == 32 ? 0xFFFFFFFFu : 0xFFFFu, bits);
+        if (tid == 0) atomicMax(reinterpret_cast<unsigned int*>(p.amax), most);
+      }
+    }
   }
-  const uint32_t* src = static_cast<const uint32_t*>(RES ? p.h : p.x) + t0 * (p.K >> 1);
-  uint8_t* out = static_cast<uint8_t*>(p.qt) + t0;
-  for (int c = tid; c < (p.K >> 1); c += 256) {
-    const uint32_t wp = static_cast<const uint32_t*>(p.w)[c];
-    const float w0 = dev::bf16_to_f32(wp & 0xFFFFu), w1 = __uint_as_float(wp & 0xFFFF0000u);
-    const uint32_t* col = src + c;
+  __syncthreads();
+  asm volatile("barrier.cluster.arrive.release;" ::: "memory");  // done with the others' shares
+  const uint32_t* src = reinterpret_cast<const uint32_t*>(s_h);
+  const uint32_t* w2 = reinterpret_cast<const uint32_t*>(w);
+  uint8_t* out = static_cast<uint8_t*>(p.qt) + static_cast<int64_t>(v0) * 8 * p.T + t0;
+  for (int c = tid; c < mine * 4; c += 256) {
+    const float w0 = dev::bf16_to_f32(w2[c] & 0xFFFFu), w1 = __uint_as_float(w2[c] & 0xFFFF0000u);
 #pragma unroll
     for (int half = 0; half < 2; ++half) {
       if (half * 16 >= rows) break;
-      uint32_t h[16], o0[4], o1[4];
-#pragma unroll
-      for (int j = 0; j < 16; ++j) h[j] = col[static_cast<int64_t>(half * 16 + j) * (p.K >> 1)];
+      uint32_t o0[4], o1[4];
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
         float a[4], b[4];
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-          const uint32_t u = h[4 * q + j];
-          const float r = s_rstd[half * 16 + 4 * q + j];
+          const int t = half * 16 + 4 * q + j;
+          const uint32_t u = src[t * (seg >> 1) + c];
+          const float r = s_rstd[t];
           a[j] = dev::bf16_to_f32(u & 0xFFFFu) * r * w0 * p.inv_scale;
           b[j] = __uint_as_float(u & 0xFFFF0000u) * r * w1 * p.inv_scale;
         }
@@ -267,6 +286,7 @@ __global__ void __launch_bounds__(256) norm_fwd_t_kernel(const NormParams p) {
       *reinterpret_cast<uint4*>(to + p.T) = make_uint4(o1[0], o1[1], o1[2], o1[3]);
     }
   }
+  asm volatile("barrier.cluster.wait.acquire;" ::: "memory");  // nobody reads this block's shares any more
 }
 
 // ---------------------------------------------------------------- gradient
@@ -275,8 +295,8 @@ __global__ void __launch_bounds__(256) norm_fwd_t_kernel(const NormParams p) {
 // block's rows in registers and writes it to the block's row of `partial`.
 // The next row is loaded before the present one is reduced (PRE), so that the
 // barrier does not leave memory idle.
-template <int NV, bool DH, bool PRE>
-__global__ void __launch_bounds__(512) norm_bwd_kernel(const NormParams p) {
+template <int NV, bool DH, bool PRE, int MAXT, int MINB>
+__global__ void __launch_bounds__(MAXT, MINB) norm_bwd_kernel(const NormParams p) {
   __shared__ float red[2][16];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, warps = blockDim.x >> 5;
   const int V = p.K >> 3;
@@ -392,10 +412,35 @@ void run_fwd(const NormParams& p, int grid, int threads, cudaStream_t s) {
   else norm_fwd_kernel<NV, false><<<grid, threads, 0, s>>>(p);
 }
 
-template <int NV, bool PRE>
+template <bool RES>
+cudaError_t run_fwd_t(const NormParams& p, cudaStream_t s) {
+  const int V = p.K / 8;
+  int cluster = 1;  // segments of at most 1024 columns (64 KiB: three blocks an SM) up to K = 8192
+  while (cluster < 8 && V > 128 * cluster) cluster *= 2;
+  const int seg = (V + cluster - 1) / cluster * 8;
+  const int smem = kTransTokens * seg * 2;
+  auto* k = norm_fwd_t_kernel<RES>;
+  cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, kTransTokens * kTransCols * 2);
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>((p.T + kTransTokens - 1) / kTransTokens * cluster), 1, 1);
+  cfg.blockDim = dim3(256, 1, 1);
+  cfg.dynamicSmemBytes = static_cast<size_t>(smem);
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = static_cast<unsigned>(cluster);
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, k, p, cluster, seg);
+}
+
+template <int NV, bool PRE, int MAXT, int MINB>
 void run_bwd(const NormParams& p, int grid, int threads, cudaStream_t s) {
-  if (p.dh != nullptr) norm_bwd_kernel<NV, true, PRE><<<grid, threads, 0, s>>>(p);
-  else norm_bwd_kernel<NV, false, PRE><<<grid, threads, 0, s>>>(p);
+  if (p.dh != nullptr) norm_bwd_kernel<NV, true, PRE, MAXT, MINB><<<grid, threads, 0, s>>>(p);
+  else norm_bwd_kernel<NV, false, PRE, MAXT, MINB><<<grid, threads, 0, s>>>(p);
 }
 
 int64_t least(int64_t a, int64_t b) { return a < b ? a : b; }
@@ -408,9 +453,9 @@ cudaError_t launch_norm_fwd(const NormParams& p0, int num_sms, cudaStream_t s) {
   cudaError_t e;
   if (p.qt == nullptr || p.y != nullptr || p.q != nullptr) {
     // Few rows: as many threads a row as it has vectors, up to 512, for the
-    // shortest time to one row.  Else up to four vectors a thread, so that a
-    // block's reduction is spread over more loads.
-    int nv = p.T < num_sms ? 1 : (V >= 512 ? 4 : (V >= 128 ? 2 : 1));
+    // shortest time to one row.  Else two vectors a thread (four past
+    // K = 8192), so that a block's reduction is spread over more loads.
+    int nv = p.T < num_sms ? 1 : (V >= 128 ? 2 : 1);
     while ((V + nv - 1) / nv > 512) nv *= 2;
     const int threads = round32((V + nv - 1) / nv);
     const int per_sm = static_cast<int>(least(32, 2048 / threads));
@@ -425,10 +470,7 @@ cudaError_t launch_norm_fwd(const NormParams& p0, int num_sms, cudaStream_t s) {
   }
   if (p.qt != nullptr) {
     if (p.amax != nullptr && (e = cudaMemsetAsync(p.amax, 0, sizeof(float), s)) != cudaSuccess) return e;
-    const int grid = static_cast<int>((p.T + kTransTokens - 1) / kTransTokens);
-    if (p.res != nullptr) norm_fwd_t_kernel<true><<<grid, 256, 0, s>>>(p);
-    else norm_fwd_t_kernel<false><<<grid, 256, 0, s>>>(p);
-    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    if ((e = p.res != nullptr ? run_fwd_t<true>(p, s) : run_fwd_t<false>(p, s)) != cudaSuccess) return e;
   }
   return cudaSuccess;
 }
@@ -443,9 +485,10 @@ cudaError_t launch_norm_bwd(const NormParams& p, int num_sms, cudaStream_t s) {
   const int threads = round32((V + nv - 1) / nv);
   const int grid = static_cast<int>(norm_bwd_blocks(p.T, p.K, num_sms));
   if (grid > 0) {
-    if (nv == 1) run_bwd<1, true>(p, grid, threads, s);
-    else if (nv == 2) run_bwd<2, true>(p, grid, threads, s);
-    else run_bwd<4, false>(p, grid, threads, s);
+    if (nv == 1) run_bwd<1, true, 256, 4>(p, grid, threads, s);
+    else if (nv == 2 && threads <= 320) run_bwd<2, true, 320, 2>(p, grid, threads, s);
+    else if (nv == 2) run_bwd<2, true, 512, 1>(p, grid, threads, s);
+    else run_bwd<4, false, 512, 1>(p, grid, threads, s);
     const cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return e;
   }

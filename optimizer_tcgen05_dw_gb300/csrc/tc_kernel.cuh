@@ -57,6 +57,7 @@
 #include <type_traits>
 
 #include "common.h"
+#include "elem.cuh"
 #include "optim.cuh"
 #include "ptx.cuh"
 
@@ -799,30 +800,6 @@ __device__ __forceinline__ void unpack_bf16x8(uint4 v, float* w) {
     w[2 * j] = dev::bf16_to_f32(a[j] & 0xFFFFu);
     w[2 * j + 1] = dev::bf16_to_f32(a[j] >> 16);
   }
-}
-
-// Eight weights to bf16 by stochastic rounding (dev::bf16_sr), packed in
-// pairs.  When all eight are finite (w * 0 is then 0; an infinite or NaN w
-// makes the sum NaN), each is its bit pattern plus its 16 random bits, upper
-// half kept: the two halves of a word come from one byte permutation.
-__device__ __forceinline__ uint4 pack_sr_bf16x8(const float* w, uint4 rnd) {
-  float probe = 0.f;
-#pragma unroll
-  for (int j = 0; j < 8; ++j) probe = __fmaf_rn(w[j], 0.f, probe);
-  const uint32_t rw[4] = {rnd.x, rnd.y, rnd.z, rnd.w};
-  uint32_t o[4];
-  if (probe == probe) {
-#pragma unroll
-    for (int j = 0; j < 4; ++j)
-      o[j] = __byte_perm(__float_as_uint(w[2 * j]) + (rw[j] & 0xFFFFu),
-                         __float_as_uint(w[2 * j + 1]) + (rw[j] >> 16), 0x7632u);
-  } else {
-#pragma unroll
-    for (int j = 0; j < 4; ++j)
-      o[j] = dev::bf16_sr(w[2 * j], dev::sr_bits(rnd, 2 * j)) |
-             (dev::bf16_sr(w[2 * j + 1], dev::sr_bits(rnd, 2 * j + 1)) << 16);
-  }
-  return make_uint4(o[0], o[1], o[2], o[3]);
 }
 
 // FP8 operands: the accumulated sum of E4M3 code products times the product
