@@ -3,6 +3,8 @@
 // hold it, and the stochastic rounding of eight weights.
 #pragma once
 
+#include <cuda_bf16.h>
+
 #include <cstdint>
 
 #include "optim.cuh"
@@ -81,11 +83,29 @@ __device__ __forceinline__ void load_bf16x8(const void* base, int64_t e0, float 
   }
 }
 
-__device__ __forceinline__ void store_bf16x8_rne(void* base, int64_t e0, const float (&v)[8]) {
-  uint32_t o[4];
+// Eight values to bf16 (dev::bf16_rne), packed in pairs: by the conversion
+// instruction, which rounds the same way and differs only in the NaN it gives,
+// so when none of the eight is a NaN.
+__device__ __forceinline__ uint4 pack_rne_bf16x8(const float (&v)[8]) {
+  bool nan = false;
 #pragma unroll
-  for (int j = 0; j < 4; ++j) o[j] = dev::bf16_rne(v[2 * j]) | (dev::bf16_rne(v[2 * j + 1]) << 16);
-  *reinterpret_cast<uint4*>(static_cast<uint16_t*>(base) + e0) = make_uint4(o[0], o[1], o[2], o[3]);
+  for (int j = 0; j < 8; ++j) nan |= v[j] != v[j];
+  uint32_t o[4];
+  if (!nan) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const __nv_bfloat162 h = __floats2bfloat162_rn(v[2 * j], v[2 * j + 1]);
+      o[j] = *reinterpret_cast<const uint32_t*>(&h);
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) o[j] = dev::bf16_rne(v[2 * j]) | (dev::bf16_rne(v[2 * j + 1]) << 16);
+  }
+  return make_uint4(o[0], o[1], o[2], o[3]);
+}
+
+__device__ __forceinline__ void store_bf16x8_rne(void* base, int64_t e0, const float (&v)[8]) {
+  *reinterpret_cast<uint4*>(static_cast<uint16_t*>(base) + e0) = pack_rne_bf16x8(v);
 }
 
 // Eight weights to bf16 by stochastic rounding (dev::bf16_sr), packed in

@@ -253,6 +253,7 @@ __global__ void __launch_bounds__(kGThreads, 1)
   GroupTable& g = *reinterpret_cast<GroupTable*>(reinterpret_cast<uint8_t*>(ss) + 512);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = ptx::cluster_ctarank();
+  ptx::grid_dep_launch();  // the step that may follow starts as this grid's CTAs end
   if (threadIdx.x == 0) {
     for (int s = 0; s < kGStages; ++s) {
       ptx::mbar_init(&ss->full[s], 1);

@@ -71,10 +71,12 @@ cudaError_t launch_dgrad_fp32w(const void* dY, const float* W, void* dX, int64_t
 
 // tc_grouped.cu: the FORGE step of every expert (mode kModeGrouped, bf16
 // weights): a, b the operands with a stage's rows as a dimension (see
-// producer_role), s1, s2, w with the experts as a third.
+// producer_role), s1, s2, w with the experts as a third.  With `after_dx` the
+// launch may start while the grouped dX kernel before it on the stream still
+// runs; it writes nothing before that grid has ended.
 cudaError_t launch_tc_grouped(int sdt, const CUtensorMap& a, const CUtensorMap& b, const CUtensorMap& s1,
                               const CUtensorMap& s2, const CUtensorMap& w, const GemmParams& p, int grid,
-                              cudaStream_t s);
+                              cudaStream_t s, bool after_dx);
 // grouped.cu: the grouped forward product (dgrad false) or dX (true).  w: the
 // weights' map; tok[i]: the token operand in boxes of 64 columns x (16 << i)
 // rows.

@@ -68,12 +68,6 @@ __device__ __forceinline__ void store_b16(void* base, int64_t e0, int cnt, uint4
       if (j < cnt) p[j] = static_cast<uint16_t>(a[j >> 1] >> (16 * (j & 1)));
   }
 }
-__device__ __forceinline__ uint4 rne_bf16x8(const float (&v)[8]) {
-  uint32_t o[4];
-#pragma unroll
-  for (int j = 0; j < 4; ++j) o[j] = dev::bf16_rne(v[2 * j]) | (dev::bf16_rne(v[2 * j + 1]) << 16);
-  return make_uint4(o[0], o[1], o[2], o[3]);
-}
 template <bool SIGNED>
 __device__ __forceinline__ void load_c8(const void* base, int64_t e0, int cnt, float a, float (&v)[8]) {
   const uint8_t* p = static_cast<const uint8_t*>(base) + e0;
@@ -137,8 +131,8 @@ __device__ __forceinline__ void multi_group(const MultiItem& it, const OptScalar
       if (uses_s1(KIND)) store_f32(it.s1, e0, cnt, s1);
       if (uses_s2(KIND)) store_f32(it.s2, e0, cnt, s2);
     } else if (SDT == kSBf16) {
-      if (uses_s1(KIND)) store_b16(it.s1, e0, cnt, rne_bf16x8(s1));
-      if (uses_s2(KIND)) store_b16(it.s2, e0, cnt, rne_bf16x8(s2));
+      if (uses_s1(KIND)) store_b16(it.s1, e0, cnt, pack_rne_bf16x8(s1));
+      if (uses_s2(KIND)) store_b16(it.s2, e0, cnt, pack_rne_bf16x8(s2));
     }
   }
   if (SDT == kSInt8) {

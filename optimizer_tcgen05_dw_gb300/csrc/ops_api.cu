@@ -238,9 +238,12 @@ forge_status_t forge_grouped_bwd_step(const forge_grouped_t* g, const forge_stat
   const CUtensorMapSwizzle sw = esize == 4 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B;
   if (uses_s1(opt_kind) && (st = expert_map(&m1, state->s1, sd, esize, g, cols, sw)) != FORGE_OK) return st;
   if (uses_s2(opt_kind) && (st = expert_map(&m2, state->s2, sd, esize, g, cols, sw)) != FORGE_OK) return st;
-  if (qb != 0 && (st = expert_map(&mw, state->W, kBf16, 2, g, 64, CU_TENSOR_MAP_SWIZZLE_128B)) != FORGE_OK) return st;
+  // weights in the columns of a chunk: 64 (INT8) or 32
+  if ((st = expert_map(&mw, state->W, kBf16, 2, g, cols, qb != 0 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B)) != FORGE_OK)
+    return st;
   const int pairs = p.num_units < d.num_sms / 2 ? p.num_units : d.num_sms / 2;
-  if ((e = launch_tc_grouped(sdt, ma, mb, m1, m2, mw, p, 2 * pairs, s)) != cudaSuccess)
+  // after dX's kernel (N > 0, T > 0: it was launched) the step may start at once
+  if ((e = launch_tc_grouped(sdt, ma, mb, m1, m2, mw, p, 2 * pairs, s, g->dX != nullptr)) != cudaSuccess)
     return cuda_fail(e, "grouped step launch");
   return FORGE_OK;
 }

@@ -25,6 +25,9 @@ __device__ __forceinline__ uint64_t global_timer_ns() {
 // when the launch had no such dependency).
 __device__ __forceinline__ void grid_dep_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
+// Let a dependent launch begin (it still waits for this grid where it says so).
+__device__ __forceinline__ void grid_dep_launch() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+
 // ---------------------------------------------------------------- mbarrier
 
 __device__ __forceinline__ void mbar_init(uint64_t* bar, uint32_t count) {
@@ -98,9 +101,13 @@ __device__ __forceinline__ uint32_t mapa(uint32_t a, uint32_t rank) {
 }
 
 // Arrive on an mbarrier given by its shared::cluster address (any CTA of
-// the cluster).
+// the cluster).  Release at CTA scope: what these arrivals hand over is tensor
+// memory whose loads have completed (tcgen05.wait::ld and the fence before),
+// not data in shared or global memory.  At cluster scope the arrival waits for
+// all of the thread's earlier accesses to be performed, about 8000 cycles
+// under the epilogue's traffic, once a tile and warp.
 __device__ __forceinline__ void mbar_arrive_cluster(uint32_t cluster_addr) {
-  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr)
+  asm volatile("mbarrier.arrive.release.cta.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr)
                : "memory");
 }
 

@@ -69,7 +69,8 @@ struct SharedState {
   uint64_t tmem_full[2];
   uint64_t tmem_empty[2];
   uint64_t mma_done;
-  uint64_t epi_full[2];     // staged epilogue chunk landed (TMA epilogue only)
+  uint64_t epi_full[4];     // staged epilogue chunk landed (TMA epilogue only)
+  uint64_t epi_done[4];     // ... and finished by every compute warp (streamed epilogue)
   uint32_t tmem_base;
   int32_t abort;
 };
@@ -88,6 +89,16 @@ constexpr int kEpiBufBytes = 32768;
 constexpr int kEpiBufBytesW = 37888;
 __host__ __device__ constexpr bool stages_weights(int sdt) { return sdt == kSInt8W || sdt == kSInt8WX; }
 __host__ __device__ constexpr bool compact_int8(int sdt) { return sdt == kSInt8W; }
+// The grouped step with fp32 or bf16 states takes the streamed epilogue
+// (grouped_io_role, grouped_compute_role), which stages the weights too, in
+// more and larger chunk buffers, and has fewer operand stages: an expert's
+// reduction is short, so the epilogue is what takes the time.
+__host__ __device__ constexpr bool streamed(int mode, int sdt) {
+  return mode == kModeGrouped && (sdt == kSFp32 || sdt == kSBf16);
+}
+__host__ __device__ constexpr int epi_bufs(int mode, int sdt) {
+  return !streamed(mode, sdt) ? 2 : (sdt == kSFp32 ? 3 : 4);
+}
 constexpr int kEpiBarrier = 1;       // named barrier of the epilogue warps
 constexpr int kEpiInnerBarrier = 2;  // the staged epilogue's compute warps only
 constexpr int kPairM = 2 * kTileM;  // rows of a pair tile
@@ -105,13 +116,15 @@ struct KCfg {
       kFp8 ? kFp8BlockK
            : (kTmaEpi ? kFusedBlockK : (MODE == kModeWgradStore ? kWgradBlockK : kBlockK));  // tokens per stage
   static constexpr int kStg =
-      kTmaEpi ? (kStageW && !compact_int8(SDT) ? kFusedStages - 1 : kFusedStages)
+      kTmaEpi ? (streamed(MODE, SDT) ? (SDT == kSFp32 ? kFusedStages - 2 : kFusedStages - 1)
+                  : kStageW && !compact_int8(SDT) ? kFusedStages - 1 : kFusedStages)
               : (MODE == kModeWgradStore ? kWgradStages : kStages);
   static constexpr int kEsz = kFp8 ? 1 : 2;           // operand element bytes
   static constexpr int kA = kTileM * kBK * kEsz;       // bytes of A per stage (this CTA's 128 rows)
   static constexpr int kB = (kTileN / 2) * kBK * kEsz; // bytes of B per stage (this CTA's 128 columns)
-  static constexpr int kEpiBuf = kStageW && !compact_int8(SDT) ? kEpiBufBytesW : kEpiBufBytes;
-  static constexpr int kEpiBytes = kTmaEpi ? 2 * kEpiBuf : 0;
+  static constexpr int kEpiBuf = streamed(MODE, SDT) ? (SDT == kSFp32 ? 40960 : 24576)
+                                 : kStageW && !compact_int8(SDT) ? kEpiBufBytesW : kEpiBufBytes;
+  static constexpr int kEpiBytes = kTmaEpi ? epi_bufs(MODE, SDT) * kEpiBuf : 0;
   static constexpr int kSmem = kStg * (kA + kB) + kEpiBytes + 512 + 1024;
   // TMA warp, MMA warp, epilogue warps (four per 32-lane quarter of TMEM in the
   // staged epilogue, two in the plain ones).
@@ -289,8 +302,7 @@ __device__ void producer_role(const CUtensorMap* mA, const CUtensorMap* mB, cons
           last_parity = (last_parity & ~(1u << s)) | (ph << s);
         }
       }
-      goto drain;
-    }
+    } else {
     for (int u = pair_id(); u < p.num_units; u += num_pairs()) {
       int tm, tn, half;
       unit_coords(u, p, tm, tn, half);
@@ -332,6 +344,7 @@ __device__ void producer_role(const CUtensorMap* mA, const CUtensorMap* mB, cons
         issued_mask |= 1u << s;
         last_parity = (last_parity & ~(1u << s)) | (ph << s);
       }
+    }
     }
   }
 drain:
@@ -928,16 +941,8 @@ __device__ __forceinline__ void epi_chunk_bf16s(uint32_t taddr, uint8_t* buf, in
 #pragma unroll
   for (int j = 0; j < 8; ++j) dev::rule<KIND>(w[j], g[j], s1[j], s2[j], p.sc);
   wv = pack_sr_bf16x8(w, rnd);
-  uint32_t o1[4], o2[4];
-#pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    o1[j] = dev::bf16_rne(s1[2 * j]) | (dev::bf16_rne(s1[2 * j + 1]) << 16);
-    o2[j] = dev::bf16_rne(s2[2 * j]) | (dev::bf16_rne(s2[2 * j + 1]) << 16);
-  }
-  if (uses_s1(KIND))
-    *reinterpret_cast<uint4*>(buf + kOffS1 + sw64(r, sub)) = make_uint4(o1[0], o1[1], o1[2], o1[3]);
-  if (uses_s2(KIND))
-    *reinterpret_cast<uint4*>(buf + kOffS2 + sw64(r, sub)) = make_uint4(o2[0], o2[1], o2[2], o2[3]);
+  if (uses_s1(KIND)) *reinterpret_cast<uint4*>(buf + kOffS1 + sw64(r, sub)) = pack_rne_bf16x8(s1);
+  if (uses_s2(KIND)) *reinterpret_cast<uint4*>(buf + kOffS2 + sw64(r, sub)) = pack_rne_bf16x8(s2);
 }
 
 // INT8 states: a chunk is 128 rows x 64 columns (codes 8 KiB per state in
@@ -1429,7 +1434,7 @@ __device__ void epilogue_io_role(const CUtensorMap* mS1, const CUtensorMap* mS2,
     if (io) {
       issue(0);
       issued = 1;
-      if (MODE == kModeFusedOpt) ptx::grid_dep_wait();  // before the first store
+      if (MODE == kModeFusedOpt || GROUPED) ptx::grid_dep_wait();  // before the first store
     }
     stop = ptx::bar_red_or(kEpiBarrier, G::kNB, !ready(0));
     if (!stop) consumed = 1;
@@ -1544,7 +1549,7 @@ __device__ void epilogue_compute_role(const GemmParams& p, SharedState* ss, uint
   bool stop = total == 0;
   if (!stop) {
     prefetch(0, wnext, o1next, o2next);
-    if (MODE == kModeFusedOpt) ptx::grid_dep_wait();  // before the first write
+    if (MODE == kModeFusedOpt || GROUPED) ptx::grid_dep_wait();  // before the first write
     begin(0);
     stop = ptx::bar_red_or(kEpiBarrier, G::kNB, false);  // the I/O warp's verdict
   }
@@ -1660,12 +1665,134 @@ __device__ void epilogue_compute_role(const GemmParams& p, SharedState* ss, uint
   }
 }
 
+// ------------------------------------------------------------------ streamed epilogue
+
+// The grouped step's epilogue for fp32 and bf16 states.  A tile's update moves
+// 1.3 MB (fp32 moments) while its MMAs over an expert's few hundred tokens take
+// a fraction of that time, so the states' stream is what has to keep going.
+// Against the staged epilogue above: the weights are staged by TMA as well (a
+// thread's 16 bytes of a row, loaded directly, are a sector of a line of their
+// own: their latency under load was most of a chunk's time), and no barrier
+// joins the CTA between chunks: a compute warp waits for chunk j's buffer
+// (epi_full) and counts itself out of it (epi_done), so warps run up to the
+// number of buffers apart and loads run that many chunks ahead.
+template <int SDT>
+struct StreamGeom {
+  static constexpr int kCC = 32, kChunks = kTileN / kCC;
+  static constexpr int kState = SDT == kSFp32 ? 16384 : 8192;  // bytes of a chunk's m or v
+  static constexpr int kOffS1 = 0, kOffS2 = kState, kOffW = 2 * kState;
+  static constexpr int kBuf = KCfg<kModeGrouped, kWBf16, SDT>::kEpiBuf;
+  static constexpr int NB = epi_bufs(kModeGrouped, SDT);
+  static_assert(kBuf >= kOffW + 8192, "m, v and 128 x 32 bf16 weights");
+};
+
+// Lane 0 of the I/O warp: loads NB chunks ahead; each finished chunk is stored
+// and, once the stores have read its buffer, the buffer loaded again.
+template <int KIND, int SDT>
+__device__ void grouped_io_role(const CUtensorMap* mS1, const CUtensorMap* mS2, const CUtensorMap* mW,
+                                const GemmParams& p, SharedState* ss, uint8_t* epi, uint32_t rank) {
+  using G = StreamGeom<SDT>;
+  constexpr int NB = G::NB;
+  constexpr bool U1 = uses_s1(KIND), U2 = uses_s2(KIND);
+  constexpr uint32_t kTx = (U1 ? G::kState : 0) + (U2 ? G::kState : 0) + 8192;
+  TileWalk<G::kChunks, true> walk;
+  walk.init(p, rank);
+  const int total = walk.total;
+  const uint64_t pol = evict_first_policy();  // touched once a step
+  auto issue = [&](int j) {
+    int row0, col0;
+    walk.where(j, G::kCC, row0, col0);
+    const int e = walk.expert(j);
+    uint8_t* buf = epi + (j % NB) * G::kBuf;
+    uint64_t* bar = &ss->epi_full[j % NB];
+    ptx::mbar_arrive_expect_tx(bar, kTx);
+    if (U1) ptx::tma_load_3d_hint(mS1, bar, buf + G::kOffS1, col0, row0, e, pol);
+    if (U2) ptx::tma_load_3d_hint(mS2, bar, buf + G::kOffS2, col0, row0, e, pol);
+    ptx::tma_load_3d_hint(mW, bar, buf + G::kOffW, col0, row0, e, pol);
+  };
+  int issued = 0, done = 0;
+  for (; issued < NB && issued < total; ++issued) issue(issued);
+  ptx::grid_dep_wait();  // dX has read the weights, before the first store
+  for (; done < total; ++done) {
+    if (done > 0 && done % G::kChunks == 0) walk.advance(done / G::kChunks, p, rank);
+    if (!bounded_wait(&ss->epi_done[done % NB], static_cast<uint32_t>(done / NB) & 1u, p, ss)) break;
+    int row0, col0;
+    walk.where(done, G::kCC, row0, col0);
+    const int e = walk.expert(done);
+    const uint8_t* buf = epi + (done % NB) * G::kBuf;
+    // rows past the expert's last are out of the maps' range, not the next expert's
+    if (U1) ptx::tma_store_3d_hint(mS1, buf + G::kOffS1, col0, row0, e, pol);
+    if (U2) ptx::tma_store_3d_hint(mS2, buf + G::kOffS2, col0, row0, e, pol);
+    ptx::tma_store_3d_hint(mW, buf + G::kOffW, col0, row0, e, pol);
+    ptx::bulk_commit_group();
+    if (issued < total) {
+      ptx::bulk_wait_group_read0();
+      issue(issued++);
+    }
+  }
+  ptx::bulk_wait_group0();
+  for (int j = done; j < issued; ++j)  // loads issued but not consumed (abort path)
+    bounded_wait(&ss->epi_full[j % NB], static_cast<uint32_t>(j / NB) & 1u, p, ss, false);
+}
+
+template <int KIND, int SDT>
+__device__ void grouped_compute_role(const GemmParams& p, SharedState* ss, uint8_t* epi, int warp, int lane,
+                                     uint32_t rank) {
+  using G = StreamGeom<SDT>;
+  constexpr int NB = G::NB;
+  const int quarter = warp & 3, sub = (warp - 2) >> 2;  // TMEM lane quarter, column quarter
+  const int r = quarter * 32 + lane;
+  const int64_t K = p.Ncols;
+  TileWalk<G::kChunks, true> walk;
+  walk.init(p, rank);
+  const uint32_t empty0 = ptx::mapa(ptx::smem_addr(&ss->tmem_empty[0]), 0);
+  // Lane 0 waits; the warp gets its verdict together.
+  auto wait = [&](uint64_t* bar, uint32_t parity) -> bool {
+    const bool ok = lane != 0 || bounded_wait(bar, parity, p, ss);
+    return __all_sync(0xFFFFFFFFu, ok);
+  };
+  for (int j = 0; j < walk.total; ++j) {
+    const int c = j % G::kChunks, local = j / G::kChunks, acc = local & 1;
+    if (c == 0) {
+      if (local > 0) walk.advance(local, p, rank);
+      if (!wait(&ss->tmem_full[acc], (static_cast<uint32_t>(local) >> 1) & 1u)) return;
+      ptx::tc_fence_after();
+    }
+    if (!wait(&ss->epi_full[j % NB], static_cast<uint32_t>(j / NB) & 1u)) return;
+    int row0, col0;
+    walk.where(j, G::kCC, row0, col0);
+    const int64_t row = static_cast<int64_t>(row0) + r + static_cast<int64_t>(walk.expert(j)) * p.M;
+    const int64_t e0 = row * K + col0 + sub * 8;  // rows and columns outside are computed on zeros and not stored
+    uint8_t* buf = epi + (j % NB) * G::kBuf;
+    const uint32_t taddr = ss->tmem_base + (static_cast<uint32_t>(quarter * 32) << 16) +
+                           static_cast<uint32_t>(acc * kTileN + c * G::kCC + sub * 8);
+    uint4* ws = reinterpret_cast<uint4*>(buf + G::kOffW + sw64(r, sub));
+    uint4 w = *ws;
+    if (SDT == kSFp32) epi_chunk_fp32<KIND, false>(taddr, buf, r, sub, e0, w, p);
+    else epi_chunk_bf16s<KIND, false>(taddr, buf, r, sub, e0, w, p);
+    *ws = w;
+    ptx::fence_proxy_async_smem();  // the new values, visible to the TMA stores
+    const bool last = c == G::kChunks - 1;
+    if (last) ptx::tc_fence_before();
+    __syncwarp();
+    if (lane == 0) {
+      ptx::mbar_arrive(&ss->epi_done[j % NB]);
+      if (last) ptx::mbar_arrive_cluster(empty0 + static_cast<uint32_t>(acc) * 8u);
+    }
+  }
+}
+
 template <int KIND, int WDT, int SDT, int MODE>
 __device__ __forceinline__ void epilogue_staged(const CUtensorMap* mS1, const CUtensorMap* mS2,
                                                 const CUtensorMap* mDX, const CUtensorMap* mW,
                                                 const GemmParams& p,
                                                 SharedState* ss, uint8_t* epi, int warp, int lane,
                                                 uint32_t rank) {
+  if constexpr (streamed(MODE, SDT)) {
+    if (warp != 2 + kNumEpiWarpsStaged) grouped_compute_role<KIND, SDT>(p, ss, epi, warp, lane, rank);
+    else if (lane == 0) grouped_io_role<KIND, SDT>(mS1, mS2, mW, p, ss, epi, rank);
+    return;
+  }
   if (warp == 2 + kNumEpiWarpsStaged)
     epilogue_io_role<KIND, SDT, MODE>(mS1, mS2, mDX, mW, p, ss, epi, lane, rank);
   else
@@ -1720,7 +1847,10 @@ __global__ void __launch_bounds__(KCfg<MODE, WDT, SDT>::kThreads, 1)
     for (int a = 0; a < 2; ++a) {
       ptx::mbar_init(&ss->tmem_full[a], 1);
       ptx::mbar_init(&ss->tmem_empty[a], 2 * Cfg::kEpiWarps);  // the leader's: both CTAs' warps
+    }
+    for (int a = 0; a < epi_bufs(MODE, SDT); ++a) {
       ptx::mbar_init(&ss->epi_full[a], 1);
+      ptx::mbar_init(&ss->epi_done[a], Cfg::kEpiWarps);
     }
     ptx::mbar_init(&ss->mma_done, 1);
     ss->abort = 0;
@@ -1759,9 +1889,9 @@ __global__ void __launch_bounds__(KCfg<MODE, WDT, SDT>::kThreads, 1)
       epilogue_role<MODE, WDT, SDT>(p, ss, warp, lane, rank);
   }
 
-  // A dependent launch (after the fp32-weight dX kernel) ends only after that
+  // A dependent launch (after the fp32-weight or the grouped dX kernel) ends only after that
   // grid, on every path (the epilogue's waits are skipped when a CTA aborts).
-  if (MODE == kModeFusedOpt) ptx::grid_dep_wait();
+  if (MODE == kModeFusedOpt || MODE == kModeGrouped) ptx::grid_dep_wait();
   __syncwarp();  // the producer's and MMA thread's lanes rejoin their warps first
   ptx::tc_fence_before();
   __syncthreads();
