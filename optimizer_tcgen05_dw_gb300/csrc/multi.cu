@@ -120,8 +120,7 @@ __device__ __forceinline__ void multi_group(const MultiItem& it, const OptScalar
       if (uses_s1(KIND)) load_f32(it.s1, e0, cnt, s1);
       if (uses_s2(KIND)) load_f32(it.s2, e0, cnt, s2);
     }
-#pragma unroll
-    for (int j = 0; j < 8; ++j) dev::rule<KIND>(w[j], g[j], s1[j], s2[j], sc);
+    dev::rule8<KIND>(w, g, s1, s2, sc);
     if (WDT == kWBf16) {
       store_b16(it.W, e0, cnt, pack_sr_bf16x8(w, dev::sr_words(static_cast<uint64_t>(e0) >> 3, seed + it.index, step)));
     } else {

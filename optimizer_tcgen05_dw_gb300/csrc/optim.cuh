@@ -93,6 +93,74 @@ __device__ __forceinline__ void rule(float& w, float g, float& s1, float& s2,
   }
 }
 
+// Pairs of float32 in one 64-bit register: Blackwell multiplies, adds and
+// fuses two at an instruction (.f32x2), each rounded as the scalar operation.
+struct f2 {
+  uint64_t v;
+};
+__device__ __forceinline__ f2 pair(float a, float b) {
+  f2 r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r.v) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ void unpair(f2 p, float& a, float& b) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(p.v));
+}
+__device__ __forceinline__ f2 mul(f2 a, f2 b) {
+  f2 r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+  return r;
+}
+// Sums stay scalar: a .f32x2 product and the .f32x2 sum that takes it come back
+// as one fused operation, .rn notwithstanding.
+__device__ __forceinline__ f2 add(f2 a, f2 b) {
+  float a0, a1, b0, b1;
+  unpair(a, a0, a1);
+  unpair(b, b0, b1);
+  return pair(__fadd_rn(a0, b0), __fadd_rn(a1, b1));
+}
+__device__ __forceinline__ f2 sub(f2 a, f2 b) {
+  float a0, a1, b0, b1;
+  unpair(a, a0, a1);
+  unpair(b, b0, b1);
+  return pair(__fsub_rn(a0, b0), __fsub_rn(a1, b1));
+}
+
+// rule<KIND> on two elements: AdamW in pairs (the same operations in the same
+// order, so the same bits), the others one after the other.
+template <int KIND>
+__device__ __forceinline__ void rule2(float (&w)[2], const float (&g)[2], float (&s1)[2], float (&s2)[2],
+                                      const OptScalars& sc) {
+  if constexpr (KIND == kAdamW) {
+    const f2 gp = pair(g[0], g[1]);
+    const f2 m = add(mul(pair(sc.b1, sc.b1), pair(s1[0], s1[1])), mul(pair(sc.omb1, sc.omb1), gp));
+    const f2 v = add(mul(pair(sc.b2, sc.b2), pair(s2[0], s2[1])), mul(pair(sc.omb2, sc.omb2), mul(gp, gp)));
+    unpair(m, s1[0], s1[1]);
+    unpair(v, s2[0], s2[1]);
+    const f2 d = add(mul(pair(sqr(s2[0]), sqr(s2[1])), pair(sc.inv_sqrt_c2, sc.inv_sqrt_c2)), pair(sc.eps, sc.eps));
+    float d0, d1;
+    unpair(d, d0, d1);
+    const f2 q = pair(dvd(s1[0], d0), dvd(s1[1], d1));
+    unpair(sub(mul(pair(w[0], w[1]), pair(sc.decay, sc.decay)), mul(pair(sc.step_size, sc.step_size), q)), w[0], w[1]);
+  } else {
+    rule<KIND>(w[0], g[0], s1[0], s2[0], sc);
+    rule<KIND>(w[1], g[1], s1[1], s2[1], sc);
+  }
+}
+template <int KIND>
+__device__ __forceinline__ void rule8(float (&w)[8], const float (&g)[8], float (&s1)[8], float (&s2)[8],
+                                      const OptScalars& sc) {
+#pragma unroll
+  for (int j = 0; j < 8; j += 2) {
+    float a[2] = {w[j], w[j + 1]}, c[2] = {s1[j], s1[j + 1]}, d[2] = {s2[j], s2[j + 1]};
+    const float b[2] = {g[j], g[j + 1]};
+    rule2<KIND>(a, b, c, d, sc);
+    w[j] = a[0]; w[j + 1] = a[1];
+    s1[j] = c[0]; s1[j + 1] = c[1];
+    s2[j] = d[0]; s2[j + 1] = d[1];
+  }
+}
+
 // ------------------------------------------------------------------ Philox
 
 // Philox4x32 with 10 rounds (Salmon et al., SC'11): per round, the 32x32->64

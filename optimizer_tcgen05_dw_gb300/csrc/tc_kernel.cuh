@@ -856,8 +856,7 @@ __device__ __forceinline__ void epi_chunk_fp32(uint32_t taddr, uint8_t* buf, int
 #pragma unroll
   for (int j = 0; j < 8; ++j) g[j] = __uint_as_float(gr[j]);
   if (SCALE) scale_grad(g, p);
-#pragma unroll
-  for (int j = 0; j < 8; ++j) dev::rule<KIND>(w[j], g[j], s1[j], s2[j], p.sc);
+  dev::rule8<KIND>(w, g, s1, s2, p.sc);
   wv = pack_sr_bf16x8(w, rnd);
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
@@ -938,8 +937,7 @@ __device__ __forceinline__ void epi_chunk_bf16s(uint32_t taddr, uint8_t* buf, in
     if (!uses_s1(KIND)) s1[j] = 0.f;
     if (!uses_s2(KIND)) s2[j] = 0.f;
   }
-#pragma unroll
-  for (int j = 0; j < 8; ++j) dev::rule<KIND>(w[j], g[j], s1[j], s2[j], p.sc);
+  dev::rule8<KIND>(w, g, s1, s2, p.sc);
   wv = pack_sr_bf16x8(w, rnd);
   if (uses_s1(KIND)) *reinterpret_cast<uint4*>(buf + kOffS1 + sw64(r, sub)) = pack_rne_bf16x8(s1);
   if (uses_s2(KIND)) *reinterpret_cast<uint4*>(buf + kOffS2 + sw64(r, sub)) = pack_rne_bf16x8(s2);
