@@ -297,6 +297,115 @@ __global__ void __launch_bounds__(kGThreads, 1)
   }
 }
 
+// ---------------------------------------------------------------- few tokens
+
+// The forward product of a few rows (decoding): every live expert's weights are
+// read once for a handful of tokens, so the floor is that read, and what
+// matters is to spread it evenly over the GPU and keep it streaming.  The
+// 256-feature tiles above do neither (12 live experts of 2048 features are 96
+// of them for 76 pairs).  Here a block takes 16 features of one expert; its
+// eight warps share K (32 columns each in turn, so that a block reads 512
+// contiguous bytes of a row at a time), multiply on the 16 x 8 x 16 warp-level
+// matrix instruction, which takes its weights from registers (each is used
+// once: staging it through shared memory for a larger instruction would only
+// lengthen its way), and add their sums in shared memory in warp order.
+// The instruction's k order is free as long as both operands agree: a lane
+// loads 16 contiguous bytes (eight k) of its row and of its token, and feeds
+// them to two instructions.
+constexpr int kFewRows = 16, kFewWarps = 8, kFewTiles = 4;  // up to 4 x 8 tokens a pass
+
+__device__ __forceinline__ uint4 ld_once(const uint4* p) {
+  uint4 v;
+  asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
+  return v;
+}
+
+__device__ __forceinline__ void mma_16x8x16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                            uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+      "{%0, %1, %2, %3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// Features f0 .. f0 + 15 (those below F) of tokens t0 .. t0 + 8 NT - 1 (those
+// below tend), by the whole block.  Rows and tokens past the end repeat the
+// last one; their results are not stored.
+template <int NT>
+__device__ __forceinline__ void few_product(const uint16_t* W, const uint16_t* X, const GroupedParams& p, int f0, int t0,
+                                            int tend, int K, float* s_sum) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, q = lane & 3;
+  const int V = K >> 3;
+  const uint4* w0 = reinterpret_cast<const uint4*>(W + static_cast<int64_t>(min(f0 + g, p.F - 1)) * K);
+  const uint4* w1 = reinterpret_cast<const uint4*>(W + static_cast<int64_t>(min(f0 + g + 8, p.F - 1)) * K);
+  const uint4* x[NT];
+  float acc[NT][4];
+#pragma unroll
+  for (int i = 0; i < NT; ++i) {
+    x[i] = reinterpret_cast<const uint4*>(X + static_cast<int64_t>(min(t0 + 8 * i + g, tend - 1)) * K);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) acc[i][j] = 0.f;
+  }
+  const uint4 zero = make_uint4(0, 0, 0, 0);
+#pragma unroll 4
+  for (int v = warp * 4 + q; v - q < V; v += kFewWarps * 4) {  // uniform over the warp
+    const bool in = v < V;
+    const uint4 a = in ? ld_once(w0 + v) : zero, b = in ? ld_once(w1 + v) : zero;
+#pragma unroll
+    for (int i = 0; i < NT; ++i) {
+      const uint4 t = in ? x[i][v] : zero;
+      mma_16x8x16(acc[i], a.x, b.x, a.y, b.y, t.x, t.y);
+      mma_16x8x16(acc[i], a.z, b.z, a.w, b.w, t.z, t.w);
+    }
+  }
+  // [warp][token][feature]; a lane holds features g, g + 8 of tokens 2 q, 2 q + 1 of each tile
+  constexpr int kCols = 8 * NT;
+#pragma unroll
+  for (int i = 0; i < NT; ++i)
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      s_sum[(warp * kCols + 8 * i + 2 * q + (j & 1)) * kFewRows + g + 8 * (j >> 1)] = acc[i][j];
+  __syncthreads();
+  for (int o = threadIdx.x; o < kCols * kFewRows; o += 32 * kFewWarps) {
+    const int t = t0 + o / kFewRows, f = f0 + o % kFewRows;
+    float sum = 0.f;
+#pragma unroll
+    for (int w = 0; w < kFewWarps; ++w) sum += s_sum[w * kCols * kFewRows + o];
+    if (t < tend && f < p.F) {
+      const __nv_bfloat16 b = __float2bfloat16_rn(sum);
+      static_cast<uint16_t*>(p.out)[static_cast<int64_t>(t) * p.F + f] = *reinterpret_cast<const uint16_t*>(&b);
+    }
+  }
+  __syncthreads();  // before the next pass overwrites the sums
+}
+
+__global__ void __launch_bounds__(32 * kFewWarps) grouped_few_kernel(const uint16_t* W, const uint16_t* X,
+                                                                     const GroupedParams p, const int K) {
+  __shared__ float s_sum[kFewWarps * 8 * kFewTiles * kFewRows];
+  const int e = blockIdx.y, f0 = blockIdx.x * kFewRows;
+  const int a = p.offsets[e], b = p.offsets[e + 1];
+  const int begin = min(max(a, 0), p.T), end = min(max(b, begin), p.T);
+  if (blockIdx.x == 0 && threadIdx.x == 0 && (a < 0 || b < a || b > p.T))
+    atomicCAS(p.status, 0u, static_cast<uint32_t>(kStatusInvalid));
+  const uint16_t* We = W + static_cast<int64_t>(e) * p.F * K;
+  for (int t0 = begin; t0 < end; t0 += 8 * kFewTiles) {
+    if (end - t0 <= 8) few_product<1>(We, X, p, f0, t0, end, K, s_sum);
+    else if (end - t0 <= 16) few_product<2>(We, X, p, f0, t0, end, K, s_sum);
+    else few_product<kFewTiles>(We, X, p, f0, t0, end, K, s_sum);
+  }
+  // rows of no group: before the first and after the last
+  const int f = f0 + static_cast<int>(threadIdx.x);
+  if (threadIdx.x < kFewRows && f < p.F) {
+    uint16_t* Y = static_cast<uint16_t*>(p.out);
+    if (e == 0)
+      for (int t = 0; t < begin; ++t) Y[static_cast<int64_t>(t) * p.F + f] = 0;
+    if (e == p.groups - 1)
+      for (int t = end; t < p.T; ++t) Y[static_cast<int64_t>(t) * p.F + f] = 0;
+  }
+}
+
 template <bool DGRAD>
 cudaError_t run_grouped(const CUtensorMap& w, const GroupedMaps& m, const GroupedParams& p, int grid, cudaStream_t s) {
   auto* k = grouped_kernel<DGRAD>;
@@ -318,6 +427,12 @@ cudaError_t run_grouped(const CUtensorMap& w, const GroupedMaps& m, const Groupe
 }
 
 }  // namespace
+
+cudaError_t launch_grouped_few(const void* W, const void* X, const GroupedParams& p, int K, cudaStream_t s) {
+  const dim3 grid(static_cast<unsigned>((p.F + kFewRows - 1) / kFewRows), static_cast<unsigned>(p.groups));
+  grouped_few_kernel<<<grid, 32 * kFewWarps, 0, s>>>(static_cast<const uint16_t*>(W), static_cast<const uint16_t*>(X), p, K);
+  return cudaGetLastError();
+}
 
 cudaError_t launch_grouped(bool dgrad, const CUtensorMap& w, const CUtensorMap (&tok)[4],
                            const GroupedParams& p, int grid, cudaStream_t s) {

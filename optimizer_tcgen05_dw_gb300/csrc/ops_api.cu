@@ -85,6 +85,11 @@ forge_status_t grouped_product(const forge_grouped_t* g, const void* W, bool dgr
   p.wait_limit_ns = wait_limit_ns();
   p.status = d.status;
   p.skip_loads = skip_loads() ? 1 : 0;
+  if (!dgrad && g->T <= kFewMaxT && p.skip_loads == 0) {  // (that hook is for the pipelined kernels' waits)
+    if ((e = launch_grouped_few(W, tok, p, static_cast<int>(R), s)) != cudaSuccess)
+      return cuda_fail(e, "grouped product launch");
+    return FORGE_OK;
+  }
   const cuuint64_t N = static_cast<cuuint64_t>(g->N), K = static_cast<cuuint64_t>(g->K),
                    E = static_cast<cuuint64_t>(g->groups);
   CUtensorMap mw, mt[4];

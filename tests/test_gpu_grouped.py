@@ -25,8 +25,11 @@ GROUPS = [
     ([1], 256, 64), ([0, 1, 0, 2], 264, 200), ([5, 0, 33, 257, 300, 16], 512, 320), ([1300], 256, 256),
     ([2049, 3, 0], 128, 72), ([0, 0, 0], 64, 64), ([63, 64, 65, 31, 32, 33], 520, 136), ([17] * 70, 136, 264),
     ([1] * 300 + [0] * 700, 8, 8), ([700, 1, 900], 1024, 1096),
+    # 32 rows or fewer in all take the forward product's own kernel: tiles of 8, 16 and 32 tokens, ragged K and N
+    ([8], 16, 32), ([9, 0, 23], 200, 328), ([16, 16], 24, 40), ([32], 264, 1032), ([1] * 32, 8, 8), ([0, 17, 15, 0], 72, 264),
+    ([33], 264, 1032),
 ]
-IDS = [f"{len(c)}groups_T{sum(c)}_N{n}_K{k}" for c, n, k in GROUPS]
+IDS = [f"{len(c)}groups_T{sum(c)}_N{n}_K{k}_{max(c)}most" for c, n, k in GROUPS]
 
 
 @pytest.fixture(scope="module", autouse=True)
@@ -98,8 +101,9 @@ def test_products_on_normal_data(counts, N, K):
         near(dX[r], dY[r], W[e], N)
 
 
-def test_rows_of_no_group_become_zero():
-    counts, N, K, lead, tail = [40, 0, 7], 72, 136, 13, 29
+@pytest.mark.parametrize("counts,lead,tail", [([40, 0, 7], 13, 29), ([5, 0, 7], 3, 9)])
+def test_rows_of_no_group_become_zero(counts, lead, tail):
+    N, K = 72, 136
     T = lead + sum(counts) + tail
     W, X, dY = _grid((3, N, K), -3, 1), _grid((T, K), 0, 2), _grid((T, N), -6, 3)
     X[:lead], X[-tail:] = float("nan"), float("inf")
@@ -113,9 +117,9 @@ def test_rows_of_no_group_become_zero():
         assert torch.equal(dX[r], _round(dY[r].double() @ W[e].double()))
 
 
+@pytest.mark.parametrize("counts", [[30, 45, 70, 3], [10, 5, 9, 3]], ids=["tiles", "few"])
 @pytest.mark.parametrize("N,K", [(200, 328), (256, 320)])
-def test_values_that_are_not_finite_stay_in_their_group(N, K):
-    counts = [30, 45, 70, 3]
+def test_values_that_are_not_finite_stay_in_their_group(N, K, counts):
     T = sum(counts)
     W, X, dY = _grid((4, N, K), -3, 1), _grid((T, K), 0, 2), _grid((T, N), -6, 3)
     rows = dict(_slices(counts))
@@ -271,9 +275,10 @@ def test_gradient_of_the_products_against_differences():
         assert abs(slope - float(dX[t, k])) <= 2.0 ** -8 * abs(slope) + 1e-9
 
 
-@pytest.mark.parametrize("offsets", [[0, 50, 20, 90], [-5, 10, 20, 90], [0, 10, 200, 300], [2 ** 31 - 1, 0, -2 ** 31, 7]])
-def test_offsets_out_of_order_or_range_are_clamped_and_reported(offsets):
-    T, N, K = 90, 64, 64
+@pytest.mark.parametrize("offsets", [[0, 50, 20, 90], [-5, 10, 20, 90], [0, 10, 200, 300], [2 ** 31 - 1, 0, -2 ** 31, 7], [0, 5, 5, 91]])
+@pytest.mark.parametrize("T", [90, 20])
+def test_offsets_out_of_order_or_range_are_clamped_and_reported(offsets, T):
+    N, K = 64, 64
     W, X, dY = _grid((3, N, K), -3, 1), _grid((T, K), 0, 2), _grid((T, N), -6, 3)
     off = torch.tensor(offsets, dtype=torch.int32, device="cuda")
     guard = torch.zeros((3 * T, N), dtype=torch.bfloat16, device="cuda")
