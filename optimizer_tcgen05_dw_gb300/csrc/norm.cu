@@ -26,37 +26,74 @@ namespace {
 
 constexpr float kE4M3Max = 448.f;
 
-__device__ __forceinline__ void unpack8(uint4 v, float (&f)[8]) {
+// Elements are handled in pairs (dev::f2): at these rates a dozen scalar
+// operations per element would take as long as its bytes.
+using dev::f2;
+using dev::pair;
+using dev::unpair;
+
+__device__ __forceinline__ f2 fma2(f2 a, f2 b, f2 c) {
+  f2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
+  return r;
+}
+__device__ __forceinline__ f2 mul2(f2 a, f2 b) { return dev::mul(a, b); }
+__device__ __forceinline__ f2 both(float a) { return pair(a, a); }
+
+// Eight bf16 as four pairs.
+__device__ __forceinline__ void unpack8(uint4 v, f2 (&f)[4]) {
   const uint32_t a[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    f[2 * j] = dev::bf16_to_f32(a[j] & 0xFFFFu);
-    f[2 * j + 1] = __uint_as_float(a[j] & 0xFFFF0000u);
-  }
+  for (int j = 0; j < 4; ++j) f[j] = pair(dev::bf16_to_f32(a[j]), __uint_as_float(a[j] & 0xFFFF0000u));
 }
 
-__device__ __forceinline__ uint32_t pack2(float a, float b) {
+__device__ __forceinline__ uint32_t pack2(f2 p) {
+  float a, b;
+  unpair(p, a, b);
   const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
   return *reinterpret_cast<const uint32_t*>(&h);
 }
 
-__device__ __forceinline__ uint4 pack8(const float (&f)[8]) {
-  return make_uint4(pack2(f[0], f[1]), pack2(f[2], f[3]), pack2(f[4], f[5]), pack2(f[6], f[7]));
+__device__ __forceinline__ uint4 pack8(const f2 (&f)[4]) {
+  return make_uint4(pack2(f[0]), pack2(f[1]), pack2(f[2]), pack2(f[3]));
 }
 
-// Two floats to E4M3 codes (a in the low byte): nearest even, saturating at
-// the largest finite value, NaN kept.
+// Two floats to E4M3 codes (the first in the low byte): nearest even,
+// saturating at the largest finite value, NaN kept.
 __device__ __forceinline__ uint32_t e4m3x2(float a, float b) {
   return __nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3);
 }
+__device__ __forceinline__ uint32_t e4m3x2(f2 p) {
+  float a, b;
+  unpair(p, a, b);
+  return e4m3x2(a, b);
+}
 
+// Sums of bf16 pairs, rounded once to bf16.  (Rounding through float32 gives
+// the same: a float32 holds the sum of two 8-bit significands exactly unless
+// one is below half a bf16 ulp of the other, and then both give the larger.)
+__device__ __forceinline__ uint32_t add_bf16x2(uint32_t a, uint32_t b) {
+  const __nv_bfloat162 s = __hadd2_rn(*reinterpret_cast<const __nv_bfloat162*>(&a), *reinterpret_cast<const __nv_bfloat162*>(&b));
+  return *reinterpret_cast<const uint32_t*>(&s);
+}
 __device__ __forceinline__ uint4 add_bf16x8(uint4 a, uint4 b) {
-  float x[8], y[8];
-  unpack8(a, x);
-  unpack8(b, y);
+  return make_uint4(add_bf16x2(a.x, b.x), add_bf16x2(a.y, b.y), add_bf16x2(a.z, b.z), add_bf16x2(a.w, b.w));
+}
+
+// The larger of `top` and the pairs' magnitudes (a NaN does not count).
+__device__ __forceinline__ float max_abs(float top, const f2 (&f)[4]) {
 #pragma unroll
-  for (int j = 0; j < 8; ++j) x[j] += y[j];
-  return pack8(x);
+  for (int j = 0; j < 4; ++j) {
+    float a, b;
+    unpair(f[j], a, b);
+    top = fmaxf(top, fmaxf(fabsf(a), fabsf(b)));
+  }
+  return top;
+}
+__device__ __forceinline__ float sum2(f2 p) {
+  float a, b;
+  unpair(p, a, b);
+  return a + b;
 }
 
 __device__ __forceinline__ float warp_sum(float v) {
@@ -78,22 +115,21 @@ __device__ __forceinline__ float inv_rms(float sum, int K, float eps) {
 // ---------------------------------------------------------------- forward
 
 // A block takes rows blockIdx.x, blockIdx.x + gridDim.x, ...; thread i holds
-// vectors i, i + blockDim.x, .. (NV of them, eight columns each) of the row and
-// of the weight.  Sum and maximum are reduced together: one barrier a row, the
-// partials in alternating halves of `red`.
-template <int NV, bool RES>
-__global__ void __launch_bounds__(512) norm_fwd_kernel(const NormParams p) {
+// vectors i, i + blockDim.x, .. (NV of them, eight columns each) of the row;
+// the weight comes from L1.  What keeps memory busy is rows in flight, so many
+// rows run on few threads each (one warp up to K = 2560: no barrier) and the
+// blocks of an SM are at different points of theirs; few rows run on many
+// threads each, for the shortest time to one.  Sum and maximum are reduced
+// together: one barrier a row, the partials in alternating halves of `red`.
+// The row is kept as the products h w, so that the output is one factor away.
+template <int NV, bool RES, bool MANY>
+__global__ void __launch_bounds__(MANY ? 256 : 512, MANY ? 2 : 1) norm_fwd_kernel(const NormParams p) {
   __shared__ float red[2][2][16];  // [row parity][sum, max][warp]
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, warps = blockDim.x >> 5;
   const int V = p.K >> 3;
   const bool want_max = p.q != nullptr;
-  const uint4* W = static_cast<const uint4*>(p.w);
-  uint4 w[NV];
-#pragma unroll
-  for (int i = 0; i < NV; ++i) {
-    const int v = tid + i * blockDim.x;
-    w[i] = v < V ? W[v] : make_uint4(0, 0, 0, 0);
-  }
+  const uint4* w = static_cast<const uint4*>(p.w);
+  const uint4 zero = make_uint4(0, 0, 0, 0);
   int par = 0;
   for (int64_t t = blockIdx.x; t < p.T; t += gridDim.x, par ^= 1) {
     const uint4* x = static_cast<const uint4*>(p.x) + t * V;
@@ -101,7 +137,7 @@ __global__ void __launch_bounds__(512) norm_fwd_kernel(const NormParams p) {
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       const int v = tid + i * blockDim.x;
-      h[i] = v < V ? x[v] : make_uint4(0, 0, 0, 0);
+      h[i] = v < V ? x[v] : zero;
     }
     if (RES) {
       const uint4* res = static_cast<const uint4*>(p.res) + t * V;
@@ -110,7 +146,7 @@ __global__ void __launch_bounds__(512) norm_fwd_kernel(const NormParams p) {
 #pragma unroll
       for (int i = 0; i < NV; ++i) {
         const int v = tid + i * blockDim.x;
-        r[i] = v < V ? res[v] : make_uint4(0, 0, 0, 0);
+        r[i] = v < V ? res[v] : zero;
       }
 #pragma unroll
       for (int i = 0; i < NV; ++i) {
@@ -119,19 +155,23 @@ __global__ void __launch_bounds__(512) norm_fwd_kernel(const NormParams p) {
         if (v < V) ho[v] = h[i];
       }
     }
-    float sum = 0.f, top = 0.f;
+    f2 sums = both(0.f);
+    float top = 0.f;
+    f2 hw[NV][4];
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      float f[8], g[8];
+      const int v = tid + i * blockDim.x;
+      f2 f[4], g[4];
       unpack8(h[i], f);
-      unpack8(w[i], g);
+      unpack8(v < V ? w[v] : zero, g);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        sum = __fmaf_rn(f[j], f[j], sum);
-        if (want_max) top = fmaxf(top, fabsf(f[j] * g[j]));
+      for (int j = 0; j < 4; ++j) {
+        sums = fma2(f[j], f[j], sums);
+        hw[i][j] = mul2(f[j], g[j]);
       }
+      if (want_max) top = max_abs(top, hw[i]);
     }
-    sum = warp_sum(sum);
+    float sum = warp_sum(sum2(sums));
     if (want_max) top = warp_max(top);
     if (warps > 1) {
       if (lane == 0) {
@@ -156,22 +196,19 @@ __global__ void __launch_bounds__(512) norm_fwd_kernel(const NormParams p) {
       inv = amax == 0.f ? 0.f : fminf(__fdiv_rn(kE4M3Max, amax), 3.4e38f) + (amax - amax);
       if (tid == 0) p.q_scale[t] = __fdiv_rn(amax, kE4M3Max);
     }
+    if (p.y == nullptr && !want_max) continue;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       const int v = tid + i * blockDim.x;
       if (v >= V) continue;
-      float f[8], g[8];
-      unpack8(h[i], f);
-      unpack8(w[i], g);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) f[j] = f[j] * rstd * g[j];
-      if (p.y != nullptr) static_cast<uint4*>(p.y)[t * V + v] = pack8(f);
+      for (int j = 0; j < 4; ++j) hw[i][j] = mul2(hw[i][j], both(rstd));
+      if (p.y != nullptr) static_cast<uint4*>(p.y)[t * V + v] = pack8(hw[i]);
       if (want_max) {
 #pragma unroll
-        for (int j = 0; j < 8; ++j) f[j] *= inv;
-        static_cast<uint2*>(p.q)[t * V + v] =
-            make_uint2(e4m3x2(f[0], f[1]) | (e4m3x2(f[2], f[3]) << 16),
-                       e4m3x2(f[4], f[5]) | (e4m3x2(f[6], f[7]) << 16));
+        for (int j = 0; j < 4; ++j) hw[i][j] = mul2(hw[i][j], both(inv));
+        static_cast<uint2*>(p.q)[t * V + v] = make_uint2(e4m3x2(hw[i][0]) | (e4m3x2(hw[i][1]) << 16),
+                                                         e4m3x2(hw[i][2]) | (e4m3x2(hw[i][3]) << 16));
       }
     }
   }
@@ -186,19 +223,34 @@ __global__ void __launch_bounds__(512) norm_fwd_kernel(const NormParams p) {
 // each, a whole sector.  Nothing is read from global memory twice: 7 B an
 // element with a residual.
 constexpr int kTransTokens = 32;
-constexpr int kTransCols = 2048;  // of a segment, at most: 128 KiB of shared memory
+constexpr int kTransSmem = 131072;  // bytes of a block, at most
 
-// A float of the same shared variable in block `rank` of the cluster.
-__device__ __forceinline__ float cluster_float(const float* p, uint32_t rank) {
-  float v;
-  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(ptx::mapa(ptx::smem_addr(p), rank)) : "memory");
-  return v;
+// 32 aligned bytes.
+__device__ __forceinline__ void store32(void* to, const uint32_t (&v)[8]) {
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};"
+               ::"l"(to), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+               : "memory");
 }
 
+// Store a pair of floats to the same shared variable of the cluster's block
+// `rank`, counted on that block's mbarrier when it has landed.
+__device__ __forceinline__ void cluster_store2(const void* dst, uint64_t* bar, uint32_t rank, float a, float b) {
+  asm volatile(
+      "st.async.shared::cluster.mbarrier::complete_tx::bytes.v2.f32 [%0], {%2, %3}, [%1];"
+      ::"r"(ptx::mapa(ptx::smem_addr(dst), rank)), "r"(ptx::mapa(ptx::smem_addr(bar), rank)), "f"(a), "f"(b)
+      : "memory");
+}
+
+// The blocks of a cluster hand their rows' shares to each other with counted
+// stores: a cluster barrier would have to wait for the h just written to
+// reach L2 as well.
 template <bool RES>
-__global__ void __launch_bounds__(256) norm_fwd_t_kernel(const NormParams p, const int cluster, const int seg) {
-  extern __shared__ __align__(16) uint4 s_h[];  // [32][seg / 8]
-  __shared__ float s_sum[kTransTokens], s_top[kTransTokens], s_rstd[kTransTokens];
+__global__ void __launch_bounds__(256, 3) norm_fwd_t_kernel(const NormParams p, const int cluster, const int seg) {
+  extern __shared__ __align__(16) uint4 s_h[];  // [rows][seg / 8]
+  __shared__ __align__(8) float2 s_part[8][kTransTokens];  // [block of the cluster][row]: sum, max
+  __shared__ float s_rstd[kTransTokens];
+  __shared__ __align__(8) uint64_t s_bar;
+  constexpr int kRows = 4;  // rows of a warp loaded together
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int V = p.K >> 3, SV = seg >> 3;
   const int rank = static_cast<int>(ptx::cluster_ctarank());
@@ -206,221 +258,274 @@ __global__ void __launch_bounds__(256) norm_fwd_t_kernel(const NormParams p, con
   const int mine = min(SV, V - v0);  // vectors of this block's segment (at least one: host)
   const int64_t t0 = static_cast<int64_t>(blockIdx.x / cluster) * kTransTokens;
   const int rows = static_cast<int>(p.T - t0 < kTransTokens ? p.T - t0 : kTransTokens);  // 16 or 32
+  if (tid == 0) {
+    ptx::mbar_init(&s_bar, 1);
+    ptx::fence_mbar_init();
+    ptx::mbar_arrive_expect_tx(&s_bar, static_cast<uint32_t>(cluster * rows * 8));
+  }
+  ptx::cluster_sync();  // every block's barrier is there
   const uint4* w = static_cast<const uint4*>(p.w) + v0;
-  for (int r = warp; r < rows; r += 8) {
-    const int64_t at = (t0 + r) * V + v0;
-    const uint4* x = static_cast<const uint4*>(p.x) + at;
-    const uint4* res = static_cast<const uint4*>(p.res) + at;
-    uint4* ho = static_cast<uint4*>(p.h) + at;
-    float sum = 0.f, top = 0.f;
-#pragma unroll 4
-    for (int v = lane; v < mine; v += 32) {
-      uint4 h = x[v];
-      if (RES) {
-        h = add_bf16x8(h, res[v]);
-        ho[v] = h;
-      }
-      s_h[r * SV + v] = h;
-      float f[8], g[8];
-      unpack8(h, f);
-      unpack8(w[v], g);
+  const bool want_max = p.amax != nullptr;
+  // rows warp, warp + 8, ..: of 16 tokens, the last two repeat the first two and are not kept
+  const int64_t at = (t0 + warp) * V + v0;
+  const uint4* x = static_cast<const uint4*>(p.x) + at;
+  const uint4* res = static_cast<const uint4*>(p.res) + at;
+  uint4* ho = static_cast<uint4*>(p.h) + at;
+  f2 sums[kRows];
+  float top[kRows];
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        sum = __fmaf_rn(f[j], f[j], sum);
-        top = fmaxf(top, fabsf(f[j] * g[j]));
-      }
+  for (int i = 0; i < kRows; ++i) {
+    sums[i] = both(0.f);
+    top[i] = 0.f;
+  }
+  const int step = rows == kTransTokens ? 8 * V : 0;  // to the third and fourth row
+  for (int v = lane; v < mine; v += 32) {
+    uint4 h[kRows], q[kRows];
+#pragma unroll
+    for (int i = 0; i < kRows; ++i) h[i] = x[v + (i & 1) * 8 * V + (i >> 1) * 2 * step];
+    if (RES) {
+#pragma unroll
+      for (int i = 0; i < kRows; ++i) q[i] = res[v + (i & 1) * 8 * V + (i >> 1) * 2 * step];
     }
-    sum = warp_sum(sum);
-    top = warp_max(top);
-    if (lane == 0) {
-      s_sum[r] = sum;
-      s_top[r] = top;
+    f2 g[4];
+    if (want_max) unpack8(w[v], g);
+#pragma unroll
+    for (int i = 0; i < kRows; ++i) {
+      const int r = warp + 8 * i;
+      if (RES) h[i] = add_bf16x8(h[i], q[i]);
+      if (r < rows) {
+        if (RES) ho[v + 8 * i * V] = h[i];
+        s_h[r * SV + v] = h[i];
+      }
+      f2 f[4];
+      unpack8(h[i], f);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        sums[i] = fma2(f[j], f[j], sums[i]);
+        f[j] = mul2(f[j], g[j]);
+      }
+      if (want_max) top[i] = max_abs(top[i], f);
     }
   }
-  ptx::cluster_sync();  // every block's shares are there
-  if (tid < rows) {     // each block adds them in the same order
-    float sum = 0.f, top = 0.f;
-    for (int c = 0; c < cluster; ++c) {
-      sum += cluster_float(&s_sum[tid], c);
-      top = fmaxf(top, cluster_float(&s_top[tid], c));
+#pragma unroll
+  for (int i = 0; i < kRows; ++i) {
+    const int r = warp + 8 * i;
+    const float sum = warp_sum(sum2(sums[i])), most = want_max ? warp_max(top[i]) : 0.f;
+    if (r < rows && lane < cluster) cluster_store2(&s_part[rank][r], &s_bar, lane, sum, most);
+  }
+  __syncthreads();  // s_h is whole
+  if (tid < rows) {
+    // landed from every block (each try waits up to a millisecond)
+    int tries = 0;
+    while (!ptx::mbar_try_wait(&s_bar, 0u)) {
+      if (++tries > p.wait_tries) {
+        atomicCAS(p.status, 0u, static_cast<uint32_t>(kStatusTimeout));
+        break;
+      }
+    }
+    float sum = 0.f, most = 0.f;
+    for (int c = 0; c < cluster; ++c) {  // the same order in each block
+      sum += s_part[c][tid].x;
+      most = fmaxf(most, s_part[c][tid].y);
     }
     const float rstd = inv_rms(sum, p.K, p.eps);
-    s_rstd[tid] = rstd;
+    s_rstd[tid] = rstd * p.inv_scale;
     if (rank == 0) {
       if (p.rstd != nullptr) p.rstd[t0 + tid] = rstd;
-      if (p.amax != nullptr) {
-        const float amax = top * rstd;
+      if (want_max) {
+        const float amax = most * rstd;
         const uint32_t bits = amax == amax ? __float_as_uint(amax) : 0x7FC00000u;  // a NaN wins
-        const uint32_t most = __reduce_max_sync(rows == 32 ? 0xFFFFFFFFu : 0xFFFFu, bits);
-        if (tid == 0) atomicMax(reinterpret_cast<unsigned int*>(p.amax), most);
+        const uint32_t all = __reduce_max_sync(rows == 32 ? 0xFFFFFFFFu : 0xFFFFu, bits);
+        if (tid == 0) atomicMax(reinterpret_cast<unsigned int*>(p.amax), all);
       }
     }
   }
   __syncthreads();
-  asm volatile("barrier.cluster.arrive.release;" ::: "memory");  // done with the others' shares
   const uint32_t* src = reinterpret_cast<const uint32_t*>(s_h);
   const uint32_t* w2 = reinterpret_cast<const uint32_t*>(w);
   uint8_t* out = static_cast<uint8_t*>(p.qt) + static_cast<int64_t>(v0) * 8 * p.T + t0;
+  const bool whole = p.T % 32 == 0 && (reinterpret_cast<uintptr_t>(p.qt) & 31u) == 0;
   for (int c = tid; c < mine * 4; c += 256) {
-    const float w0 = dev::bf16_to_f32(w2[c] & 0xFFFFu), w1 = __uint_as_float(w2[c] & 0xFFFF0000u);
+    const f2 wp = pair(dev::bf16_to_f32(w2[c]), __uint_as_float(w2[c] & 0xFFFF0000u));
+    uint8_t* to = out + static_cast<int64_t>(2 * c) * p.T;
+    uint32_t o0[8], o1[8];
 #pragma unroll
-    for (int half = 0; half < 2; ++half) {
-      if (half * 16 >= rows) break;
-      uint32_t o0[4], o1[4];
+    for (int q = 0; q < 8; ++q) {
+      float a[4], b[4];
 #pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        float a[4], b[4];
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const int t = half * 16 + 4 * q + j;
-          const uint32_t u = src[t * (seg >> 1) + c];
-          const float r = s_rstd[t];
-          a[j] = dev::bf16_to_f32(u & 0xFFFFu) * r * w0 * p.inv_scale;
-          b[j] = __uint_as_float(u & 0xFFFF0000u) * r * w1 * p.inv_scale;
-        }
-        o0[q] = e4m3x2(a[0], a[1]) | (e4m3x2(a[2], a[3]) << 16);
-        o1[q] = e4m3x2(b[0], b[1]) | (e4m3x2(b[2], b[3]) << 16);
+      for (int j = 0; j < 4; ++j) {
+        const int t = 4 * q + j;  // past `rows`: not stored
+        const uint32_t u = src[t * (seg >> 1) + c];
+        const f2 y = mul2(mul2(pair(dev::bf16_to_f32(u), __uint_as_float(u & 0xFFFF0000u)), both(s_rstd[t])), wp);
+        unpair(y, a[j], b[j]);
       }
-      uint8_t* to = out + static_cast<int64_t>(2 * c) * p.T + half * 16;
-      *reinterpret_cast<uint4*>(to) = make_uint4(o0[0], o0[1], o0[2], o0[3]);
-      *reinterpret_cast<uint4*>(to + p.T) = make_uint4(o1[0], o1[1], o1[2], o1[3]);
+      o0[q] = e4m3x2(a[0], a[1]) | (e4m3x2(a[2], a[3]) << 16);
+      o1[q] = e4m3x2(b[0], b[1]) | (e4m3x2(b[2], b[3]) << 16);
+    }
+    if (whole) {  // rows of whole 32-byte sectors: one a store
+      store32(to, o0);
+      store32(to + p.T, o1);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+        if (16 * i < rows) {
+          *reinterpret_cast<uint4*>(to + 16 * i) = make_uint4(o0[4 * i], o0[4 * i + 1], o0[4 * i + 2], o0[4 * i + 3]);
+          *reinterpret_cast<uint4*>(to + p.T + 16 * i) = make_uint4(o1[4 * i], o1[4 * i + 1], o1[4 * i + 2], o1[4 * i + 3]);
+        }
     }
   }
-  asm volatile("barrier.cluster.wait.acquire;" ::: "memory");  // nobody reads this block's shares any more
 }
 
 // ---------------------------------------------------------------- gradient
 
-// As the forward's rows; each thread keeps its columns' share of dw over the
-// block's rows in registers and writes it to the block's row of `partial`.
-// The next row is loaded before the present one is reduced (PRE), so that the
-// barrier does not leave memory idle.
+// A block takes rows blockIdx.x, blockIdx.x + gridDim.x, ...; each thread keeps
+// its columns' share of dw over them in registers and writes it to the block's
+// row of `partial` at the end.  The next row is loaded before the present one is
+// reduced (PRE), so that the barrier does not leave memory idle; the weight
+// waits in shared memory.
 template <int NV, bool DH, bool PRE, int MAXT, int MINB>
 __global__ void __launch_bounds__(MAXT, MINB) norm_bwd_kernel(const NormParams p) {
+  extern __shared__ __align__(16) uint4 s_w[];  // [NV * blockDim.x]
   __shared__ float red[2][16];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, warps = blockDim.x >> 5;
   const int V = p.K >> 3;
   const uint4 zero = make_uint4(0, 0, 0, 0);
-  uint4 w[NV];
-  float acc[NV][8];
+  f2 acc[NV][4];
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
     const int v = tid + i * blockDim.x;
-    w[i] = v < V ? static_cast<const uint4*>(p.w)[v] : zero;
+    s_w[v] = v < V ? static_cast<const uint4*>(p.w)[v] : zero;  // its own reader
 #pragma unroll
-    for (int j = 0; j < 8; ++j) acc[i][j] = 0.f;
+    for (int j = 0; j < 4; ++j) acc[i][j] = both(0.f);
   }
-  uint4 dy[NV], h[NV], dh[NV], dy2[NV], h2[NV], dh2[NV];
-  float rs = 0.f, rs2 = 0.f;
-  auto load = [&](int64_t t, uint4 (&a)[NV], uint4 (&b)[NV], uint4 (&c)[NV], float& r) {
-    r = p.rstd[t];
+  struct Row {
+    uint4 dy[NV], h[NV], dh[NV];
+    float rs;
+  };
+  auto load = [&](int64_t t, Row& r) {
+    r.rs = p.rstd[t];
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       const int v = tid + i * blockDim.x;
-      a[i] = v < V ? static_cast<const uint4*>(p.dy)[t * V + v] : zero;
-      b[i] = v < V ? static_cast<const uint4*>(p.x)[t * V + v] : zero;
-      if (DH) c[i] = v < V ? static_cast<const uint4*>(p.dh)[t * V + v] : zero;
+      r.dy[i] = v < V ? static_cast<const uint4*>(p.dy)[t * V + v] : zero;
+      r.h[i] = v < V ? static_cast<const uint4*>(p.x)[t * V + v] : zero;
+      if (DH) r.dh[i] = v < V ? static_cast<const uint4*>(p.dh)[t * V + v] : zero;
     }
   };
   int par = 0;
-  if (blockIdx.x < p.T) load(blockIdx.x, dy, h, dh, rs);
-  for (int64_t t = blockIdx.x; t < p.T; t += gridDim.x, par ^= 1) {
-    const bool more = t + gridDim.x < p.T;
-    if (PRE && more) load(t + gridDim.x, dy2, h2, dh2, rs2);
-    float dot = 0.f;
+  auto row = [&](int64_t t, const Row& r) {
+    f2 dots = both(0.f), g[NV][4];
+    const f2 r2 = both(r.rs);
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      float a[8], b[8], g[8];
-      unpack8(dy[i], a);
-      unpack8(h[i], b);
-      unpack8(w[i], g);
+      f2 a[4], b[4], w[4];
+      unpack8(r.dy[i], a);
+      unpack8(r.h[i], b);
+      unpack8(s_w[tid + i * blockDim.x], w);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const float n = b[j] * rs;
-        dot = __fmaf_rn(a[j] * g[j], n, dot);
-        acc[i][j] = __fmaf_rn(a[j], n, acc[i][j]);
+      for (int j = 0; j < 4; ++j) {
+        const f2 n = mul2(b[j], r2);
+        g[i][j] = mul2(a[j], w[j]);
+        dots = fma2(g[i][j], n, dots);
+        acc[i][j] = fma2(a[j], n, acc[i][j]);
       }
     }
-    dot = warp_sum(dot);
+    float dot = warp_sum(sum2(dots));
     if (warps > 1) {
       if (lane == 0) red[par][warp] = dot;
       __syncthreads();
       dot = 0.f;
       for (int i = 0; i < warps; ++i) dot += red[par][i];
+      par ^= 1;
     }
-    const float mean = __fdiv_rn(dot, static_cast<float>(p.K));
+    // dx = rs (g - n mean) + dh = rs g - (rs^2 mean) h + dh
+    const f2 back = both(-(r.rs * r.rs) * __fdiv_rn(dot, static_cast<float>(p.K)));
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       const int v = tid + i * blockDim.x;
       if (v >= V) continue;
-      float a[8], b[8], g[8], d[8];
-      unpack8(dy[i], a);
-      unpack8(h[i], b);
-      unpack8(w[i], g);
-      if (DH) unpack8(dh[i], d);
+      f2 b[4], d[4];
+      unpack8(r.h[i], b);
+      if (DH) unpack8(r.dh[i], d);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const float x = rs * __fmaf_rn(-b[j] * rs, mean, a[j] * g[j]);
-        a[j] = DH ? x + d[j] : x;
-      }
-      static_cast<uint4*>(p.y)[t * V + v] = pack8(a);
+      for (int j = 0; j < 4; ++j) b[j] = fma2(g[i][j], r2, DH ? fma2(b[j], back, d[j]) : mul2(b[j], back));
+      static_cast<uint4*>(p.y)[t * V + v] = pack8(b);
     }
-    if (PRE) {
-#pragma unroll
-      for (int i = 0; i < NV; ++i) {
-        dy[i] = dy2[i];
-        h[i] = h2[i];
-        if (DH) dh[i] = dh2[i];
-      }
-      rs = rs2;
-    } else if (more) {
-      load(t + gridDim.x, dy, h, dh, rs);
+  };
+  const int64_t G = gridDim.x;
+  int64_t t = blockIdx.x;
+  Row r0;
+  if (PRE) {  // two rows' registers take turns
+    Row r1;
+    if (t < p.T) load(t, r0);
+    while (t < p.T) {
+      if (t + G < p.T) load(t + G, r1);
+      row(t, r0);
+      t += G;
+      if (t >= p.T) break;
+      if (t + G < p.T) load(t + G, r0);
+      row(t, r1);
+      t += G;
+    }
+  } else {
+    for (; t < p.T; t += G) {
+      load(t, r0);
+      row(t, r0);
     }
   }
+  ptx::grid_dep_launch();  // the sum over blocks may start as they end
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
     const int v = tid + i * blockDim.x;
     if (v >= V) continue;
     float4* o = reinterpret_cast<float4*>(p.partial + static_cast<int64_t>(blockIdx.x) * p.K + 8 * v);
-    o[0] = make_float4(acc[i][0], acc[i][1], acc[i][2], acc[i][3]);
-    o[1] = make_float4(acc[i][4], acc[i][5], acc[i][6], acc[i][7]);
+    float a[8];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) unpair(acc[i][j], a[2 * j], a[2 * j + 1]);
+    o[0] = make_float4(a[0], a[1], a[2], a[3]);
+    o[1] = make_float4(a[4], a[5], a[6], a[7]);
   }
 }
 
-// dw = the sum of the blocks' shares, always in the same order.
-__global__ void __launch_bounds__(256) norm_dw_kernel(const float* partial, float* dw, int K, int rows) {
-  __shared__ float s[8][33];
+// dw = the sum of the blocks' shares, always in the same order: sixteen groups
+// of rows in parallel, eight loads ahead in each.
+constexpr int kDwParts = 16;
+__global__ void __launch_bounds__(32 * kDwParts) norm_dw_kernel(const float* partial, float* dw, int K, int rows) {
+  __shared__ float s[kDwParts][33];
   const int lane = threadIdx.x & 31, part = threadIdx.x >> 5;
   const int k = blockIdx.x * 32 + lane;
   float sum = 0.f;
-  if (k < K)
-    for (int r = part; r < rows; r += 8) sum += partial[static_cast<int64_t>(r) * K + k];
+  ptx::grid_dep_wait();
+  if (k < K) {
+#pragma unroll 8
+    for (int r = part; r < rows; r += kDwParts) sum += partial[static_cast<int64_t>(r) * K + k];
+  }
   s[part][lane] = sum;
   __syncthreads();
   if (part == 0 && k < K) {
 #pragma unroll
-    for (int i = 1; i < 8; ++i) sum += s[i][lane];
+    for (int i = 1; i < kDwParts; ++i) sum += s[i][lane];
     dw[k] = sum;
   }
 }
 
 int round32(int n) { return (n + 31) / 32 * 32; }
 
-template <int NV>
+template <int NV, bool MANY>
 void run_fwd(const NormParams& p, int grid, int threads, cudaStream_t s) {
-  if (p.res != nullptr) norm_fwd_kernel<NV, true><<<grid, threads, 0, s>>>(p);
-  else norm_fwd_kernel<NV, false><<<grid, threads, 0, s>>>(p);
+  if (p.res != nullptr) norm_fwd_kernel<NV, true, MANY><<<grid, threads, 0, s>>>(p);
+  else norm_fwd_kernel<NV, false, MANY><<<grid, threads, 0, s>>>(p);
 }
 
 template <bool RES>
 cudaError_t run_fwd_t(const NormParams& p, cudaStream_t s) {
   const int V = p.K / 8;
-  int cluster = 1;  // segments of at most 1024 columns (64 KiB: three blocks an SM) up to K = 8192
-  while (cluster < 8 && V > 128 * cluster) cluster *= 2;
+  int cluster = 1;  // segments of at most 512 columns (32 KiB) up to K = 4096
+  while (cluster < 8 && V > 64 * cluster) cluster *= 2;
   const int seg = (V + cluster - 1) / cluster * 8;
   const int smem = kTransTokens * seg * 2;
   auto* k = norm_fwd_t_kernel<RES>;
-  cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, kTransTokens * kTransCols * 2);
+  cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, kTransSmem);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>((p.T + kTransTokens - 1) / kTransTokens * cluster), 1, 1);
@@ -439,8 +544,8 @@ cudaError_t run_fwd_t(const NormParams& p, cudaStream_t s) {
 
 template <int NV, bool PRE, int MAXT, int MINB>
 void run_bwd(const NormParams& p, int grid, int threads, cudaStream_t s) {
-  if (p.dh != nullptr) norm_bwd_kernel<NV, true, PRE, MAXT, MINB><<<grid, threads, 0, s>>>(p);
-  else norm_bwd_kernel<NV, false, PRE, MAXT, MINB><<<grid, threads, 0, s>>>(p);
+  if (p.dh != nullptr) norm_bwd_kernel<NV, true, PRE, MAXT, MINB><<<grid, threads, NV * threads * 16, s>>>(p);
+  else norm_bwd_kernel<NV, false, PRE, MAXT, MINB><<<grid, threads, NV * threads * 16, s>>>(p);
 }
 
 int64_t least(int64_t a, int64_t b) { return a < b ? a : b; }
@@ -452,17 +557,26 @@ cudaError_t launch_norm_fwd(const NormParams& p0, int num_sms, cudaStream_t s) {
   const int V = p.K / 8;
   cudaError_t e;
   if (p.qt == nullptr || p.y != nullptr || p.q != nullptr) {
-    // Few rows: as many threads a row as it has vectors, up to 512, for the
-    // shortest time to one row.  Else two vectors a thread (four past
-    // K = 8192), so that a block's reduction is spread over more loads.
-    int nv = p.T < num_sms ? 1 : (V >= 128 ? 2 : 1);
-    while ((V + nv - 1) / nv > 512) nv *= 2;
-    const int threads = round32((V + nv - 1) / nv);
-    const int per_sm = static_cast<int>(least(32, 2048 / threads));
-    const int grid = static_cast<int>(least(p.T, static_cast<int64_t>(num_sms) * per_sm));
-    if (nv == 1) run_fwd<1>(p, grid, threads, s);
-    else if (nv == 2) run_fwd<2>(p, grid, threads, s);
-    else run_fwd<4>(p, grid, threads, s);
+    if (p.T < 2 * num_sms) {  // few rows
+      int nv = 1;
+      while ((V + nv - 1) / nv > 512) nv *= 2;
+      const int threads = round32((V + nv - 1) / nv);
+      const int grid = static_cast<int>(p.T);
+      if (nv == 1) run_fwd<1, false>(p, grid, threads, s);
+      else if (nv == 2) run_fwd<2, false>(p, grid, threads, s);
+      else run_fwd<4, false>(p, grid, threads, s);
+    } else {
+      int warps = 1;
+      while (V > 32 * 10 * warps) warps *= 2;
+      const int nv = (V + 32 * warps - 1) / (32 * warps);
+      const int grid = static_cast<int>(least(p.T, static_cast<int64_t>(num_sms) * (32 / warps)));
+      if (nv <= 1) run_fwd<1, true>(p, grid, 32 * warps, s);
+      else if (nv <= 2) run_fwd<2, true>(p, grid, 32 * warps, s);
+      else if (nv <= 4) run_fwd<4, true>(p, grid, 32 * warps, s);
+      else if (nv <= 6) run_fwd<6, true>(p, grid, 32 * warps, s);
+      else if (nv <= 8) run_fwd<8, true>(p, grid, 32 * warps, s);
+      else run_fwd<10, true>(p, grid, 32 * warps, s);
+    }
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
     if (p.res != nullptr) p.x = p.h;  // for the codes below
     p.res = nullptr;
@@ -476,24 +590,38 @@ cudaError_t launch_norm_fwd(const NormParams& p0, int num_sms, cudaStream_t s) {
 }
 
 int64_t norm_bwd_blocks(int64_t T, int K, int num_sms) {
+  // two blocks an SM, or eight of narrow rows (few threads each); every block adds a row to `partial`
   return least(T, static_cast<int64_t>(num_sms) * (K >= 2048 ? 2 : 8));
 }
 
 cudaError_t launch_norm_bwd(const NormParams& p, int num_sms, cudaStream_t s) {
   const int V = p.K / 8;
+  // Loading a row ahead pays where its registers leave room for it: with one
+  // vector a thread (16384 x 2048: 60 us, 69 without) and with two in one block
+  // an SM (4096 x 8192: 50 and 69); two blocks of two vectors a thread are
+  // faster without (12289 x 5120: 87 and 107, spilled), and four do not fit.
   const int nv = V <= 256 ? 1 : (V <= 1024 ? 2 : 4);
   const int threads = round32((V + nv - 1) / nv);
   const int grid = static_cast<int>(norm_bwd_blocks(p.T, p.K, num_sms));
   if (grid > 0) {
     if (nv == 1) run_bwd<1, true, 256, 4>(p, grid, threads, s);
-    else if (nv == 2 && threads <= 320) run_bwd<2, true, 320, 2>(p, grid, threads, s);
+    else if (nv == 2 && threads <= 320) run_bwd<2, false, 320, 2>(p, grid, threads, s);
     else if (nv == 2) run_bwd<2, true, 512, 1>(p, grid, threads, s);
     else run_bwd<4, false, 512, 1>(p, grid, threads, s);
     const cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return e;
   }
-  norm_dw_kernel<<<(p.K + 31) / 32, 256, 0, s>>>(p.partial, p.dw, p.K, grid);
-  return cudaGetLastError();
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>((p.K + 31) / 32), 1, 1);
+  cfg.blockDim = dim3(32 * kDwParts, 1, 1);
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = grid > 0 ? 1 : 0;
+  const float* partial = p.partial;
+  return cudaLaunchKernelEx(&cfg, norm_dw_kernel, partial, p.dw, static_cast<int>(p.K), grid);
 }
 
 }  // namespace forge
