@@ -101,9 +101,8 @@ struct MultiItem {
   uint32_t first;    // its first tile in the launch
   uint32_t index;    // its place in the caller's list: added to the rounding seed
 };
-// Tensors a launch carries in its parameters (64 bytes each): the short form
-// fits the 4 KB that every launch can pass at no extra cost.
-constexpr int kMultiShort = 56, kMultiLong = 480;
+// Tensors a launch carries in its parameters (64 bytes each, 32 KB at most).
+constexpr int kMultiShort = 56, kMultiMiddle = 140, kMultiLong = 480;
 constexpr int kMultiTile = 2048;  // elements per block
 template <int CAP>
 struct MultiParams {

@@ -122,7 +122,7 @@ def test_int8_block_widths(block):
     s.check(gpu, 3, 77)
 
 
-@pytest.mark.parametrize("count", [1, 56, 57, 480, 481, 1000])
+@pytest.mark.parametrize("count", [1, 56, 57, 140, 141, 480, 481, 1000])
 def test_table_sizes_on_either_side_of_a_launch(count):
     s = Set([1 + (37 * i) % 150 for i in range(count)], "bf16", "bf16", "fp32", "adamw")
     gpu = s.on_gpu()
