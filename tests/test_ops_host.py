@@ -72,7 +72,49 @@ def test_norm_gradient_refusals(L, change, status, word):
     assert rc == status and word in _message(L), (rc, _message(L))
 
 
+def _grouped(**kw):
+    a = dict(T=40, N=64, K=128, groups=4, offsets=FAKE, X=FAKE, dY=FAKE, Y=FAKE, dX=FAKE)
+    a.update(kw)
+    return ctypes.byref(api.ForgeGrouped(**a))
+
+
+@pytest.mark.parametrize("change,status,word", [
+    (dict(T=-1), 1, "negative"), (dict(groups=-1), 1, "negative"), (dict(N=12), 1, "multiples of 8"),
+    (dict(K=100), 1, "multiples of 8"), (dict(groups=1025), 2, "1024 groups"), (dict(offsets=0), 1, "offsets"),
+    (dict(offsets=FAKE + 2), 1, "offsets"), (dict(T=1 << 31), 2, "31 bits"), (dict(N=1 << 24, groups=200), 2, "31 bits")])
+def test_grouped_refusals(L, change, status, word):
+    st = api.ForgeState(FAKE, api.W_BF16_SR, api.STATE_FP32, FAKE, FAKE, None, None)
+    hp = api.hparams()
+    for call in (lambda g: L.forge_grouped_linear(g, FAKE, None), lambda g: L.forge_grouped_dgrad(g, FAKE, None),
+                 lambda g: L.forge_grouped_bwd_step(g, ctypes.byref(st), 0, ctypes.byref(hp), 1, 0, None)):
+        rc = call(_grouped(**change))
+        assert rc == status and word in _message(L), (rc, _message(L))
+
+
+@pytest.mark.parametrize("state,kind,step,change,status,word", [
+    (dict(w_dtype=0), 0, 1, {}, 2, "bf16 weights"), (dict(s1=0), 0, 1, {}, 1, "needs s1"),
+    (dict(s_dtype=1), 0, 1, {}, 1, "scale"), (dict(s_dtype=1), 0, 1, dict(K=72), 1, "K % 64"),
+    (dict(), 9, 1, {}, 1, "opt_kind"), (dict(), 0, 0, {}, 1, "step"), (dict(), 0, 1, dict(X=0), 1, "X is NULL"),
+    (dict(), 0, 1, dict(dY=FAKE + 8), 1, "dY must"), (dict(), 0, 1, dict(dX=FAKE + 8), 1, "dX must"),
+    (dict(W=0), 0, 1, {}, 1, "W must")])
+def test_grouped_step_refusals(L, state, kind, step, change, status, word):
+    a = dict(W=FAKE, w_dtype=1, s_dtype=0, s1=FAKE, s2=FAKE, s1_scale=None, s2_scale=None)
+    a.update(state)
+    st, hp = api.ForgeState(**a), api.hparams()
+    rc = L.forge_grouped_bwd_step(_grouped(**change), ctypes.byref(st), kind, ctypes.byref(hp), step, 0, None)
+    assert rc == status and word in _message(L), (rc, _message(L))
+
+
+def test_grouped_nothing_to_do_needs_no_device(L):
+    assert L.forge_grouped_linear(_grouped(T=0), FAKE, None) == 0
+    assert L.forge_grouped_linear(_grouped(N=0), FAKE, None) == 0
+    assert L.forge_grouped_dgrad(_grouped(T=0), FAKE, None) == 0
+    st, hp = api.ForgeState(FAKE, api.W_BF16_SR, api.STATE_FP32, FAKE, FAKE, None, None), api.hparams()
+    assert L.forge_grouped_bwd_step(_grouped(groups=0, dX=None), ctypes.byref(st), 0, ctypes.byref(hp), 1, 0, None) == 0
+
+
 def test_null_structs(L):
+    assert L.forge_grouped_linear(None, None, None) == 1 and L.forge_grouped_dgrad(None, None, None) == 1
     assert L.forge_rmsnorm_fwd(None, None) == 1 and L.forge_rmsnorm_bwd(None, None) == 1
     hp = api.hparams()
     assert L.forge_multi_opt_step(None, 3, 0, 0, 0, 0, ctypes.byref(hp), 1, 0, None) == 1
@@ -94,6 +136,11 @@ def test_the_binding_refuses_what_the_library_could_not_see():
         api.make_tensors([f((4, 4)).t()], [f(16)])
     with pytest.raises(ValueError, match="block"):
         api.make_tensors([f(4)], [f(4)], [f(4, torch.int8)], [f(4, torch.uint8)], block=48)
+    b = lambda *n: torch.zeros(n, dtype=torch.bfloat16)  # noqa: E731
+    with pytest.raises(ValueError, match=r"\[groups, N, K\]"):
+        api.forge_grouped_linear(b(4, 8), b(8, 8), torch.zeros(2, dtype=torch.int32), b(4, 8))
+    with pytest.raises(ValueError, match="CUDA tensor"):
+        api.forge_grouped_linear(b(4, 8), b(2, 8, 8), torch.zeros(3, dtype=torch.int32), b(4, 8))
     x = torch.zeros((2, 8), dtype=torch.bfloat16)
     with pytest.raises(ValueError, match="CUDA tensor"):
         api.forge_rmsnorm_fwd(x, x[0], 1e-6, y=x)
