@@ -123,8 +123,9 @@ def test_int8_block_widths(block):
 
 
 @pytest.mark.parametrize("count", [1, 56, 57, 140, 141, 480, 481, 1000])
-def test_table_sizes_on_either_side_of_a_launch(count):
-    s = Set([1 + (37 * i) % 150 for i in range(count)], "bf16", "bf16", "fp32", "adamw")
+@pytest.mark.parametrize("s_dtype", ["fp32", "int8"])
+def test_table_sizes_on_either_side_of_a_launch(count, s_dtype):
+    s = Set([(37 * i) % 150 if i % 7 else 2048 * (i % 3) + i % 5 for i in range(count - 1)] + [9], "bf16", "bf16", s_dtype, "adamw")
     gpu = s.on_gpu()
     _step(s, gpu)
     s.check(gpu, 3, 77)
