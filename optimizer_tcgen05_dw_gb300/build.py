@@ -27,10 +27,10 @@ NVCC_FLAGS = ARCH + ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC",
 
 LIBS = {
     "libforge.so": ["api.cu", "ops_api.cu", "tc_fused.cu", "tc_step.cu", "tc_fp8.cu", "tc_plain.cu", "elementwise.cu",
-                    "tc_grouped.cu", "grouped.cu", "multi.cu", "norm.cu"],
+                    "tc_grouped.cu", "tc_grouped_long.cu", "grouped.cu", "multi.cu", "norm.cu"],
     "libforge_testkit.so": ["testkit.cu"],
 }
-HEADERS = ["common.h", "elem.cuh", "host.h", "launch.h", "optim.cuh", "ptx.cuh", "tc_kernel.cuh"]
+HEADERS = ["common.h", "elem.cuh", "host.h", "launch.h", "optim.cuh", "ptx.cuh", "tc_grouped.cuh", "tc_kernel.cuh"]
 
 
 def nvcc() -> str:

@@ -93,7 +93,9 @@ enum GemmMode : int32_t {
   kModeDgrad = 2,      // dX tile -> bf16 store
   kModeStep = 3,       // one launch: the dX tiles, then the dW tiles -> optimizer epilogue
   kModeFusedFp8 = 4,   // the FORGE step from E4M3 operands (token-contiguous, scaled)
-  kModeGrouped = 5     // the FORGE step of many experts' weights over ragged token groups
+  kModeGrouped = 5,    // the FORGE step of many experts' weights over ragged token groups
+  kModeGroupedMid = 6, // the same for longer groups,
+  kModeGroupedLong = 7 // and for long ones or INT8 states (see grouped() in tc_kernel.cuh)
 };
 
 // Column blocks (of kTileN) whose dX-completion counters the one-launch step
@@ -155,7 +157,7 @@ struct GemmParams {
   // INT8 states: elements per absmax block along a row (32, 64, 128 or 256;
   // the scale arrays are [M x Ncols / qblock]) and its base-2 logarithm.
   int32_t qblock, qshift;
-  // kModeGrouped: W and the states hold `groups` experts' [M x Ncols] in
+  // kModeGrouped*: W and the states hold `groups` experts' [M x Ncols] in
   // sequence; expert e's gradient sums over token rows offsets[e] ..
   // offsets[e + 1] - 1 of the operands' `tokens` rows.
   const int32_t* offsets;

@@ -69,14 +69,29 @@ cudaError_t launch_dgrad_fp32w(const void* dY, const float* W, void* dX, int64_t
                                int64_t K, int num_sms, cudaStream_t s);
 
 
-// tc_grouped.cu: the FORGE step of every expert (mode kModeGrouped, bf16
-// weights): a, b the operands with a stage's rows as a dimension (see
-// producer_role), s1, s2, w with the experts as a third.  With `after_dx` the
-// launch may start while the grouped dX kernel before it on the stream still
-// runs; it writes nothing before that grid has ended.
-cudaError_t launch_tc_grouped(int sdt, const CUtensorMap& a, const CUtensorMap& b, const CUtensorMap& s1,
+// The grouped step's mode for T tokens over `groups` experts.  An expert's
+// length is known on the device only, so the rule goes by their mean.  Step
+// kernels, us, fp32 and bf16 moments, in the order short, middle, long
+// (16384 tokens):
+//   mean 16384 (1 of 4096 x 4096)   526 408   420 362   363 354
+//   mean  4096 (4 of 4096 x 4096)   562 428   468 395   425 390
+//   mean  2048 (8 of 4096 x 4096)   681 492   577 468   686 527
+//   mean  1024 (16 of 2048 x 4096)  493 367   577 434   661 504
+inline int group_mode(int64_t T, int64_t groups, int sdt) {
+  if (sdt != kSFp32 && sdt != kSBf16) return kModeGroupedLong;
+  return T < 1536 * groups ? kModeGrouped : (T < 3584 * groups ? kModeGroupedMid : kModeGroupedLong);
+}
+// tc_grouped.cu, tc_grouped_long.cu: the FORGE step of every expert (modes
+// kModeGrouped*, bf16 weights): a, b the operands with a stage's rows as a
+// dimension (see producer_role), s1, s2, w with the experts as a third.  With
+// `after_dx` the launch may start while the grouped dX kernel before it on the
+// stream still runs; it writes nothing before that grid has ended.
+cudaError_t launch_tc_grouped(int mode, int sdt, const CUtensorMap& a, const CUtensorMap& b, const CUtensorMap& s1,
                               const CUtensorMap& s2, const CUtensorMap& w, const GemmParams& p, int grid,
                               cudaStream_t s, bool after_dx);
+cudaError_t launch_tc_grouped_long(int mode, int sdt, const CUtensorMap& a, const CUtensorMap& b,
+                                   const CUtensorMap& s1, const CUtensorMap& s2, const CUtensorMap& w,
+                                   const GemmParams& p, int grid, cudaStream_t s, bool after_dx);
 // grouped.cu: the grouped forward product (dgrad false) or dX (true).  w: the
 // weights' map; tok[i]: the token operand in boxes of 64 columns x (16 << i)
 // rows.

@@ -248,7 +248,7 @@ forge_status_t forge_grouped_bwd_step(const forge_grouped_t* g, const forge_stat
     return st;
   const int pairs = p.num_units < d.num_sms / 2 ? p.num_units : d.num_sms / 2;
   // after dX's kernel (N > 0, T > 0: it was launched) the step may start at once
-  if ((e = launch_tc_grouped(sdt, ma, mb, m1, m2, mw, p, 2 * pairs, s, g->dX != nullptr)) != cudaSuccess)
+  if ((e = launch_tc_grouped(group_mode(T, g->groups, sdt), sdt, ma, mb, m1, m2, mw, p, 2 * pairs, s, g->dX != nullptr)) != cudaSuccess)
     return cuda_fail(e, "grouped step launch");
   return FORGE_OK;
 }

@@ -89,15 +89,21 @@ constexpr int kEpiBufBytes = 32768;
 constexpr int kEpiBufBytesW = 37888;
 __host__ __device__ constexpr bool stages_weights(int sdt) { return sdt == kSInt8W || sdt == kSInt8WX; }
 __host__ __device__ constexpr bool compact_int8(int sdt) { return sdt == kSInt8W; }
-// The grouped step with fp32 or bf16 states takes the streamed epilogue
-// (grouped_io_role, grouped_compute_role), which stages the weights too, in
-// more and larger chunk buffers, and has fewer operand stages: an expert's
-// reduction is short, so the epilogue is what takes the time.
-__host__ __device__ constexpr bool streamed(int mode, int sdt) {
-  return mode == kModeGrouped && (sdt == kSFp32 || sdt == kSBf16);
+// The grouped step's epilogue and its share of shared memory go by how long an
+// expert's reduction is (group_mode, launch.h): short ones take the streamed
+// epilogue (grouped_io_role, grouped_compute_role), which stages the weights
+// too, with many chunk buffers and a short operand ring, since the epilogue is
+// what takes the time; longer ones the same with the ring deeper, and the
+// longest, as INT8 states, the staged epilogue of the linear step.
+__host__ __device__ constexpr bool grouped(int mode) {
+  return mode == kModeGrouped || mode == kModeGroupedMid || mode == kModeGroupedLong;
 }
+__host__ __device__ constexpr bool streamed(int mode) { return mode == kModeGrouped || mode == kModeGroupedMid; }
 __host__ __device__ constexpr int epi_bufs(int mode, int sdt) {
-  return !streamed(mode, sdt) ? 2 : (sdt == kSFp32 ? 3 : 4);
+  return mode != kModeGrouped ? 2 : (sdt == kSFp32 ? 3 : 4);
+}
+__host__ __device__ constexpr int stream_stages(int mode, int sdt) {  // what the buffers leave of 227 KiB
+  return sdt == kSFp32 ? (mode == kModeGrouped ? 3 : 4) : (mode == kModeGrouped ? 4 : 5);
 }
 constexpr int kEpiBarrier = 1;       // named barrier of the epilogue warps
 constexpr int kEpiInnerBarrier = 2;  // the staged epilogue's compute warps only
@@ -109,20 +115,20 @@ struct KCfg {
   // the staged epilogue: every FORGE step with bf16 weights, and the fused
   // step with fp32 weights and fp32 states
   static constexpr bool kTmaEpi =
-      ((MODE == kModeFusedOpt || MODE == kModeStep || MODE == kModeGrouped || kFp8) && WDT == kWBf16) ||
+      ((MODE == kModeFusedOpt || MODE == kModeStep || grouped(MODE) || kFp8) && WDT == kWBf16) ||
       (MODE == kModeFusedOpt && WDT == kWFp32 && SDT == kSFp32);
   static constexpr bool kStageW = kTmaEpi && stages_weights(SDT);
   static constexpr int kBK =
       kFp8 ? kFp8BlockK
            : (kTmaEpi ? kFusedBlockK : (MODE == kModeWgradStore ? kWgradBlockK : kBlockK));  // tokens per stage
   static constexpr int kStg =
-      kTmaEpi ? (streamed(MODE, SDT) ? (SDT == kSFp32 ? kFusedStages - 2 : kFusedStages - 1)
+      kTmaEpi ? (streamed(MODE) ? stream_stages(MODE, SDT)
                   : kStageW && !compact_int8(SDT) ? kFusedStages - 1 : kFusedStages)
               : (MODE == kModeWgradStore ? kWgradStages : kStages);
   static constexpr int kEsz = kFp8 ? 1 : 2;           // operand element bytes
   static constexpr int kA = kTileM * kBK * kEsz;       // bytes of A per stage (this CTA's 128 rows)
   static constexpr int kB = (kTileN / 2) * kBK * kEsz; // bytes of B per stage (this CTA's 128 columns)
-  static constexpr int kEpiBuf = streamed(MODE, SDT) ? (SDT == kSFp32 ? 40960 : 24576)
+  static constexpr int kEpiBuf = streamed(MODE) ? (SDT == kSFp32 ? 40960 : 24576)
                                  : kStageW && !compact_int8(SDT) ? kEpiBufBytesW : kEpiBufBytes;
   static constexpr int kEpiBytes = kTmaEpi ? epi_bufs(MODE, SDT) * kEpiBuf : 0;
   static constexpr int kSmem = kStg * (kA + kB) + kEpiBytes + 512 + 1024;
@@ -131,6 +137,10 @@ struct KCfg {
   static constexpr int kEpiWarps = kTmaEpi ? kNumEpiWarpsStaged : kNumEpiWarps;
   static constexpr int kThreads = 32 * (2 + kEpiWarps + (kTmaEpi ? 1 : 0));  // + the I/O warp
 };
+static_assert(KCfg<kModeGrouped, kWBf16, kSFp32>::kSmem <= 232448 && KCfg<kModeGrouped, kWBf16, kSBf16>::kSmem <= 232448 &&
+                  KCfg<kModeGroupedMid, kWBf16, kSFp32>::kSmem <= 232448 &&
+                  KCfg<kModeGroupedMid, kWBf16, kSBf16>::kSmem <= 232448,
+              "dynamic shared memory limit");
 static_assert(sizeof(SharedState) <= 512, "shared state region");
 static_assert(KCfg<kModeFusedOpt, kWBf16>::kStg <= 8 && KCfg<kModeWgradStore, kWBf16>::kStg <= 8 &&
                   kStages <= 8, "barrier arrays");
@@ -267,7 +277,7 @@ __device__ void producer_role(const CUtensorMap* mA, const CUtensorMap* mB, cons
         }
       }
     }
-    if constexpr (MODE == kModeGrouped) {
+    if constexpr (grouped(MODE)) {
       // Ragged reductions: the operands' maps have the 64 rows of a stage as a
       // dimension of their own ahead of the row it starts from.  A full stage
       // is read from row 0 of that dimension; an expert's last stage of n < 64
@@ -416,7 +426,7 @@ __device__ void mma_role(const GemmParams& p, uint8_t* smA, uint8_t* smB, Shared
   }
   for (int u = pair_id(); u < p.num_units; u += num_pairs()) {  // a half unit: N = 128
     int num_kb = p.num_kb;
-    if (MODE == kModeGrouped) {
+    if (grouped(MODE)) {
       int begin, count;
       group_rows(u / p.group_tiles, p, begin, count);
       num_kb = group_stages(count, BK);
@@ -1336,7 +1346,7 @@ __device__ void epilogue_io_role(const CUtensorMap* mS1, const CUtensorMap* mS2,
                                  const CUtensorMap* mDX, const CUtensorMap* mW, const GemmParams& p,
                                  SharedState* ss, uint8_t* epi, int lane, uint32_t rank) {
   using G = StagedGeom<KIND, SDT>;
-  constexpr bool STEP = MODE == kModeStep, GROUPED = MODE == kModeGrouped;
+  constexpr bool STEP = MODE == kModeStep, GROUPED = grouped(MODE);
   TileWalk<G::kChunks, GROUPED> walk;
   walk.init(p, rank);
   const int total = walk.total;
@@ -1472,7 +1482,7 @@ template <int KIND, int WDT, int SDT, int MODE>
 __device__ void epilogue_compute_role(const GemmParams& p, SharedState* ss, uint8_t* epi,
                                       int warp, int lane, uint32_t rank) {
   using G = StagedGeom<KIND, SDT>;
-  constexpr bool STEP = MODE == kModeStep, SCALE = MODE == kModeFusedFp8, GROUPED = MODE == kModeGrouped;
+  constexpr bool STEP = MODE == kModeStep, SCALE = MODE == kModeFusedFp8, GROUPED = grouped(MODE);
   constexpr bool F32W = WDT == kWFp32;
   constexpr int kCC = G::kCC, kChunks = G::kChunks, kWPerThread = G::kWPerThread;
   constexpr int kWV = kWPerThread * (F32W ? 4 : 2) / 16;  // 16-byte words of weights per thread and chunk
@@ -1674,22 +1684,22 @@ __device__ void epilogue_compute_role(const GemmParams& p, SharedState* ss, uint
 // joins the CTA between chunks: a compute warp waits for chunk j's buffer
 // (epi_full) and counts itself out of it (epi_done), so warps run up to the
 // number of buffers apart and loads run that many chunks ahead.
-template <int SDT>
+template <int MODE, int SDT>
 struct StreamGeom {
   static constexpr int kCC = 32, kChunks = kTileN / kCC;
   static constexpr int kState = SDT == kSFp32 ? 16384 : 8192;  // bytes of a chunk's m or v
   static constexpr int kOffS1 = 0, kOffS2 = kState, kOffW = 2 * kState;
-  static constexpr int kBuf = KCfg<kModeGrouped, kWBf16, SDT>::kEpiBuf;
-  static constexpr int NB = epi_bufs(kModeGrouped, SDT);
+  static constexpr int kBuf = KCfg<MODE, kWBf16, SDT>::kEpiBuf;
+  static constexpr int NB = epi_bufs(MODE, SDT);
   static_assert(kBuf >= kOffW + 8192, "m, v and 128 x 32 bf16 weights");
 };
 
 // Lane 0 of the I/O warp: loads NB chunks ahead; each finished chunk is stored
 // and, once the stores have read its buffer, the buffer loaded again.
-template <int KIND, int SDT>
+template <int KIND, int SDT, int MODE>
 __device__ void grouped_io_role(const CUtensorMap* mS1, const CUtensorMap* mS2, const CUtensorMap* mW,
                                 const GemmParams& p, SharedState* ss, uint8_t* epi, uint32_t rank) {
-  using G = StreamGeom<SDT>;
+  using G = StreamGeom<MODE, SDT>;
   constexpr int NB = G::NB;
   constexpr bool U1 = uses_s1(KIND), U2 = uses_s2(KIND);
   constexpr uint32_t kTx = (U1 ? G::kState : 0) + (U2 ? G::kState : 0) + 8192;
@@ -1735,10 +1745,10 @@ __device__ void grouped_io_role(const CUtensorMap* mS1, const CUtensorMap* mS2, 
     bounded_wait(&ss->epi_full[j % NB], static_cast<uint32_t>(j / NB) & 1u, p, ss, false);
 }
 
-template <int KIND, int SDT>
+template <int KIND, int SDT, int MODE>
 __device__ void grouped_compute_role(const GemmParams& p, SharedState* ss, uint8_t* epi, int warp, int lane,
                                      uint32_t rank) {
-  using G = StreamGeom<SDT>;
+  using G = StreamGeom<MODE, SDT>;
   constexpr int NB = G::NB;
   const int quarter = warp & 3, sub = (warp - 2) >> 2;  // TMEM lane quarter, column quarter
   const int r = quarter * 32 + lane;
@@ -1788,9 +1798,9 @@ __device__ __forceinline__ void epilogue_staged(const CUtensorMap* mS1, const CU
                                                 const GemmParams& p,
                                                 SharedState* ss, uint8_t* epi, int warp, int lane,
                                                 uint32_t rank) {
-  if constexpr (streamed(MODE, SDT)) {
-    if (warp != 2 + kNumEpiWarpsStaged) grouped_compute_role<KIND, SDT>(p, ss, epi, warp, lane, rank);
-    else if (lane == 0) grouped_io_role<KIND, SDT>(mS1, mS2, mW, p, ss, epi, rank);
+  if constexpr (streamed(MODE)) {
+    if (warp != 2 + kNumEpiWarpsStaged) grouped_compute_role<KIND, SDT, MODE>(p, ss, epi, warp, lane, rank);
+    else if (lane == 0) grouped_io_role<KIND, SDT, MODE>(mS1, mS2, mW, p, ss, epi, rank);
     return;
   }
   if (warp == 2 + kNumEpiWarpsStaged)
@@ -1891,7 +1901,7 @@ __global__ void __launch_bounds__(KCfg<MODE, WDT, SDT>::kThreads, 1)
 
   // A dependent launch (after the fp32-weight or the grouped dX kernel) ends only after that
   // grid, on every path (the epilogue's waits are skipped when a CTA aborts).
-  if (MODE == kModeFusedOpt || MODE == kModeGrouped) ptx::grid_dep_wait();
+  if (MODE == kModeFusedOpt || grouped(MODE)) ptx::grid_dep_wait();
   __syncwarp();  // the producer's and MMA thread's lanes rejoin their warps first
   ptx::tc_fence_before();
   __syncthreads();

@@ -223,6 +223,20 @@ def test_more_tiles_than_pairs():
     _step_case([40, 90, 0, 128], 1040, 1280, "fp32", "adamw")
 
 
+@pytest.mark.parametrize("s_dtype", ["fp32", "bf16", "int8"])
+@pytest.mark.parametrize("counts", [[1535], [1536], [3583], [3584], [5000, 900], [9001, 0, 1800]],
+                         ids=lambda c: "_".join(map(str, c)))
+def test_step_of_longer_groups(counts, s_dtype):
+    """Means on either side of each change of the kernel's layout (1536 and 3584 tokens), ragged ends."""
+    _step_case(counts, 136, 192, s_dtype, "adamw")
+
+
+@pytest.mark.parametrize("rule", ["lion", "rmsprop", "sgd", "sgd_momentum"])
+@pytest.mark.parametrize("tokens", [1700, 4000])
+def test_step_of_longer_groups_other_rules(rule, tokens):
+    _step_case([tokens], 264, 320, "fp32", rule)
+
+
 @pytest.mark.parametrize("s_dtype", ["fp32", "int8"])
 def test_one_group_steps_as_the_linear_step(s_dtype):
     # whole 64-token stages: a ragged last stage holds its rows after the zeros here, before them there, which
