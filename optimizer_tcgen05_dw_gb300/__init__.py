@@ -1,4 +1,6 @@
-"""FORGE tile-fused weight-gradient + optimizer step for GB300 (sm_103a).
+"""FORGE tile-fused weight-gradient + optimizer step for GB300 (sm_103a), and the
+operators around it: linears grouped by expert, the root-mean-square norm and
+the optimizer step over many tensors.
 
 The compute path is a C-ABI shared library of hand-written CUDA kernels
 (``include/forge.h``); this package holds its sources (``csrc/``), the build step

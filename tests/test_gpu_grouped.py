@@ -327,6 +327,33 @@ def test_side_stream_and_graph_replay_read_the_offsets_when_they_run():
     assert torch.equal(Y, ref)
 
 
+@pytest.mark.parametrize("s_dtype", ["fp32", "int8"])
+def test_the_captured_step_replays_with_its_dx(s_dtype):
+    """dX and the step that starts under its tail, replayed: the same bits as the direct calls, step after step."""
+    counts, N, K, hp = [300, 0, 70], 328 if s_dtype == "fp32" else 320, 384, dict(lr=1e-2, weight_decay=0.1)
+    T, off = sum(counts), _offsets(counts)
+    X, dY = inputs.normal((T, K), 1.0, 2, device="cuda"), inputs.normal((T, N), 1e-2, 3, device="cuda")
+
+    def fresh():
+        W = inputs.normal((3, N, K), 0.02, 1, device="cuda")
+        if s_dtype == "fp32":
+            return W, [torch.zeros((3, N, K), device="cuda") for _ in range(2)], _nan(T, K)
+        return W, [torch.zeros((3, N, K), dtype=torch.int8, device="cuda"), torch.zeros((3, N, K), dtype=torch.uint8, device="cuda"),
+                   torch.zeros((3, N, K // 64), device="cuda"), torch.zeros((3, N, K // 64), device="cuda")], _nan(T, K)
+
+    (Wa, sa, da), (Wb, sb, db) = fresh(), fresh()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        api.forge_grouped_bwd_step(X, dY, Wb, off, "adamw", hp, 1, 5, *sb, dX=db)
+    for _ in range(3):
+        api.forge_grouped_bwd_step(X, dY, Wa, off, "adamw", hp, 1, 5, *sa, dX=da)
+        graph.replay()
+        torch.cuda.synchronize()
+        for a, b in zip([Wa, da, *sa], [Wb, db, *sb]):
+            assert torch.equal(a, b)
+    api.forge_get_device_status()
+
+
 def test_a_wait_that_runs_out_is_reported():
     W, X = _grid((2, 64, 64), -3, 1), _grid((20, 64), 0, 2)
     Y, off = _nan(20, 64), _offsets([10, 10])

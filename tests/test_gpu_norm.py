@@ -205,6 +205,28 @@ def test_residual_stream_in_place_and_side_stream():
     assert torch.equal(over, h) and torch.equal(y2, y)
 
 
+def test_graph_replay_of_the_gradient_and_the_codes():
+    """Two launches (the second starts under the first's end) and a cleared maximum, replayed on new values."""
+    T, K = 320, 2048
+    x, dy, w = _inputs(T, K)
+    rstd, dx, dw = torch.empty(T, device="cuda"), _empty(T, K), _empty(K, dtype=torch.float32)
+    yt, amax = _empty(K, T, dtype=torch.float8_e4m3fn), _empty(1, dtype=torch.float32)
+    work = torch.empty(api.forge_rmsnorm_bwd_workspace(T, K), device="cuda")
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        api.forge_rmsnorm_fwd(x, w, EPS, rstd=rstd, yt=yt, yt_scale=0.125, amax=amax)
+        api.forge_rmsnorm_bwd(dy, x, w, rstd, dx, dw, work)
+    for scale in (1.0, 0.25):  # the second maximum is smaller: it must not keep the first
+        x.copy_(inputs.normal((T, K), 1.0, 77, device="cuda"))
+        w.copy_((w.float() * scale).bfloat16())
+        graph.replay()
+        got = [t.clone() for t in (rstd, yt.view(torch.uint8), amax, dx, dw)]
+        api.forge_rmsnorm_fwd(x, w, EPS, rstd=rstd, yt=yt, yt_scale=0.125, amax=amax)
+        api.forge_rmsnorm_bwd(dy, x, w, rstd, dx, dw, work)
+        for a, b in zip(got, (rstd, yt.view(torch.uint8), amax, dx, dw)):
+            assert torch.equal(a, b)
+
+
 def test_codes_feed_the_e4m3_step():
     """yt and its scale are what forge_linear_bwd_step_fp8 takes as X: the step's gradient is that of the dequantised y."""
     T, K, N = 64, 128, 256
