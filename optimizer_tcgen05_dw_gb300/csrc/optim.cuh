@@ -252,26 +252,15 @@ __device__ __forceinline__ int quant(float x, float a) {
   return static_cast<int>(q);
 }
 
-// quant<SIGNED>(x, a) with the block's step s = a/127 (or a/255) and its
-// reciprocal inv = RN(1/s) formed once per block: the same code, mostly
-// without the division.  y = RN(x * inv) = (x/s)(1 + e1)(1 + e2) with
-// |e1|, |e2| <= 2^-24, so |y - x/s| <= 2^-23 (1 + 2^-25) |x/s| < 1.6e-5 for
-// |x/s| <= 128, and RN(x/s) lies within 2^-24 * 128 < 7.7e-6 of x/s: y and
-// RN(x/s) round to the same integer unless a half-integer lies within
-// 2.4e-5 of y.  There (and whenever inv is not finite) the quotient is
-// formed exactly as in quant; elsewhere rint(y) is the code.
-template <bool SIGNED>
-__device__ __forceinline__ int quant_recip(float x, float a, float s, float inv) {
-  if (a == 0.f) return 0;
-  const float y = mul(x, inv);
-  const float fr = __fsub_rn(y, floorf(y));  // exact for |y| < 2^23
-  const float r = (fabsf(__fsub_rn(fr, 0.5f)) <= 3.0e-5f || !(fabsf(inv) <= 3.0e38f)) ? dvd(x, s) : y;
-  if (r != r) return 0;
-  float q = rintf(r);
-  q = fminf(fmaxf(q, SIGNED ? -127.f : 0.f), SIGNED ? 127.f : 255.f);
-  return static_cast<int>(q);
-}
-
+// quant<SIGNED>(x, a) mostly without the division: with the block's step s =
+// a/127 (or a/255) and its reciprocal inv = RN(1/s), formed once per block, the
+// code is rint(y), y = RN(x * inv), unless y lies next to a half-integer.
+// With u the spacing of floats at y (at most 2^-16): x * inv is within 0.996 u
+// of x/s (|e1| <= 2^-24 of at most 255), and RN(x/s) reaches a half-integer
+// only from within u/2 of it, so where the two would round apart y is at most
+// one u from it.  There (within 3e-5, which is more), and whenever inv is not
+// finite, the quotient is formed exactly as in quant.
+//
 // The fused epilogue's INT8 arithmetic, written to keep off the conversion
 // unit (int <-> float casts and floor/rint run there at a fraction of the FP32
 // rate); every function gives the same values as the definitions above.
@@ -287,7 +276,7 @@ __device__ __forceinline__ float code_f32(uint32_t word, int k) {
 
 // clamp(rint(y)) as an integer, NaN -> 0: adding 1.5 * 2^23 rounds any |y| <
 // 2^22 to an integer (nearest even) held in the low mantissa bits.  `near`
-// reports a y within 3e-5 of a half-integer (see quant_recip), where the
+// reports a y within 3e-5 of a half-integer (see above), where the
 // rounding of y and of the exact quotient may differ.  CLAMP = false is for
 // y = x * RN(1/s) with a finite reciprocal and |x| <= absmax: then s >=
 // 3.3e-39, whose relative spacing is below 5e-7, so |y| <= 127.0001 (255.0002

@@ -1021,7 +1021,7 @@ __device__ __forceinline__ void epi_chunk_int8(uint32_t taddr, uint8_t* buf, int
     }
     if (CMP) ptx::bar_sync(kEpiInnerBarrier, nthreads);  // read by all before weights return
   }
-  // New codes (dev::quant_recip's rule): round x * (1/s) with the shifter;
+  // New codes (see dev::code_round): round x * (1/s) with the shifter;
   // the few near a half-integer or not finite, and every code of a block
   // whose reciprocal is not finite, are redone from the exact quotient x / s
   // (a branch that is rarely taken).
