@@ -1756,10 +1756,12 @@ __device__ void grouped_compute_role(const GemmParams& p, SharedState* ss, uint8
   TileWalk<G::kChunks, true> walk;
   walk.init(p, rank);
   const uint32_t empty0 = ptx::mapa(ptx::smem_addr(&ss->tmem_empty[0]), 0);
-  // Lane 0 waits; the warp gets its verdict together.
+  // Lane 0 waits; the warp gets its verdict together, and what lane 0 saw is
+  // ordered before the other lanes' reads (the vote alone orders nothing).
   auto wait = [&](uint64_t* bar, uint32_t parity) -> bool {
-    const bool ok = lane != 0 || bounded_wait(bar, parity, p, ss);
-    return __all_sync(0xFFFFFFFFu, ok);
+    const bool ok = __all_sync(0xFFFFFFFFu, lane != 0 || bounded_wait(bar, parity, p, ss));
+    __syncwarp();
+    return ok;
   };
   for (int j = 0; j < walk.total; ++j) {
     const int c = j % G::kChunks, local = j / G::kChunks, acc = local & 1;
