@@ -311,7 +311,10 @@ __global__ void __launch_bounds__(kGThreads, 1)
 // lengthen its way), and add their sums in shared memory in warp order.
 // The instruction's k order is free as long as both operands agree: a lane
 // loads 16 contiguous bytes (eight k) of its row and of its token, and feeds
-// them to two instructions.
+// them to two instructions.  How far the loads run ahead (AHEAD) goes by how
+// many blocks have work: with more than two an SM, two turns (fewer registers,
+// more blocks an SM: 16 rows over 12 of 16 experts of 2048 x 4096 33 us, eight
+// turns 34, four 36, one 40), with fewer, eight (one row: 6.9 us, two turns 8.0).
 constexpr int kFewRows = 16, kFewWarps = 8, kFewTiles = 4;  // up to 4 x 8 tokens a pass
 
 __device__ __forceinline__ uint4 ld_once(const uint4* p) {
@@ -333,7 +336,7 @@ __device__ __forceinline__ void mma_16x8x16(float (&c)[4], uint32_t a0, uint32_t
 // Features f0 .. f0 + 15 (those below F) of tokens t0 .. t0 + 8 NT - 1 (those
 // below tend), by the whole block.  Rows and tokens past the end repeat the
 // last one; their results are not stored.
-template <int NT>
+template <int NT, int AHEAD>
 __device__ __forceinline__ void few_product(const uint16_t* W, const uint16_t* X, const GroupedParams& p, int f0, int t0,
                                             int tend, int K, float* s_sum) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, q = lane & 3;
@@ -349,7 +352,7 @@ __device__ __forceinline__ void few_product(const uint16_t* W, const uint16_t* X
     for (int j = 0; j < 4; ++j) acc[i][j] = 0.f;
   }
   const uint4 zero = make_uint4(0, 0, 0, 0);
-#pragma unroll 4
+#pragma unroll AHEAD
   for (int v = warp * 4 + q; v - q < V; v += kFewWarps * 4) {  // uniform over the warp
     const bool in = v < V;
     const uint4 a = in ? ld_once(w0 + v) : zero, b = in ? ld_once(w1 + v) : zero;
@@ -381,6 +384,7 @@ __device__ __forceinline__ void few_product(const uint16_t* W, const uint16_t* X
   __syncthreads();  // before the next pass overwrites the sums
 }
 
+template <int AHEAD>
 __global__ void __launch_bounds__(32 * kFewWarps) grouped_few_kernel(const uint16_t* W, const uint16_t* X,
                                                                      const GroupedParams p, const int K) {
   __shared__ float s_sum[kFewWarps * 8 * kFewTiles * kFewRows];
@@ -391,9 +395,9 @@ __global__ void __launch_bounds__(32 * kFewWarps) grouped_few_kernel(const uint1
     atomicCAS(p.status, 0u, static_cast<uint32_t>(kStatusInvalid));
   const uint16_t* We = W + static_cast<int64_t>(e) * p.F * K;
   for (int t0 = begin; t0 < end; t0 += 8 * kFewTiles) {
-    if (end - t0 <= 8) few_product<1>(We, X, p, f0, t0, end, K, s_sum);
-    else if (end - t0 <= 16) few_product<2>(We, X, p, f0, t0, end, K, s_sum);
-    else few_product<kFewTiles>(We, X, p, f0, t0, end, K, s_sum);
+    if (end - t0 <= 8) few_product<1, AHEAD>(We, X, p, f0, t0, end, K, s_sum);
+    else if (end - t0 <= 16) few_product<2, AHEAD>(We, X, p, f0, t0, end, K, s_sum);
+    else few_product<kFewTiles, AHEAD>(We, X, p, f0, t0, end, K, s_sum);
   }
   // rows of no group: before the first and after the last
   const int f = f0 + static_cast<int>(threadIdx.x);
@@ -428,9 +432,14 @@ cudaError_t run_grouped(const CUtensorMap& w, const GroupedMaps& m, const Groupe
 
 }  // namespace
 
-cudaError_t launch_grouped_few(const void* W, const void* X, const GroupedParams& p, int K, cudaStream_t s) {
+cudaError_t launch_grouped_few(const void* W, const void* X, const GroupedParams& p, int K, int num_sms,
+                               cudaStream_t s) {
   const dim3 grid(static_cast<unsigned>((p.F + kFewRows - 1) / kFewRows), static_cast<unsigned>(p.groups));
-  grouped_few_kernel<<<grid, 32 * kFewWarps, 0, s>>>(static_cast<const uint16_t*>(W), static_cast<const uint16_t*>(X), p, K);
+  const auto* w = static_cast<const uint16_t*>(W);
+  const auto* x = static_cast<const uint16_t*>(X);
+  const int live = p.groups < p.T ? p.groups : p.T;  // groups with rows, at most
+  if (static_cast<int64_t>(grid.x) * live > 2 * num_sms) grouped_few_kernel<2><<<grid, 32 * kFewWarps, 0, s>>>(w, x, p, K);
+  else grouped_few_kernel<8><<<grid, 32 * kFewWarps, 0, s>>>(w, x, p, K);
   return cudaGetLastError();
 }
 

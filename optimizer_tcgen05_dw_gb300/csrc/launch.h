@@ -99,10 +99,11 @@ cudaError_t launch_grouped(bool dgrad, const CUtensorMap& w, const CUtensorMap (
                            const GroupedParams& p, int grid, cudaStream_t s);
 // grouped.cu: the forward product of at most kFewMaxT token rows (K: reduction
 // length).  Against the tensor-core tiles, us for experts of 2048 x 4096: one
-// row 7.5 and 21; 32 rows of one expert 19 and 22, over 16 experts 46 and 49;
+// row 7 and 21; 32 rows of one expert 20 to 22 and 22, over 16 experts 43 and 49;
 // 64 rows of one expert (read twice here) 37 and 22, over 16 experts 46 and 50.
 constexpr int64_t kFewMaxT = 32;
-cudaError_t launch_grouped_few(const void* W, const void* X, const GroupedParams& p, int K, cudaStream_t s);
+cudaError_t launch_grouped_few(const void* W, const void* X, const GroupedParams& p, int K, int num_sms,
+                               cudaStream_t s);
 
 // One tensor of a many-tensor optimizer step.
 struct MultiItem {

@@ -86,7 +86,7 @@ forge_status_t grouped_product(const forge_grouped_t* g, const void* W, bool dgr
   p.status = d.status;
   p.skip_loads = skip_loads() ? 1 : 0;
   if (!dgrad && g->T <= kFewMaxT && p.skip_loads == 0) {  // (that hook is for the pipelined kernels' waits)
-    if ((e = launch_grouped_few(W, tok, p, static_cast<int>(R), s)) != cudaSuccess)
+    if ((e = launch_grouped_few(W, tok, p, static_cast<int>(R), d.num_sms, s)) != cudaSuccess)
       return cuda_fail(e, "grouped product launch");
     return FORGE_OK;
   }
