@@ -117,13 +117,13 @@ __device__ __forceinline__ float inv_rms(float sum, int K, float eps) {
 // A block takes rows blockIdx.x, blockIdx.x + gridDim.x, ...; thread i holds
 // vectors i, i + blockDim.x, .. (NV of them, eight columns each) of the row;
 // the weight comes from L1.  What keeps memory busy is rows in flight, so many
-// rows run on few threads each (one warp up to K = 2560: no barrier) and the
+// rows run on few threads each (one warp up to K = 2048: no barrier) and the
 // blocks of an SM are at different points of theirs; few rows run on many
 // threads each, for the shortest time to one.  Sum and maximum are reduced
 // together: one barrier a row, the partials in alternating halves of `red`.
 // The row is kept as the products h w, so that the output is one factor away.
 template <int NV, bool RES, bool MANY>
-__global__ void __launch_bounds__(MANY ? 256 : 512, MANY ? 2 : 1) norm_fwd_kernel(const NormParams p) {
+__global__ void __launch_bounds__(MANY ? 256 : 512, MANY ? (NV >= 8 ? 2 : NV >= 6 ? 3 : 4) : 1) norm_fwd_kernel(const NormParams p) {
   __shared__ float red[2][2][16];  // [row parity][sum, max][warp]
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, warps = blockDim.x >> 5;
   const int V = p.K >> 3;
@@ -567,15 +567,15 @@ cudaError_t launch_norm_fwd(const NormParams& p0, int num_sms, cudaStream_t s) {
       else run_fwd<4, false>(p, grid, threads, s);
     } else {
       int warps = 1;
-      while (V > 32 * 10 * warps) warps *= 2;
+      while (V > 32 * 8 * warps) warps *= 2;
       const int nv = (V + 32 * warps - 1) / (32 * warps);
       const int grid = static_cast<int>(least(p.T, static_cast<int64_t>(num_sms) * (32 / warps)));
       if (nv <= 1) run_fwd<1, true>(p, grid, 32 * warps, s);
       else if (nv <= 2) run_fwd<2, true>(p, grid, 32 * warps, s);
       else if (nv <= 4) run_fwd<4, true>(p, grid, 32 * warps, s);
+      else if (nv <= 5) run_fwd<5, true>(p, grid, 32 * warps, s);
       else if (nv <= 6) run_fwd<6, true>(p, grid, 32 * warps, s);
-      else if (nv <= 8) run_fwd<8, true>(p, grid, 32 * warps, s);
-      else run_fwd<10, true>(p, grid, 32 * warps, s);
+      else run_fwd<8, true>(p, grid, 32 * warps, s);
     }
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
     if (p.res != nullptr) p.x = p.h;  // for the codes below
