@@ -243,9 +243,10 @@ __device__ __forceinline__ void cluster_store2(const void* dst, uint64_t* bar, u
 
 // The blocks of a cluster hand their rows' shares to each other with counted
 // stores: a cluster barrier would have to wait for the h just written to
-// reach L2 as well.
-template <bool RES>
-__global__ void __launch_bounds__(256, 3) norm_fwd_t_kernel(const NormParams p, const int cluster, const int seg) {
+// reach L2 as well.  (The one barrier, that the others' mbarriers exist, is
+// entered before the loads and left after them.)
+template <bool RES, int WARPS>
+__global__ void __launch_bounds__(32 * WARPS, WARPS == 4 ? 5 : 3) norm_fwd_t_kernel(const NormParams p, const int cluster, const int seg) {
   extern __shared__ __align__(16) uint4 s_h[];  // [rows][seg / 8]
   __shared__ __align__(8) float2 s_part[8][kTransTokens];  // [block of the cluster][row]: sum, max
   __shared__ float s_rstd[kTransTokens];
@@ -263,56 +264,64 @@ __global__ void __launch_bounds__(256, 3) norm_fwd_t_kernel(const NormParams p, 
     ptx::fence_mbar_init();
     ptx::mbar_arrive_expect_tx(&s_bar, static_cast<uint32_t>(cluster * rows * 8));
   }
-  ptx::cluster_sync();  // every block's barrier is there
+  asm volatile("barrier.cluster.arrive.release;" ::: "memory");  // this block's barrier is there
   const uint4* w = static_cast<const uint4*>(p.w) + v0;
   const bool want_max = p.amax != nullptr;
-  // rows warp, warp + 8, ..: of 16 tokens, the last two repeat the first two and are not kept
-  const int64_t at = (t0 + warp) * V + v0;
-  const uint4* x = static_cast<const uint4*>(p.x) + at;
-  const uint4* res = static_cast<const uint4*>(p.res) + at;
-  uint4* ho = static_cast<uint4*>(p.h) + at;
-  f2 sums[kRows];
-  float top[kRows];
-#pragma unroll
-  for (int i = 0; i < kRows; ++i) {
-    sums[i] = both(0.f);
-    top[i] = 0.f;
-  }
-  const int step = rows == kTransTokens ? 8 * V : 0;  // to the third and fourth row
-  for (int v = lane; v < mine; v += 32) {
-    uint4 h[kRows], q[kRows];
-#pragma unroll
-    for (int i = 0; i < kRows; ++i) h[i] = x[v + (i & 1) * 8 * V + (i >> 1) * 2 * step];
-    if (RES) {
-#pragma unroll
-      for (int i = 0; i < kRows; ++i) q[i] = res[v + (i & 1) * 8 * V + (i >> 1) * 2 * step];
-    }
-    f2 g[4];
-    if (want_max) unpack8(w[v], g);
+  // A warp's rows, four at a time: warp, warp + WARPS, ..  Of 16 tokens,
+  // those past the last repeat an earlier row and are not kept.
+  bool met = false;
+  for (int first = warp; first < rows; first += kRows * WARPS) {
+    const int64_t at = (t0 + first) * V + v0;
+    const uint4* x = static_cast<const uint4*>(p.x) + at;
+    const uint4* res = static_cast<const uint4*>(p.res) + at;
+    uint4* ho = static_cast<uint4*>(p.h) + at;
+    f2 sums[kRows];
+    float top[kRows];
+    int step[kRows];
 #pragma unroll
     for (int i = 0; i < kRows; ++i) {
-      const int r = warp + 8 * i;
-      if (RES) h[i] = add_bf16x8(h[i], q[i]);
-      if (r < rows) {
-        if (RES) ho[v + 8 * i * V] = h[i];
-        s_h[r * SV + v] = h[i];
-      }
-      f2 f[4];
-      unpack8(h[i], f);
+      sums[i] = both(0.f);
+      top[i] = 0.f;
+      step[i] = first + i * WARPS < rows ? i * WARPS * V : 0;
+    }
+    for (int v = lane; v < mine; v += 32) {
+      uint4 h[kRows], q[kRows];
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        sums[i] = fma2(f[j], f[j], sums[i]);
-        f[j] = mul2(f[j], g[j]);
+      for (int i = 0; i < kRows; ++i) h[i] = x[v + step[i]];
+      if (RES) {
+#pragma unroll
+        for (int i = 0; i < kRows; ++i) q[i] = res[v + step[i]];
       }
-      if (want_max) top[i] = max_abs(top[i], f);
+      f2 g[4];
+      unpack8(want_max ? w[v] : make_uint4(0, 0, 0, 0), g);
+#pragma unroll
+      for (int i = 0; i < kRows; ++i) {
+        const int r = first + i * WARPS;
+        if (RES) h[i] = add_bf16x8(h[i], q[i]);
+        if (r < rows) {
+          if (RES) ho[v + step[i]] = h[i];
+          s_h[r * SV + v] = h[i];
+        }
+        f2 f[4];
+        unpack8(h[i], f);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          sums[i] = fma2(f[j], f[j], sums[i]);
+          f[j] = mul2(f[j], g[j]);
+        }
+        if (want_max) top[i] = max_abs(top[i], f);
+      }
+    }
+    if (!met) asm volatile("barrier.cluster.wait.acquire;" ::: "memory");  // every block's barrier is there
+    met = true;
+#pragma unroll
+    for (int i = 0; i < kRows; ++i) {
+      const int r = first + i * WARPS;
+      const float sum = warp_sum(sum2(sums[i])), most = want_max ? warp_max(top[i]) : 0.f;
+      if (r < rows && lane < cluster) cluster_store2(&s_part[rank][r], &s_bar, lane, sum, most);
     }
   }
-#pragma unroll
-  for (int i = 0; i < kRows; ++i) {
-    const int r = warp + 8 * i;
-    const float sum = warp_sum(sum2(sums[i])), most = want_max ? warp_max(top[i]) : 0.f;
-    if (r < rows && lane < cluster) cluster_store2(&s_part[rank][r], &s_bar, lane, sum, most);
-  }
+  if (!met) asm volatile("barrier.cluster.wait.acquire;" ::: "memory");
   __syncthreads();  // s_h is whole
   if (tid < rows) {
     // landed from every block (each try waits up to a millisecond)
@@ -345,7 +354,7 @@ __global__ void __launch_bounds__(256, 3) norm_fwd_t_kernel(const NormParams p, 
   const uint32_t* w2 = reinterpret_cast<const uint32_t*>(w);
   uint8_t* out = static_cast<uint8_t*>(p.qt) + static_cast<int64_t>(v0) * 8 * p.T + t0;
   const bool whole = p.T % 32 == 0 && (reinterpret_cast<uintptr_t>(p.qt) & 31u) == 0;
-  for (int c = tid; c < mine * 4; c += 256) {
+  for (int c = tid; c < mine * 4; c += 32 * WARPS) {
     const f2 wp = pair(dev::bf16_to_f32(w2[c]), __uint_as_float(w2[c] & 0xFFFF0000u));
     uint8_t* to = out + static_cast<int64_t>(2 * c) * p.T;
     uint32_t o0[8], o1[8];
@@ -524,12 +533,15 @@ cudaError_t run_fwd_t(const NormParams& p, cudaStream_t s) {
   while (cluster < 8 && V > 64 * cluster) cluster *= 2;
   const int seg = (V + cluster - 1) / cluster * 8;
   const int smem = kTransTokens * seg * 2;
-  auto* k = norm_fwd_t_kernel<RES>;
+  // Five blocks of four warps an SM overlap their passes better than three of
+  // eight (16384 x 4096: 88 and 94 us) as long as their memory lets five in.
+  const bool small = smem <= 40960;
+  auto* k = small ? norm_fwd_t_kernel<RES, 4> : norm_fwd_t_kernel<RES, 8>;
   cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, kTransSmem);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>((p.T + kTransTokens - 1) / kTransTokens * cluster), 1, 1);
-  cfg.blockDim = dim3(256, 1, 1);
+  cfg.blockDim = dim3(small ? 128 : 256, 1, 1);
   cfg.dynamicSmemBytes = static_cast<size_t>(smem);
   cfg.stream = s;
   cudaLaunchAttribute attr[1];

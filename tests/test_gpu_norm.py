@@ -85,7 +85,7 @@ def test_forward_bf16_and_token_codes(T, K, residual):
 
 
 @pytest.mark.parametrize("residual", [False, True])
-@pytest.mark.parametrize("T,K", [(16, 8), (16, 4096), (48, 520), (160, 5120), (1296, 2048), (32, 16384)])
+@pytest.mark.parametrize("T,K", [(16, 8), (16, 4096), (48, 520), (160, 5120), (1296, 2048), (32, 16384), (112, 5128), (80, 8192), (48, 136)])
 def test_forward_token_contiguous_codes(T, K, residual):
     x, res, w = _inputs(T, K)
     h, qt, y = _empty(T, K), _empty(K, T, dtype=torch.float8_e4m3fn), _empty(T, K)
