@@ -246,12 +246,12 @@ __device__ __forceinline__ void cluster_store2(const void* dst, uint64_t* bar, u
 // reach L2 as well.  (The one barrier, that the others' mbarriers exist, is
 // entered before the loads and left after them.)
 template <bool RES, int WARPS>
-__global__ void __launch_bounds__(32 * WARPS, WARPS == 4 ? 5 : 3) norm_fwd_t_kernel(const NormParams p, const int cluster, const int seg) {
+__global__ void __launch_bounds__(32 * WARPS, WARPS == 4 ? 5 : WARPS == 8 ? 3 : 1) norm_fwd_t_kernel(const NormParams p, const int cluster, const int seg) {
   extern __shared__ __align__(16) uint4 s_h[];  // [rows][seg / 8]
   __shared__ __align__(8) float2 s_part[8][kTransTokens];  // [block of the cluster][row]: sum, max
   __shared__ float s_rstd[kTransTokens];
   __shared__ __align__(8) uint64_t s_bar;
-  constexpr int kRows = 4;  // rows of a warp loaded together
+  constexpr int kRows = WARPS == 16 ? 2 : 4;  // rows of a warp loaded together
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int V = p.K >> 3, SV = seg >> 3;
   const int rank = static_cast<int>(ptx::cluster_ctarank());
@@ -534,14 +534,15 @@ cudaError_t run_fwd_t(const NormParams& p, cudaStream_t s) {
   const int seg = (V + cluster - 1) / cluster * 8;
   const int smem = kTransTokens * seg * 2;
   // Five blocks of four warps an SM overlap their passes better than three of
-  // eight (16384 x 4096: 88 and 94 us) as long as their memory lets five in.
-  const bool small = smem <= 40960;
-  auto* k = small ? norm_fwd_t_kernel<RES, 4> : norm_fwd_t_kernel<RES, 8>;
+  // eight (16384 x 4096: 88 and 94 us) as long as their memory lets five in;
+  // where it lets one in (K > 8192), sixteen warps (2048 x 16384: 74 and 84).
+  const int warps = smem <= 40960 ? 4 : (smem <= 65536 ? 8 : 16);
+  auto* k = warps == 4 ? norm_fwd_t_kernel<RES, 4> : (warps == 8 ? norm_fwd_t_kernel<RES, 8> : norm_fwd_t_kernel<RES, 16>);
   cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, kTransSmem);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>((p.T + kTransTokens - 1) / kTransTokens * cluster), 1, 1);
-  cfg.blockDim = dim3(small ? 128 : 256, 1, 1);
+  cfg.blockDim = dim3(static_cast<unsigned>(32 * warps), 1, 1);
   cfg.dynamicSmemBytes = static_cast<size_t>(smem);
   cfg.stream = s;
   cudaLaunchAttribute attr[1];
