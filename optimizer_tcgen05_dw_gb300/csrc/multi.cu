@@ -196,8 +196,9 @@ void run_multi_cap(const MultiParams<kMultiLong>& p, uint32_t tiles, cudaStream_
   multi_opt_kernel<WDT, SDT, GDT, CAP><<<tiles, kMultiThreads, 0, s>>>(q);
 }
 
-// A launch costs host time for its parameters' bytes (30 KB about 3 us more
-// than 4 KB), so a table goes in the shortest of three forms that holds it.
+// A launch costs host time for its parameters' bytes, so a table goes in the
+// shortest of three forms that holds it (81 small tensors, a pass with the
+// host's part: 7.2 us in 140 entries, 7.9 in 480).
 template <int WDT, int SDT, int GDT>
 cudaError_t run_multi(const MultiParams<kMultiLong>& p, uint32_t tiles, cudaStream_t s) {
   if (p.count <= kMultiShort) run_multi_cap<WDT, SDT, GDT, kMultiShort>(p, tiles, s);
