@@ -32,7 +32,9 @@ __device__ __forceinline__ float group_max(float a, int lanes) {
 // Codes are formed and read without the conversion unit (int <-> float casts
 // and rint run there at a quarter of the float rate): code_f32, and
 // code_round_fast with all eight redone from the exact quotient when one lies
-// near a half-integer or is not finite.  The values are dequant's and quant's.
+// near a half-integer or is not finite.  The values are dequant's and quant's
+// for any v that `a` is the absmax of: an unsigned code clamps at 0 itself (a
+// quantiser's caller may give negative values, a second moment has none).
 template <bool SIGNED>
 __device__ __forceinline__ void decode8(uint2 c, float a, float (&v)[8]) {
   const float s = dev::dvd(a, SIGNED ? 127.f : 255.f);
@@ -49,7 +51,8 @@ __device__ __forceinline__ uint2 encode8(const float (&v)[8], float a) {
 #pragma unroll
   for (int j = 0; j < 8; ++j) {
     bool redo;
-    k[j] = dev::code_round_fast<SIGNED>(dev::mul(v[j], inv), redo);
+    const float y = dev::mul(v[j], inv);
+    k[j] = dev::code_round_fast<SIGNED>(SIGNED ? y : fmaxf(y, 0.f), redo);  // a NaN's code is 0 too
     any |= redo;
   }
   if (any) {

@@ -162,3 +162,24 @@ def test_int8_blocks_realistic_interval(T, qb):
     prob = Problem(T=T, N=256, K=512, w_dtype="bf16", s_dtype="int8", opt_name="adamw",
                    hp=_hp("adamw"), steps=2, seed=81 + qb, qblock=qb)
     prob.per_step_from_common_state()
+
+
+@pytest.mark.parametrize("qb", BLOCKS + [64])
+@pytest.mark.parametrize("signed", [True, False])
+def test_quantiser_of_any_values(signed, qb):
+    """Either sign in both codes (the unsigned one gives 0 to a negative value,
+    whatever its neighbours are), values that are not finite, tiny blocks."""
+    rows, cols = 64, 1024
+    x = inputs.normal((rows, cols), 1e-3, 171 + qb, torch.float32)
+    steps = torch.arange(cols, dtype=torch.float32) % 512 - 255  # x / s of -255 .. 256, halves on odd rows
+    x[0], x[1], x[2] = steps / 256, (steps + 0.5) / 256, -steps.abs()
+    x[3], x[4] = x[3] * 2.0 ** -130, x[4] * 2.0 ** -139  # blocks whose step is denormal, its reciprocal infinite
+    x[5, ::7], x[6, ::9], x[7, ::11] = float("nan"), float("inf"), float("-inf")
+    x[8] = float("nan")
+    codes = torch.empty((rows, cols), dtype=torch.int8 if signed else torch.uint8, device="cuda")
+    amax = torch.empty((rows, cols // qb), dtype=torch.float32, device="cuda")
+    api.forge_quantize_state(x.cuda(), codes, amax, signed, block=qb)
+    api.forge_get_device_status()
+    rc, ra = quant.quantize_blocks(x.numpy(), signed=signed, block=qb)
+    assert_bitexact(codes, rc, "codes")
+    assert_bitexact(amax, ra, "absmax")
