@@ -420,13 +420,14 @@ FORGE_API int64_t forge_rmsnorm_bwd_workspace(int64_t T, int64_t K);
 FORGE_API forge_status_t forge_get_device_status(void* stream);
 
 /* Bound, in nanoseconds, on every pipeline wait inside the tensor-core
- * kernels (default 2e9).  When a wait expires the kernel records
- * FORGE_ERR_TIMEOUT, stops issuing work, releases its tensor memory and
- * returns.  0 restores the default.  Applies to later launches. */
+ * kernels and on the wait of the token-contiguous norm for its cluster
+ * (default 2e9).  When a wait expires the kernel records FORGE_ERR_TIMEOUT,
+ * stops issuing work, releases its tensor memory and returns.  0 restores the default.  Applies to later launches. */
 FORGE_API forge_status_t forge_set_wait_limit_ns(uint64_t ns);
 
 /* Test hook for the failure path: while nonzero, the tensor-core kernels'
- * load-issuing warp issues nothing, so the consumers' bounded waits expire.
+ * load-issuing warp issues nothing (and the token-contiguous norm sends its
+ * cluster nothing), so the consumers' bounded waits expire.
  * Never set it outside tests. */
 FORGE_API forge_status_t forge_debug_skip_loads(int32_t enable);
 

@@ -152,8 +152,9 @@ struct NormParams {
   int32_t K;
   float eps;
   float inv_scale;       // qt: 1 / its scale
-  int32_t wait_tries;    // qt: milliseconds a block waits for its cluster's
+  uint64_t wait_limit_ns;  // qt: how long a block waits for its cluster's
   uint32_t* status;      // device status word
+  int32_t skip_sends;    // qt: the test hook of the failure path
 };
 cudaError_t launch_norm_fwd(const NormParams& p, int num_sms, cudaStream_t s);
 cudaError_t launch_norm_bwd(const NormParams& p, int num_sms, cudaStream_t s);

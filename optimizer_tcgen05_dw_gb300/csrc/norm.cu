@@ -241,10 +241,23 @@ __device__ __forceinline__ void cluster_store2(const void* dst, uint64_t* bar, u
       : "memory");
 }
 
+// Until the mbarrier's first phase completes (true) or the limit passes.
+__device__ __forceinline__ bool shares_landed(uint64_t* bar, uint64_t limit_ns) {
+  if (ptx::mbar_try_wait(bar, 0u)) return true;
+  const uint64_t t0 = ptx::global_timer_ns();
+  while (!ptx::mbar_try_wait(bar, 0u))
+    if (ptx::global_timer_ns() - t0 > limit_ns) return false;
+  return true;
+}
+
 // The blocks of a cluster hand their rows' shares to each other with counted
 // stores: a cluster barrier would have to wait for the h just written to
-// reach L2 as well.  (The one barrier, that the others' mbarriers exist, is
-// entered before the loads and left after them.)
+// reach L2 as well.  Two barriers of the cluster stand around them, neither of
+// which waits for memory: that every block's mbarrier exists (entered before
+// the loads, left after them), and that every block has sent its shares
+// (entered then, left at the end).  A block whose shares did not land within
+// the limit writes nothing more and leaves only after the second barrier and
+// another bounded wait for them, so that none comes to a block that is gone.
 template <bool RES, int WARPS>
 __global__ void __launch_bounds__(32 * WARPS, WARPS == 4 ? 5 : WARPS == 8 ? 3 : 1) norm_fwd_t_kernel(const NormParams p, const int cluster, const int seg) {
   extern __shared__ __align__(16) uint4 s_h[];  // [rows][seg / 8]
@@ -318,20 +331,19 @@ __global__ void __launch_bounds__(32 * WARPS, WARPS == 4 ? 5 : WARPS == 8 ? 3 : 
     for (int i = 0; i < kRows; ++i) {
       const int r = first + i * WARPS;
       const float sum = warp_sum(sum2(sums[i])), most = want_max ? warp_max(top[i]) : 0.f;
-      if (r < rows && lane < cluster) cluster_store2(&s_part[rank][r], &s_bar, lane, sum, most);
+      if (r < rows && lane < cluster && !p.skip_sends) cluster_store2(&s_part[rank][r], &s_bar, lane, sum, most);
     }
   }
   if (!met) asm volatile("barrier.cluster.wait.acquire;" ::: "memory");
-  __syncthreads();  // s_h is whole
+  asm volatile("barrier.cluster.arrive.relaxed;" ::: "memory");  // this thread's shares are sent
+  const bool landed = tid >= rows || shares_landed(&s_bar, p.wait_limit_ns);
+  if (__syncthreads_or(!landed)) {  // (else s_h is whole as well)
+    if (!landed) atomicCAS(p.status, 0u, static_cast<uint32_t>(kStatusTimeout));
+    asm volatile("barrier.cluster.wait.acquire;" ::: "memory");
+    shares_landed(&s_bar, p.wait_limit_ns);
+    return;
+  }
   if (tid < rows) {
-    // landed from every block (each try waits up to a millisecond)
-    int tries = 0;
-    while (!ptx::mbar_try_wait(&s_bar, 0u)) {
-      if (++tries > p.wait_tries) {
-        atomicCAS(p.status, 0u, static_cast<uint32_t>(kStatusTimeout));
-        break;
-      }
-    }
     float sum = 0.f, most = 0.f;
     for (int c = 0; c < cluster; ++c) {  // the same order in each block
       sum += s_part[c][tid].x;
@@ -383,6 +395,7 @@ __global__ void __launch_bounds__(32 * WARPS, WARPS == 4 ? 5 : WARPS == 8 ? 3 : 
         }
     }
   }
+  asm volatile("barrier.cluster.wait.acquire;" ::: "memory");
 }
 
 // ---------------------------------------------------------------- gradient

@@ -352,8 +352,9 @@ forge_status_t forge_rmsnorm_fwd(const forge_rmsnorm_t* n, void* stream) {
   p.q = n->yq; p.q_scale = n->yq_scale; p.qt = n->yt; p.amax = n->amax;
   p.T = n->T; p.K = static_cast<int32_t>(n->K); p.eps = n->eps;
   p.inv_scale = n->yt != nullptr ? 1.f / n->yt_scale : 1.f;
-  p.wait_tries = static_cast<int32_t>(wait_limit_ns() / 1000000u < 100000u ? wait_limit_ns() / 1000000u + 1u : 100000u);
+  p.wait_limit_ns = wait_limit_ns();
   p.status = d.status;
+  p.skip_sends = skip_loads() ? 1 : 0;
   if ((e = launch_norm_fwd(p, d.num_sms, s)) != cudaSuccess) return cuda_fail(e, "norm launch");
   // without a residual h is x itself
   if (n->residual == nullptr && n->h != nullptr && n->h != n->x &&
