@@ -243,9 +243,9 @@ __device__ __forceinline__ void cluster_store2(const void* dst, uint64_t* bar, u
 
 // Until the mbarrier's first phase completes (true) or the limit passes.
 __device__ __forceinline__ bool shares_landed(uint64_t* bar, uint64_t limit_ns) {
-  if (ptx::mbar_try_wait(bar, 0u)) return true;
+  if (ptx::mbar_try_wait_cluster(bar, 0u)) return true;
   const uint64_t t0 = ptx::global_timer_ns();
-  while (!ptx::mbar_try_wait(bar, 0u))
+  while (!ptx::mbar_try_wait_cluster(bar, 0u))
     if (ptx::global_timer_ns() - t0 > limit_ns) return false;
   return true;
 }

@@ -68,6 +68,20 @@ __device__ __forceinline__ bool mbar_try_wait(uint64_t* bar, uint32_t parity) {
   return ok != 0;
 }
 
+// The same for a phase that other blocks of the cluster complete with counted
+// stores to this block's shared memory: their data is acquired at that scope.
+__device__ __forceinline__ bool mbar_try_wait_cluster(uint64_t* bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2, %3;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(smem_addr(bar)), "r"(parity), "n"(kWaitSuspendNs)
+      : "memory");
+  return ok != 0;
+}
+
 // ---------------------------------------------------------------- grid-wide counters
 
 // Add to a counter in global memory, ordered after this thread's earlier
