@@ -460,8 +460,9 @@ __global__ void __launch_bounds__(MAXT, MINB) norm_bwd_kernel(const NormParams p
       for (int i = 0; i < warps; ++i) dot += red[par][i];
       par ^= 1;
     }
-    // dx = rs (g - n mean) + dh = rs g - (rs^2 mean) h + dh
-    const f2 back = both(-(r.rs * r.rs) * __fdiv_rn(dot, static_cast<float>(p.K)));
+    // dx = rs (g - n mean) + dh, n mean = h (rs mean): rs itself may be past the
+    // root of the largest float (a tiny row without eps), n is near one
+    const f2 back = both(-r.rs * __fdiv_rn(dot, static_cast<float>(p.K)));
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       const int v = tid + i * blockDim.x;
@@ -470,7 +471,10 @@ __global__ void __launch_bounds__(MAXT, MINB) norm_bwd_kernel(const NormParams p
       unpack8(r.h[i], b);
       if (DH) unpack8(r.dh[i], d);
 #pragma unroll
-      for (int j = 0; j < 4; ++j) b[j] = fma2(g[i][j], r2, DH ? fma2(b[j], back, d[j]) : mul2(b[j], back));
+      for (int j = 0; j < 4; ++j) {
+        const f2 inner = fma2(b[j], back, g[i][j]);
+        b[j] = DH ? fma2(inner, r2, d[j]) : mul2(inner, r2);
+      }
       static_cast<uint4*>(p.y)[t * V + v] = pack8(b);
     }
   };

@@ -61,3 +61,31 @@ def test_a_wait_for_the_cluster_that_runs_out_is_reported():
     api.forge_get_device_status()
     assert torch.equal(a["h"], b["h"]) and torch.isfinite(a["yt"].float()).all() and a["amax"] > 1
     assert torch.allclose(a["rstd"], b["rstd"], rtol=1e-5)
+
+
+def _gradient(dy, h, w, rstd, dh=None):
+    T, K = h.shape
+    dx, dw = _nan(T, K), _nan(K, dtype=torch.float32)
+    api.forge_rmsnorm_bwd(dy, h, w, rstd, dx, dw, _nan(api.forge_rmsnorm_bwd_workspace(T, K), dtype=torch.float32), dh=dh)
+    return dx, dw
+
+
+@pytest.mark.parametrize("stream_grad", [False, True])
+@pytest.mark.parametrize("T,K", [(9, 512), (9, 4104), (9, 9000)])
+def test_gradient_of_rows_far_from_one(T, K, stream_grad):
+    """rstd of 2^66 has no square in float32, dx is 2^66 times an ordinary number and has its value."""
+    h, dh, w = _inputs(T, K)
+    dy = inputs.normal((T, K), 1e-2, 21, device="cuda")
+    for t, e in enumerate((-66, -60, -40, 0, 40, 60)):
+        h[t] *= 2.0 ** e
+    dh = dh if stream_grad else None
+    rstd = h.double().square().mean(1).rsqrt().float()
+    dx, _ = _gradient(dy, h, w, rstd, dh)
+    r = rstd.double()[:, None]
+    n, g = h.double() * r, dy.double() * w.double()
+    ref = r * (g - n * (g * n).mean(1, keepdim=True))
+    size = r * (g.abs() + n.abs() * (g * n).abs().mean(1, keepdim=True))
+    if stream_grad:
+        ref, size = ref + dh.double(), size + dh.double().abs()
+    assert torch.isfinite(dx).all()
+    assert ((dx.double() - ref).abs() <= ref.abs() * 2.0 ** -8 + 2 * (_steps(K) + 8) * U * size + 1e-38).all()
