@@ -190,20 +190,39 @@ __global__ void __launch_bounds__(MANY ? 256 : 512, MANY ? (NV >= 8 ? 2 : NV >= 
     if (tid == 0 && p.rstd != nullptr) p.rstd[t] = rstd;
     // A token's codes: scale = max|y| / 448 (0 and zero codes for a zero row;
     // NaN, and NaN codes, when the row holds a value that is not finite).
+    // Near the smallest floats the scale is a denormal of few bits and its
+    // reciprocal past the largest float: there the codes are of the stored scale,
+    // it and the row (once y is out) brought up by the same power of two.
     float inv = 0.f;
+    bool to_y = p.y != nullptr;
     if (want_max) {
-      const float amax = top * rstd;
-      inv = amax == 0.f ? 0.f : fminf(__fdiv_rn(kE4M3Max, amax), 3.4e38f) + (amax - amax);
-      if (tid == 0) p.q_scale[t] = __fdiv_rn(amax, kE4M3Max);
+      const float amax = top * rstd, scale = __fdiv_rn(amax, kE4M3Max);
+      if (tid == 0) p.q_scale[t] = scale;
+      inv = __fdiv_rn(kE4M3Max, amax) + (amax - amax);
+      if (scale < 0x1p-120f) {
+        inv = scale > 0.f ? __fdiv_rn(1.f, scale * 0x1p100f) : 0.f;
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+          const int v = tid + i * blockDim.x;
+          f2 y[4];
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            y[j] = mul2(hw[i][j], both(rstd));
+            hw[i][j] = mul2(hw[i][j], both(0x1p100f));
+          }
+          if (to_y && v < V) static_cast<uint4*>(p.y)[t * V + v] = pack8(y);
+        }
+        to_y = false;
+      }
     }
-    if (p.y == nullptr && !want_max) continue;
+    if (!to_y && !want_max) continue;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       const int v = tid + i * blockDim.x;
       if (v >= V) continue;
 #pragma unroll
       for (int j = 0; j < 4; ++j) hw[i][j] = mul2(hw[i][j], both(rstd));
-      if (p.y != nullptr) static_cast<uint4*>(p.y)[t * V + v] = pack8(hw[i]);
+      if (to_y) static_cast<uint4*>(p.y)[t * V + v] = pack8(hw[i]);
       if (want_max) {
 #pragma unroll
         for (int j = 0; j < 4; ++j) hw[i][j] = mul2(hw[i][j], both(inv));

@@ -89,3 +89,30 @@ def test_gradient_of_rows_far_from_one(T, K, stream_grad):
         ref, size = ref + dh.double(), size + dh.double().abs()
     assert torch.isfinite(dx).all()
     assert ((dx.double() - ref).abs() <= ref.abs() * 2.0 ** -8 + 2 * (_steps(K) + 8) * U * size + 1e-38).all()
+
+
+@pytest.mark.parametrize("T,K", [(3, 264), (700, 128), (64, 8200)])
+def test_codes_of_tiny_rows_are_those_of_the_stored_scale(T, K):
+    """y near 2^-126: 448 / max|y| is past the largest float, max|y| / 448 a denormal; code * scale is y all the same.
+    A product's denormal rounding is 2^-150, far below a code's 2^-10 of the scale (2^-134 and more)."""
+    x, _, w = _inputs(T, K)
+    w = (w.float() * 2.0 ** -126).to(B16)
+    y, q, scale = _nan(T, K), _nan(T, K, dtype=E4M3), _nan(T, dtype=torch.float32)
+    api.forge_rmsnorm_fwd(x, w, 1e-6, y=y, yq=q, yq_scale=scale)
+    h = x.double()
+    ref = h * (h.square().mean(1, keepdim=True) + 1e-6).rsqrt() * w.double()
+    s = ref.abs().amax(1) / 448
+    rel = 2 * (_steps(K) / 2 + 8) * U
+    assert ((scale.double() - s).abs() <= rel * s + 2.0 ** -149).all()
+    code = (ref / scale.double()[:, None]).clamp(-448, 448)
+    assert ((q.double() - code).abs() <= code.abs() * (2.0 ** -4 + 2 * (_steps(K) + 12) * U) + 2.0 ** -10 * 1.01).all()
+
+
+def test_a_scale_that_is_no_float_is_a_zero_rows():
+    """max|y| / 448 below the smallest denormal: scale 0 and zero codes."""
+    T, K = 5, 64
+    x = torch.full((T, K), 2.0 ** -10, device="cuda").to(B16)
+    w = torch.full((K,), 2.0 ** -133, device="cuda").to(B16)
+    q, scale = _nan(T, K, dtype=E4M3), _nan(T, dtype=torch.float32)
+    api.forge_rmsnorm_fwd(x, w, 1.0, yq=q, yq_scale=scale)
+    assert not scale.any() and not q.float().any()
