@@ -365,11 +365,11 @@ FORGE_API forge_status_t forge_multi_opt_step(const forge_tensor_t* tensors, int
  *   yq        E4M3 codes [T x K] with one scale per token in yq_scale [T]:
  *             scale = max_k |y| / 448, code = E4M3(y / scale); a row whose
  *             scale is 0 (a zero row, or max |y| / 448 below the smallest
- *             float) has zero codes; a row with a value that is not finite
- *             has NaN scale and codes
+ *             float) has zero codes; a row whose h or w has a value that is
+ *             not finite has NaN scale and codes
  *   yt        E4M3 codes [K x T] (token-contiguous, as forge_linear_bwd_step_fp8
  *             reads X) of y / yt_scale, saturating at +-448; T % 16 == 0
- *   amax      [1], with yt: max |y| over the tensor (NaN if any row has a value
+ *   amax      [1], with yt: max |y| over the tensor (NaN if h or w has a value
  *             that is not finite), from which the caller forms the next step's
  *             yt_scale */
 typedef struct forge_rmsnorm {

@@ -80,13 +80,20 @@ __device__ __forceinline__ uint4 add_bf16x8(uint4 a, uint4 b) {
   return make_uint4(add_bf16x2(a.x, b.x), add_bf16x2(a.y, b.y), add_bf16x2(a.z, b.z), add_bf16x2(a.w, b.w));
 }
 
-// The larger of `top` and the pairs' magnitudes (a NaN does not count).
+// The larger of two magnitudes; a NaN wins.
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+
+// The largest of `top` and the pairs' magnitudes.
 __device__ __forceinline__ float max_abs(float top, const f2 (&f)[4]) {
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
     float a, b;
     unpair(f[j], a, b);
-    top = fmaxf(top, fmaxf(fabsf(a), fabsf(b)));
+    top = max_nan(top, max_nan(fabsf(a), fabsf(b)));
   }
   return top;
 }
@@ -103,9 +110,12 @@ __device__ __forceinline__ float warp_sum(float v) {
 }
 __device__ __forceinline__ float warp_max(float v) {
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xFFFFFFFFu, v, o));
+  for (int o = 16; o > 0; o >>= 1) v = max_nan(v, __shfl_xor_sync(0xFFFFFFFFu, v, o));
   return v;
 }
+
+// An infinite maximum is no scale.
+__device__ __forceinline__ float nan_unless_finite(float a) { return a + (a - a); }
 
 // 1 / sqrt(sum / K + eps)
 __device__ __forceinline__ float inv_rms(float sum, int K, float eps) {
@@ -183,22 +193,23 @@ __global__ void __launch_bounds__(MANY ? 256 : 512, MANY ? (NV >= 8 ? 2 : NV >= 
       top = 0.f;
       for (int i = 0; i < warps; ++i) {
         sum += red[par][0][i];
-        top = fmaxf(top, red[par][1][i]);
+        top = max_nan(top, red[par][1][i]);
       }
     }
     const float rstd = inv_rms(sum, p.K, p.eps);
     if (tid == 0 && p.rstd != nullptr) p.rstd[t] = rstd;
     // A token's codes: scale = max|y| / 448 (0 and zero codes for a zero row;
-    // NaN, and NaN codes, when the row holds a value that is not finite).
+    // NaN, and NaN codes, when the row or the weight holds a value that is not
+    // finite).
     // Near the smallest floats the scale is a denormal of few bits and its
     // reciprocal past the largest float: there the codes are of the stored scale,
     // it and the row (once y is out) brought up by the same power of two.
     float inv = 0.f;
     bool to_y = p.y != nullptr;
     if (want_max) {
-      const float amax = top * rstd, scale = __fdiv_rn(amax, kE4M3Max);
+      const float amax = nan_unless_finite(top * rstd), scale = __fdiv_rn(amax, kE4M3Max);
       if (tid == 0) p.q_scale[t] = scale;
-      inv = __fdiv_rn(kE4M3Max, amax) + (amax - amax);
+      inv = __fdiv_rn(kE4M3Max, amax);
       if (scale < 0x1p-120f) {
         inv = scale > 0.f ? __fdiv_rn(1.f, scale * 0x1p100f) : 0.f;
 #pragma unroll
@@ -366,14 +377,14 @@ __global__ void __launch_bounds__(32 * WARPS, WARPS == 4 ? 5 : WARPS == 8 ? 3 : 
     float sum = 0.f, most = 0.f;
     for (int c = 0; c < cluster; ++c) {  // the same order in each block
       sum += s_part[c][tid].x;
-      most = fmaxf(most, s_part[c][tid].y);
+      most = max_nan(most, s_part[c][tid].y);
     }
     const float rstd = inv_rms(sum, p.K, p.eps);
     s_rstd[tid] = rstd * p.inv_scale;
     if (rank == 0) {
       if (p.rstd != nullptr) p.rstd[t0 + tid] = rstd;
       if (want_max) {
-        const float amax = most * rstd;
+        const float amax = nan_unless_finite(most * rstd);
         const uint32_t bits = amax == amax ? __float_as_uint(amax) : 0x7FC00000u;  // a NaN wins
         const uint32_t all = __reduce_max_sync(rows == 32 ? 0xFFFFFFFFu : 0xFFFFu, bits);
         if (tid == 0) atomicMax(reinterpret_cast<unsigned int*>(p.amax), all);

@@ -116,3 +116,18 @@ def test_a_scale_that_is_no_float_is_a_zero_rows():
     q, scale = _nan(T, K, dtype=E4M3), _nan(T, dtype=torch.float32)
     api.forge_rmsnorm_fwd(x, w, 1.0, yq=q, yq_scale=scale)
     assert not scale.any() and not q.float().any()
+
+
+@pytest.mark.parametrize("T,K", [(16, 512), (48, 5120), (640, 264)])
+@pytest.mark.parametrize("bad", [float("nan"), float("inf"), float("-inf")])
+def test_a_weight_that_is_not_finite_shows_in_scale_and_amax(T, K, bad):
+    x, _, w = _inputs(T, K)
+    w[K // 2 + 1] = bad
+    y, q, scale = _nan(T, K), _nan(T, K, dtype=E4M3), torch.zeros(T, device="cuda")
+    qt, amax = _nan(K, T, dtype=E4M3), torch.zeros(1, device="cuda")
+    api.forge_rmsnorm_fwd(x, w, 1e-6, y=y, yq=q, yq_scale=scale)
+    api.forge_rmsnorm_fwd(x, w, 1e-6, yt=qt, yt_scale=2.0 ** -5, amax=amax)
+    assert torch.isnan(scale).all() and torch.isnan(q.float()).all() and torch.isnan(amax).all()
+    rest = [k for k in range(K) if k != K // 2 + 1]  # bf16 and the codes of a given scale keep it to its column
+    assert torch.isfinite(y[:, rest]).all() and torch.isfinite(qt.float()[rest]).all()
+    assert not torch.isfinite(y[:, K // 2 + 1]).any()
