@@ -356,7 +356,9 @@ FORGE_API forge_status_t forge_multi_opt_step(const forge_tensor_t* tensors, int
 
 /* Root-mean-square norm of T tokens of K columns (K % 8 == 0, 8 <= K <= 16384):
  *   h = bf16(x + residual), or x where residual is NULL;
- *   rstd = 1 / sqrt(mean_k h^2 + eps);   y = h * rstd * w.
+ *   rstd = 1 / sqrt(mean_k h^2 + eps), or 0 where that root is 0 (eps = 0 and
+ *   a row whose squares are 0 in float32);   y = h * rstd * w.
+ * The squares and h * w have to be in float32's range.
  * Statistics and y are float32 from the rounded h, so that the gradient, which
  * reads h, is that of the function computed.  Outputs that are not NULL:
  *   h         bf16 [T x K], needed with a residual; may be x or residual itself

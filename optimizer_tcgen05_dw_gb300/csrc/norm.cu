@@ -3,7 +3,7 @@
 //
 //   h = bf16(x + residual)      (h = x without one; the stream the next
 //                                layers and the gradient read)
-//   r = 1 / sqrt(mean_k h^2 + eps)
+//   r = 1 / sqrt(mean_k h^2 + eps)      (0 where that is 1 / 0)
 //   y = h r w
 //   dx = r (g - n mean_k(g n)) + dh,  g = dy w,  n = h r;   dw = sum_t dy n
 //
@@ -117,9 +117,12 @@ __device__ __forceinline__ float warp_max(float v) {
 // An infinite maximum is no scale.
 __device__ __forceinline__ float nan_unless_finite(float a) { return a + (a - a); }
 
-// 1 / sqrt(sum / K + eps)
+// 1 / sqrt(sum / K + eps), or 0 where that root is 0 (eps = 0, a row whose
+// squares are): such a row's y and codes are zeros and its gradient is dh, where
+// 0 / 0 would make them NaN.
 __device__ __forceinline__ float inv_rms(float sum, int K, float eps) {
-  return __frsqrt_rn(__fdiv_rn(sum, static_cast<float>(K)) + eps);
+  const float square = __fdiv_rn(sum, static_cast<float>(K)) + eps;
+  return square == 0.f ? 0.f : __frsqrt_rn(square);
 }
 
 // ---------------------------------------------------------------- forward

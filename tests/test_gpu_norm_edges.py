@@ -131,3 +131,21 @@ def test_a_weight_that_is_not_finite_shows_in_scale_and_amax(T, K, bad):
     rest = [k for k in range(K) if k != K // 2 + 1]  # bf16 and the codes of a given scale keep it to its column
     assert torch.isfinite(y[:, rest]).all() and torch.isfinite(qt.float()[rest]).all()
     assert not torch.isfinite(y[:, K // 2 + 1]).any()
+
+
+@pytest.mark.parametrize("T", [48, 640])
+def test_zero_rows_without_eps(T):
+    """A row whose mean square plus eps is zero: rstd 0, so y, codes and scale are zero and its gradient is the stream's."""
+    K = 512
+    x, dh, w = _inputs(T, K)
+    x[::5] = 0
+    y, q, scale = _nan(T, K), _nan(T, K, dtype=E4M3), _nan(T, dtype=torch.float32)
+    qt, amax, rstd = _nan(K, T, dtype=E4M3), _nan(1, dtype=torch.float32), _nan(T, dtype=torch.float32)
+    r2 = torch.empty_like(rstd)
+    api.forge_rmsnorm_fwd(x, w, 0.0, rstd=rstd, y=y, yq=q, yq_scale=scale)
+    api.forge_rmsnorm_fwd(x, w, 0.0, rstd=r2, yt=qt, yt_scale=2.0 ** -5, amax=amax)
+    for t in (y[::5], q.float()[::5], scale[::5], qt.float()[:, ::5], rstd[::5], r2[::5]):
+        assert not t.any()
+    assert all(torch.isfinite(t.float()).all() for t in (y, q, scale, qt, rstd, r2, amax)) and amax > 1
+    dx, dw = _gradient(dh, x, w, rstd, dh)
+    assert torch.equal(dx[::5], dh[::5]) and torch.isfinite(dx).all() and torch.isfinite(dw).all()
