@@ -383,7 +383,8 @@ __global__ void __launch_bounds__(32 * WARPS, WARPS == 4 ? 5 : WARPS == 8 ? 3 : 
       most = max_nan(most, s_part[c][tid].y);
     }
     const float rstd = inv_rms(sum, p.K, p.eps);
-    s_rstd[tid] = rstd * p.inv_scale;
+    const float factor = rstd * p.inv_scale;  // past the largest float every code but zero's saturates
+    s_rstd[tid] = factor > 3.4e38f ? 3.4e38f : factor;
     if (rank == 0) {
       if (p.rstd != nullptr) p.rstd[t0 + tid] = rstd;
       if (want_max) {

@@ -149,3 +149,15 @@ def test_zero_rows_without_eps(T):
     assert all(torch.isfinite(t.float()).all() for t in (y, q, scale, qt, rstd, r2, amax)) and amax > 1
     dx, dw = _gradient(dh, x, w, rstd, dh)
     assert torch.equal(dx[::5], dh[::5]) and torch.isfinite(dx).all() and torch.isfinite(dw).all()
+
+
+def test_token_contiguous_codes_of_a_scale_far_below_the_rows():
+    """rstd / yt_scale past the largest float: zeros stay zero codes, the rest saturate."""
+    T, K = 32, 512
+    x, _, w = _inputs(T, K)
+    x = x.clamp(-3, 3) * 2.0 ** -60
+    x[:, ::3] = 0
+    w = w.abs().clamp(0.125)
+    qt = _nan(K, T, dtype=E4M3)
+    api.forge_rmsnorm_fwd(x, w, 0.0, yt=qt, yt_scale=2.0 ** -100)
+    assert torch.equal(qt.float(), (x.float().sign() * 448).t())
