@@ -363,7 +363,7 @@ FORGE_API forge_status_t forge_multi_opt_step(const forge_tensor_t* tensors, int
  * reads h, is that of the function computed.  Outputs that are not NULL:
  *   h         bf16 [T x K], needed with a residual; may be x or residual itself
  *   rstd      [T]
- *   y         bf16 [T x K]
+ *   y         bf16 [T x K]; may be x or residual (where h is not the same)
  *   yq        E4M3 codes [T x K] with one scale per token in yq_scale [T]:
  *             scale = max_k |y| / 448, code = E4M3(y / scale); a row whose
  *             scale is 0 (a zero row, or max |y| / 448 below the smallest

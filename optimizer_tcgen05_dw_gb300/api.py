@@ -569,7 +569,7 @@ def forge_rmsnorm_fwd(x, w, eps: float, residual=None, h=None, rstd=None, y=None
                       yt=None, yt_scale: float = 1.0, amax=None, stream=None):
     """Root-mean-square norm of x [T, K] bf16 (+ residual) with weight w [K]
     bf16.  Writes the outputs given: h (the sum, bf16; may be x or residual), rstd [T], y
-    [T, K] bf16, yq [T, K] E4M3 with yq_scale [T], yt [K, T] E4M3 of y /
+    [T, K] bf16 (may be x or residual where h is not), yq [T, K] E4M3 with yq_scale [T], yt [K, T] E4M3 of y /
     yt_scale with amax [1]."""
     T, K = shape = _rows(x, "x")
     _need(x, "x", torch.bfloat16, shape)

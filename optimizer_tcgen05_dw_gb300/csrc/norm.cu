@@ -620,37 +620,35 @@ cudaError_t launch_norm_fwd(const NormParams& p0, int num_sms, cudaStream_t s) {
   NormParams p = p0;
   const int V = p.K / 8;
   cudaError_t e;
-  if (p.qt == nullptr || p.y != nullptr || p.q != nullptr) {
-    if (p.T < 2 * num_sms) {  // few rows
-      int nv = 1;
-      while ((V + nv - 1) / nv > 512) nv *= 2;
-      const int threads = round32((V + nv - 1) / nv);
-      const int grid = static_cast<int>(p.T);
-      if (nv == 1) run_fwd<1, false>(p, grid, threads, s);
-      else if (nv == 2) run_fwd<2, false>(p, grid, threads, s);
-      else run_fwd<4, false>(p, grid, threads, s);
-    } else {
-      int warps = 1;
-      while (V > 32 * 8 * warps) warps *= 2;
-      const int nv = (V + 32 * warps - 1) / (32 * warps);
-      const int grid = static_cast<int>(least(p.T, static_cast<int64_t>(num_sms) * (32 / warps)));
-      if (nv <= 1) run_fwd<1, true>(p, grid, 32 * warps, s);
-      else if (nv <= 2) run_fwd<2, true>(p, grid, 32 * warps, s);
-      else if (nv <= 4) run_fwd<4, true>(p, grid, 32 * warps, s);
-      else if (nv <= 5) run_fwd<5, true>(p, grid, 32 * warps, s);
-      else if (nv <= 6) run_fwd<6, true>(p, grid, 32 * warps, s);
-      else run_fwd<8, true>(p, grid, 32 * warps, s);
-    }
-    if ((e = cudaGetLastError()) != cudaSuccess) return e;
-    if (p.res != nullptr) p.x = p.h;  // for the codes below
+  if (p.qt != nullptr) {  // first: y may lie over x or the residual
+    if (p.amax != nullptr && (e = cudaMemsetAsync(p.amax, 0, sizeof(float), s)) != cudaSuccess) return e;
+    if ((e = p.res != nullptr ? run_fwd_t<true>(p, s) : run_fwd_t<false>(p, s)) != cudaSuccess) return e;
+    if (p.y == nullptr && p.q == nullptr) return cudaSuccess;
+    if (p.res != nullptr) p.x = p.h;  // the sum is there
     p.res = nullptr;
     p.rstd = nullptr;
   }
-  if (p.qt != nullptr) {
-    if (p.amax != nullptr && (e = cudaMemsetAsync(p.amax, 0, sizeof(float), s)) != cudaSuccess) return e;
-    if ((e = p.res != nullptr ? run_fwd_t<true>(p, s) : run_fwd_t<false>(p, s)) != cudaSuccess) return e;
+  if (p.T < 2 * num_sms) {  // few rows
+    int nv = 1;
+    while ((V + nv - 1) / nv > 512) nv *= 2;
+    const int threads = round32((V + nv - 1) / nv);
+    const int grid = static_cast<int>(p.T);
+    if (nv == 1) run_fwd<1, false>(p, grid, threads, s);
+    else if (nv == 2) run_fwd<2, false>(p, grid, threads, s);
+    else run_fwd<4, false>(p, grid, threads, s);
+  } else {
+    int warps = 1;
+    while (V > 32 * 8 * warps) warps *= 2;
+    const int nv = (V + 32 * warps - 1) / (32 * warps);
+    const int grid = static_cast<int>(least(p.T, static_cast<int64_t>(num_sms) * (32 / warps)));
+    if (nv <= 1) run_fwd<1, true>(p, grid, 32 * warps, s);
+    else if (nv <= 2) run_fwd<2, true>(p, grid, 32 * warps, s);
+    else if (nv <= 4) run_fwd<4, true>(p, grid, 32 * warps, s);
+    else if (nv <= 5) run_fwd<5, true>(p, grid, 32 * warps, s);
+    else if (nv <= 6) run_fwd<6, true>(p, grid, 32 * warps, s);
+    else run_fwd<8, true>(p, grid, 32 * warps, s);
   }
-  return cudaSuccess;
+  return cudaGetLastError();
 }
 
 int64_t norm_bwd_blocks(int64_t T, int K, int num_sms) {

@@ -355,11 +355,11 @@ forge_status_t forge_rmsnorm_fwd(const forge_rmsnorm_t* n, void* stream) {
   p.wait_limit_ns = wait_limit_ns();
   p.status = d.status;
   p.skip_sends = skip_loads() ? 1 : 0;
-  if ((e = launch_norm_fwd(p, d.num_sms, s)) != cudaSuccess) return cuda_fail(e, "norm launch");
-  // without a residual h is x itself
+  // without a residual h is x itself (copied first: y may lie over x)
   if (n->residual == nullptr && n->h != nullptr && n->h != n->x &&
       (e = cudaMemcpyAsync(n->h, n->x, static_cast<size_t>(n->T * n->K * 2), cudaMemcpyDeviceToDevice, s)) != cudaSuccess)
     return cuda_fail(e, "cudaMemcpyAsync(h)");
+  if ((e = launch_norm_fwd(p, d.num_sms, s)) != cudaSuccess) return cuda_fail(e, "norm launch");
   return FORGE_OK;
 }
 

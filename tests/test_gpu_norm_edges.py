@@ -161,3 +161,25 @@ def test_token_contiguous_codes_of_a_scale_far_below_the_rows():
     qt = _nan(K, T, dtype=E4M3)
     api.forge_rmsnorm_fwd(x, w, 0.0, yt=qt, yt_scale=2.0 ** -100)
     assert torch.equal(qt.float(), (x.float().sign() * 448).t())
+
+
+@pytest.mark.parametrize("T,K", [(32, 512), (640, 1024)])
+@pytest.mark.parametrize("residual", [False, True])
+def test_y_over_x(T, K, residual):
+    """y may be x (or the residual): h and the codes are still those of the input."""
+    x, res, w = _inputs(T, K)
+    kw = dict(residual=res if residual else None)
+    h, y, qt, q, scale = _nan(T, K), _nan(T, K), _nan(K, T, dtype=E4M3), _nan(T, K, dtype=E4M3), _nan(T, dtype=torch.float32)
+    api.forge_rmsnorm_fwd(x, w, 1e-6, h=h, y=y, **kw)
+    api.forge_rmsnorm_fwd(x, w, 1e-6, h=torch.empty_like(h), yt=qt, yt_scale=2.0 ** -5, **kw)
+    api.forge_rmsnorm_fwd(x, w, 1e-6, h=torch.empty_like(h), yq=q, yq_scale=scale, **kw)
+    for over in ("x", "residual") if residual else ("x",):
+        a, b = x.clone(), res.clone()
+        to = a if over == "x" else b
+        h2, qt2, q2 = _nan(T, K), _nan(K, T, dtype=E4M3), _nan(T, K, dtype=E4M3)
+        api.forge_rmsnorm_fwd(a, w, 1e-6, residual=b if residual else None, h=h2, y=to, yt=qt2, yt_scale=2.0 ** -5,
+                              yq=q2, yq_scale=torch.empty_like(scale))
+        assert torch.equal(h2, h) and torch.equal(to, y)
+        # the two kernels sum a row in their own orders: a code may round apart where it lies between two
+        assert ((qt2.double() - qt.double()).abs() <= 2.0 ** -3 * qt.double().abs() + 2.0 ** -9).all()
+        assert torch.equal(q2.view(torch.uint8), q.view(torch.uint8))
