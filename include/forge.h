@@ -293,7 +293,8 @@ FORGE_API forge_status_t forge_dequantize_state_block(const void* codes, const f
  *   - offsets is a DEVICE array of groups + 1 ascending int32 in [0, T], read
  *     by the kernels when they run (nothing waits for it on the host).  A
  *     group may be empty, of one row, or hold every row.  Offsets that
- *     decrease or leave [0, T] are clamped and reported by
+ *     leave [0, T] are clamped to it, those that decrease count as the largest
+ *     before them (so no row has two experts), and either is reported by
  *     forge_get_device_status as FORGE_ERR_INVALID_ARG.
  *   - N % 8 == 0, K % 8 == 0, groups <= 1024; T, K and groups * N within 31
  *     bits; all tensors bf16. */

@@ -21,8 +21,9 @@
 //
 // The group offsets are read on the device (no host synchronisation, so calls
 // can be captured in a graph): every CTA builds the same table of column tiles
-// from them.  Offsets that decrease or leave [0, T] are clamped and reported in
-// the status word.  Rows that belong to no group are set to zero.
+// from them.  Offsets that leave [0, T] are clamped to it, those that decrease
+// count as the largest before them, and either is reported in the status word.
+// Rows that belong to no group are set to zero.
 #include <cuda_bf16.h>
 
 #include "launch.h"
@@ -390,7 +391,10 @@ __global__ void __launch_bounds__(32 * kFewWarps) grouped_few_kernel(const uint1
   __shared__ float s_sum[kFewWarps * 8 * kFewTiles * kFewRows];
   const int e = blockIdx.y, f0 = blockIdx.x * kFewRows;
   const int a = p.offsets[e], b = p.offsets[e + 1];
-  const int begin = min(max(a, 0), p.T), end = min(max(b, begin), p.T);
+  // the table's rows (build_groups): each warp finds the largest offset up to e
+  int most = 0;
+  for (int i = threadIdx.x & 31; i <= e; i += 32) most = max(most, min(p.offsets[i], p.T));
+  const int begin = __reduce_max_sync(0xFFFFFFFFu, most), end = max(begin, min(b, p.T));
   if (blockIdx.x == 0 && threadIdx.x == 0 && (a < 0 || b < a || b > p.T))
     atomicCAS(p.status, 0u, static_cast<uint32_t>(kStatusInvalid));
   const uint16_t* We = W + static_cast<int64_t>(e) * p.F * K;

@@ -73,6 +73,7 @@ struct SharedState {
   uint64_t epi_done[4];     // ... and finished by every compute warp (streamed epilogue)
   uint32_t tmem_base;
   int32_t abort;
+  int32_t bad_offsets;      // grouped step: some decrease or leave [0, tokens]
 };
 
 // Per-instantiation layout (per CTA).  The FORGE step with bf16 weights
@@ -205,14 +206,28 @@ __device__ __forceinline__ int group_tile(int u, const GemmParams& p, int& tm, i
   tile_coords_of(u - e * p.group_tiles, p.tiles_m, p.tiles_n, tm, tn);
   return e;
 }
-// Token rows [begin, begin + count) of expert e; offsets that decrease or
-// leave [0, tokens] are clamped (and reported, once a launch finds one).
-__device__ __forceinline__ void group_rows(int e, const GemmParams& p, int& begin, int& count) {
-  const int a = p.offsets[e], b = p.offsets[e + 1];
-  begin = min(max(a, 0), p.tokens);
-  const int end = min(max(b, begin), p.tokens);
+// Whether a pair of neighbouring offsets this thread looks at decreases or
+// leaves [0, tokens]; the CTA's threads look at all of them between them.
+__device__ __forceinline__ bool sees_bad_offsets(const GemmParams& p) {
+  bool bad = false;
+  for (int e = threadIdx.x; e < p.groups; e += blockDim.x) {
+    const int a = p.offsets[e], b = p.offsets[e + 1];
+    bad |= a < 0 || b < a || b > p.tokens;
+  }
+  return bad;
+}
+// Token rows [begin, begin + count) of expert e: from the largest of the
+// offsets up to e to the largest up to e + 1, all clamped to [0, tokens] (each
+// row then has one expert at most, the same in the products of grouped.cu).
+__device__ __forceinline__ void group_rows(int e, const GemmParams& p, const SharedState* ss, int& begin, int& count) {
+  begin = p.offsets[e];
+  int end = p.offsets[e + 1];
+  if (ss->bad_offsets) {
+    begin = 0;
+    for (int i = 0; i <= e; ++i) begin = max(begin, min(p.offsets[i], p.tokens));
+    end = max(begin, min(end, p.tokens));
+  }
   count = end - begin;
-  if (a < 0 || b < a || b > p.tokens) atomicCAS(p.status, 0u, static_cast<uint32_t>(kStatusInvalid));
 }
 // Stages of an expert's reduction: at least one, which an expert without
 // tokens fills with zeros (its gradient).
@@ -286,7 +301,7 @@ __device__ void producer_role(const CUtensorMap* mA, const CUtensorMap* mB, cons
       // among them neither) and its n rows follow.
       for (int u = pair_id(); u < p.num_units; u += num_pairs()) {
         int tm, tn, begin, count;
-        group_rows(group_tile(u, p, tm, tn), p, begin, count);
+        group_rows(group_tile(u, p, tm, tn), p, ss, begin, count);
         const int m0 = tm * kPairM + static_cast<int>(rank) * kTileM;
         const int n0 = tn * kTileN + static_cast<int>(rank) * (kTileN / 2);
         const int stages = group_stages(count, BK);
@@ -428,7 +443,7 @@ __device__ void mma_role(const GemmParams& p, uint8_t* smA, uint8_t* smB, Shared
     int num_kb = p.num_kb;
     if (grouped(MODE)) {
       int begin, count;
-      group_rows(u / p.group_tiles, p, begin, count);
+      group_rows(u / p.group_tiles, p, ss, begin, count);
       num_kb = group_stages(count, BK);
     }
     if (!run_tile(num_kb, MODE == kModeDgrad, u < p.split_from ? kTileN : kTileN / 2)) goto done;
@@ -1885,7 +1900,15 @@ __global__ void __launch_bounds__(KCfg<MODE, WDT, SDT>::kThreads, 1)
   // different paths above), so the barrier counts every thread.
   __syncwarp();
   ptx::tc_fence_before();
-  __syncthreads();
+  if constexpr (grouped(MODE)) {
+    const bool bad = __syncthreads_or(sees_bad_offsets(p));
+    if (threadIdx.x == 0) {
+      ss->bad_offsets = bad;
+      if (bad) atomicCAS(p.status, 0u, static_cast<uint32_t>(kStatusInvalid));
+    }
+  } else {
+    __syncthreads();
+  }
   ptx::cluster_sync();  // both CTAs' barriers exist before either signals the other's
   ptx::tc_fence_after();
   if (MODE == kModeStep && threadIdx.x == 0) atomicAdd(p.dx_done + p.tiles_n, 1u);  // residency_gate

@@ -372,3 +372,34 @@ def test_a_wait_that_runs_out_is_reported():
     api.forge_grouped_linear(X, W, off, Y)
     api.forge_get_device_status()
     assert torch.equal(Y[:10], _round(X[:10].double() @ W[0].double().t()))
+
+
+@pytest.mark.parametrize("offsets", [[0, 50, 20, 90], [-5, 10, 20, 90], [0, 10, 200, 300], [2 ** 31 - 1, 0, -2 ** 31, 7],
+                                     [30, 5, 60, 40], [0, 5, 5, 91]])
+@pytest.mark.parametrize("T", [90, 20, 5000, 11000])
+def test_clamped_offsets_give_every_kernel_the_same_rows(offsets, T):
+    """Expert e's rows run from the largest offset up to e to the largest up to e + 1, all clamped to [0, T]:
+    in Y (both forward kernels), dX and dW, in each layout of the step."""
+    if T > 90:  # the same order over longer groups
+        offsets = [min(o * (T // 90), 2 ** 31 - 1) if o > 0 else o for o in offsets]
+    N, K = 72, 64
+    W, X, dY = _grid((3, N, K), -3, 1), _grid((T, K), 0, 2), _grid((T, N), -6, 3)
+    off = torch.tensor(offsets, dtype=torch.int32, device="cuda")
+    Y, dX, dX2, m = _nan(T, N), _nan(T, K), _nan(T, K), torch.zeros((3, N, K), device="cuda")
+    W0 = W.clone()
+    for call in (lambda: api.forge_grouped_linear(X, W, off, Y), lambda: api.forge_grouped_dgrad(dY, W, off, dX),
+                 lambda: api.forge_grouped_bwd_step(X, dY, W, off, "sgd_momentum", dict(lr=0.0), 1, 0, m, dX=dX2)):
+        call()
+        with pytest.raises(api.ForgeError, match="offsets"):
+            api.forge_get_device_status()
+    edges = np.maximum.accumulate(np.clip(offsets, 0, T))
+    own = torch.zeros(T, dtype=torch.bool, device="cuda")
+    for e in range(3):
+        r = slice(int(edges[e]), int(edges[e + 1]))
+        own[r] = True
+        assert torch.equal(Y[r], _round(X[r].double() @ W0[e].double().t())), f"Y of group {e}"
+        assert torch.equal(dX[r], _round(dY[r].double() @ W0[e].double())), f"dX of group {e}"
+        assert torch.equal(m[e].double(), dY[r].double().t() @ X[r].double()), f"dW of group {e}"
+    assert torch.equal(dX2, dX)
+    for out in (Y, dX):
+        assert not out[~own].any()
