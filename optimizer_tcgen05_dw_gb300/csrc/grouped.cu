@@ -226,7 +226,7 @@ __device__ __forceinline__ void grouped_epilogue(const GroupedParams& p, const G
     }
     ptx::tc_fence_before();
     __syncwarp();
-    if (lane == 0) ptx::mbar_arrive_cluster(empty0 + static_cast<uint32_t>(acc) * 8u);
+    if (lane == 0) ptx::mbar_arrive_cluster_tmem(empty0 + static_cast<uint32_t>(acc) * 8u);
   }
   // rows of no group: before the first and after the last
   const int64_t vec = F / 8, first = g.off[0] * vec, last = g.off[p.groups] * vec, all = p.T * vec;

@@ -814,7 +814,7 @@ __device__ void epilogue_role(const GemmParams& p, SharedState* ss, int warp, in
       epi_store<MODE>(tbase, row, colbase, row_ok, p);
     ptx::tc_fence_before();
     __syncwarp();
-    if (lane == 0) ptx::mbar_arrive_cluster(empty0 + static_cast<uint32_t>(acc) * 8u);
+    if (lane == 0) ptx::mbar_arrive_cluster_tmem(empty0 + static_cast<uint32_t>(acc) * 8u);
   }
 }
 
@@ -1559,7 +1559,7 @@ __device__ void epilogue_compute_role(const GemmParams& p, SharedState* ss, uint
       ptx::fence_proxy_async_smem();  // the staged values, visible to the TMA store
       ptx::tc_fence_before();
       ptx::bar_sync(kEpiBarrier, G::kNB);
-      if (lane == 0) ptx::mbar_arrive_cluster(empty0 + static_cast<uint32_t>(acc) * 8u);
+      if (lane == 0) ptx::mbar_arrive_cluster_tmem(empty0 + static_cast<uint32_t>(acc) * 8u);
     }
   }
   const int first = local + 1;  // accumulator index of the first dW tile
@@ -1679,7 +1679,7 @@ __device__ void epilogue_compute_role(const GemmParams& p, SharedState* ss, uint
       stop = ptx::bar_red_or(kEpiBarrier, G::kNB, false);
     } else {
       ptx::bar_sync(kEpiBarrier, G::kNB);
-      if (lane == 0) ptx::mbar_arrive_cluster(empty0 + static_cast<uint32_t>(acc) * 8u);
+      if (lane == 0) ptx::mbar_arrive_cluster_tmem(empty0 + static_cast<uint32_t>(acc) * 8u);
       if (more) {
         begin(j + 1);
         stop = ptx::bar_red_or(kEpiBarrier, G::kNB, false);
@@ -1804,7 +1804,7 @@ __device__ void grouped_compute_role(const GemmParams& p, SharedState* ss, uint8
     __syncwarp();
     if (lane == 0) {
       ptx::mbar_arrive(&ss->epi_done[j % NB]);
-      if (last) ptx::mbar_arrive_cluster(empty0 + static_cast<uint32_t>(acc) * 8u);
+      if (last) ptx::mbar_arrive_cluster_tmem(empty0 + static_cast<uint32_t>(acc) * 8u);
     }
   }
 }
