@@ -183,3 +183,34 @@ def test_y_over_x(T, K, residual):
         # the two kernels sum a row in their own orders: a code may round apart where it lies between two
         assert ((qt2.double() - qt.double()).abs() <= 2.0 ** -3 * qt.double().abs() + 2.0 ** -9).all()
         assert torch.equal(q2.view(torch.uint8), q.view(torch.uint8))
+
+
+@pytest.mark.parametrize("T,K", [(48, 1024), (48, 2048), (400, 4104), (700, 5120), (400, 8192), (64, 16384)])
+def test_dx_over_dh(T, K):
+    """The documented aliasing, in each variant of the kernel (two load a row ahead)."""
+    h, dh, w = _inputs(T, K)
+    dy = inputs.normal((T, K), 1e-2, 21, device="cuda")
+    rstd = (h.float().square().mean(1) + 1e-6).rsqrt()
+    dx, dw = _gradient(dy, h, w, rstd, dh)
+    over, dw2 = dh.clone(), _nan(K, dtype=torch.float32)
+    api.forge_rmsnorm_bwd(dy, h, w, rstd, over, dw2, _nan(api.forge_rmsnorm_bwd_workspace(T, K), dtype=torch.float32), dh=over)
+    assert torch.equal(over, dx) and torch.equal(dw2, dw)
+
+
+@pytest.mark.parametrize("T,K", [(16, 520), (48, 4096), (112, 5128), (48, 16384), (400, 2048)])
+@pytest.mark.parametrize("with_y", [False, True])
+def test_h_over_its_inputs_with_token_contiguous_codes(T, K, with_y):
+    """h over x and over the residual, T % 32 == 16 (the last tile repeats rows)."""
+    x, res, w = _inputs(T, K)
+    y = _nan(T, K) if with_y else None
+
+    def call(a, b, h):
+        qt, rstd = _nan(K, T, dtype=E4M3), _nan(T, dtype=torch.float32)
+        api.forge_rmsnorm_fwd(a, w, 1e-6, residual=b, h=h, rstd=rstd, y=y, yt=qt, yt_scale=2.0 ** -5)
+        return h, qt.view(torch.uint8), rstd, y.clone() if with_y else rstd
+
+    want = call(x, res, _nan(T, K))
+    assert torch.equal(want[0], (x.float() + res.float()).to(B16))
+    a, b = x.clone(), res.clone()
+    for got in (call(a, res, a), call(x, b, b)):
+        assert all(torch.equal(i, j) for i, j in zip(got, want))
