@@ -206,11 +206,11 @@ __device__ __forceinline__ int group_tile(int u, const GemmParams& p, int& tm, i
   tile_coords_of(u - e * p.group_tiles, p.tiles_m, p.tiles_n, tm, tn);
   return e;
 }
-// Whether a pair of neighbouring offsets this thread looks at decreases or
-// leaves [0, tokens]; the CTA's threads look at all of them between them.
-__device__ __forceinline__ bool sees_bad_offsets(const GemmParams& p) {
+// Whether a pair of neighbouring offsets this lane looks at decreases or leaves
+// [0, tokens]; a warp looks at all of them.
+__device__ __forceinline__ bool sees_bad_offsets(const GemmParams& p, int lane) {
   bool bad = false;
-  for (int e = threadIdx.x; e < p.groups; e += blockDim.x) {
+  for (int e = lane; e < p.groups; e += 32) {
     const int a = p.offsets[e], b = p.offsets[e + 1];
     bad |= a < 0 || b < a || b > p.tokens;
   }
@@ -1881,6 +1881,7 @@ __global__ void __launch_bounds__(KCfg<MODE, WDT, SDT>::kThreads, 1)
     }
     ptx::mbar_init(&ss->mma_done, 1);
     ss->abort = 0;
+    if (grouped(MODE)) ss->bad_offsets = 0;
     ptx::fence_mbar_init();
   }
   if (warp == 0 && lane == 0) {
@@ -1891,6 +1892,10 @@ __global__ void __launch_bounds__(KCfg<MODE, WDT, SDT>::kThreads, 1)
       ptx::prefetch_tensormap(&mapDB);
     }
   }
+  if (grouped(MODE) && warp == 0 && __any_sync(0xFFFFFFFFu, sees_bad_offsets(p, lane)) && lane == 0) {
+    ss->bad_offsets = 1;
+    atomicCAS(p.status, 0u, static_cast<uint32_t>(kStatusInvalid));
+  }
   if (warp == 1) {
     __syncwarp();
     ptx::tmem_alloc_pair(&ss->tmem_base, kTmemCols);
@@ -1900,15 +1905,7 @@ __global__ void __launch_bounds__(KCfg<MODE, WDT, SDT>::kThreads, 1)
   // different paths above), so the barrier counts every thread.
   __syncwarp();
   ptx::tc_fence_before();
-  if constexpr (grouped(MODE)) {
-    const bool bad = __syncthreads_or(sees_bad_offsets(p));
-    if (threadIdx.x == 0) {
-      ss->bad_offsets = bad;
-      if (bad) atomicCAS(p.status, 0u, static_cast<uint32_t>(kStatusInvalid));
-    }
-  } else {
-    __syncthreads();
-  }
+  __syncthreads();
   ptx::cluster_sync();  // both CTAs' barriers exist before either signals the other's
   ptx::tc_fence_after();
   if (MODE == kModeStep && threadIdx.x == 0) atomicAdd(p.dx_done + p.tiles_n, 1u);  // residency_gate
