@@ -206,40 +206,31 @@ __global__ void __launch_bounds__(MANY ? 256 : 512, MANY ? (NV >= 8 ? 2 : NV >= 
     // finite).
     // Near the smallest floats the scale is a denormal of few bits and its
     // reciprocal past the largest float: there the codes are of the stored scale,
-    // it and the row (once y is out) brought up by the same power of two.
-    float inv = 0.f;
-    bool to_y = p.y != nullptr;
+    // with it and the row brought up by the same power of two.
+    float by = rstd, by2 = 0.f;  // codes: (h w) by by2
     if (want_max) {
       const float amax = nan_unless_finite(top * rstd), scale = __fdiv_rn(amax, kE4M3Max);
       if (tid == 0) p.q_scale[t] = scale;
-      inv = __fdiv_rn(kE4M3Max, amax);
-      if (scale < 0x1p-120f) {
-        inv = scale > 0.f ? __fdiv_rn(1.f, scale * 0x1p100f) : 0.f;
-#pragma unroll
-        for (int i = 0; i < NV; ++i) {
-          const int v = tid + i * blockDim.x;
-          f2 y[4];
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            y[j] = mul2(hw[i][j], both(rstd));
-            hw[i][j] = mul2(hw[i][j], both(0x1p100f));
-          }
-          if (to_y && v < V) static_cast<uint4*>(p.y)[t * V + v] = pack8(y);
-        }
-        to_y = false;
-      }
+      const bool tiny = scale < 0x1p-120f;
+      const float inv = __fdiv_rn(tiny ? 1.f : kE4M3Max, tiny ? scale * 0x1p100f : amax);
+      by = tiny ? 0x1p100f : rstd;
+      by2 = tiny ? (scale > 0.f ? inv * rstd : 0.f) : inv;
     }
+    const bool to_y = p.y != nullptr;
     if (!to_y && !want_max) continue;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       const int v = tid + i * blockDim.x;
       if (v >= V) continue;
+      if (to_y) {
+        f2 y[4];
 #pragma unroll
-      for (int j = 0; j < 4; ++j) hw[i][j] = mul2(hw[i][j], both(rstd));
-      if (to_y) static_cast<uint4*>(p.y)[t * V + v] = pack8(hw[i]);
+        for (int j = 0; j < 4; ++j) y[j] = mul2(hw[i][j], both(rstd));
+        static_cast<uint4*>(p.y)[t * V + v] = pack8(y);
+      }
       if (want_max) {
 #pragma unroll
-        for (int j = 0; j < 4; ++j) hw[i][j] = mul2(hw[i][j], both(inv));
+        for (int j = 0; j < 4; ++j) hw[i][j] = mul2(mul2(hw[i][j], both(by)), both(by2));
         static_cast<uint2*>(p.q)[t * V + v] = make_uint2(e4m3x2(hw[i][0]) | (e4m3x2(hw[i][1]) << 16),
                                                          e4m3x2(hw[i][2]) | (e4m3x2(hw[i][3]) << 16));
       }
