@@ -321,7 +321,9 @@ FORGE_API forge_status_t forge_grouped_dgrad(const forge_grouped_t* g, const voi
  * is that of one [groups * N x K] matrix (bf16 weights; FP32, BF16 or INT8
  * states of any width): stochastic rounding draws the bits of index
  * (e * N + n) * K + k, and an expert without tokens takes a step on a zero
- * gradient.  FP32 weights return FORGE_ERR_UNSUPPORTED. */
+ * gradient.  FP32 weights return FORGE_ERR_UNSUPPORTED.  In a captured graph
+ * the offsets are read anew at each replay; hp, step and seed are those of the
+ * capture. */
 FORGE_API forge_status_t forge_grouped_bwd_step(const forge_grouped_t* g, const forge_state_t* state,
                                                 int32_t opt_kind, const forge_hparams_t* hp, int64_t step,
                                                 uint64_t seed, void* stream);
@@ -349,7 +351,9 @@ typedef struct forge_tensor {
  * tensor steps as forge_unfused_opt_step steps it with that seed.  Every
  * pairing of w_dtype and s_dtype is supported.  One launch per 480 tensors
  * that are not empty; the table travels with the launch, so `tensors` may be
- * freed on return. */
+ * freed on return.  hp, step and seed travel with it too: a call captured in a
+ * graph replays the step number, learning rate and rounding bits of its
+ * capture. */
 FORGE_API forge_status_t forge_multi_opt_step(const forge_tensor_t* tensors, int32_t count,
                                               int32_t w_dtype, int32_t g_dtype, int32_t s_dtype,
                                               int32_t opt_kind, const forge_hparams_t* hp,
@@ -374,7 +378,7 @@ FORGE_API forge_status_t forge_multi_opt_step(const forge_tensor_t* tensors, int
  *             reads X) of y / yt_scale, saturating at +-448; T % 16 == 0
  *   amax      [1], with yt: max |y| over the tensor (NaN if h or w has a value
  *             that is not finite), from which the caller forms the next step's
- *             yt_scale */
+ *             yt_scale (a host value: a captured call keeps its own) */
 typedef struct forge_rmsnorm {
   int64_t T, K;
   const void* x;         /* bf16 [T x K]                                     */

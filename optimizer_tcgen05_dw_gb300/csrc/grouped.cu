@@ -314,8 +314,9 @@ __global__ void __launch_bounds__(kGThreads, 1)
 // loads 16 contiguous bytes (eight k) of its row and of its token, and feeds
 // them to two instructions.  How far the loads run ahead (AHEAD) goes by how
 // many blocks have work: with more than two an SM, two turns (fewer registers,
-// more blocks an SM: 16 rows over 12 of 16 experts of 2048 x 4096 33 us, eight
-// turns 34, four 36, one 40), with fewer, eight (one row: 6.9 us, two turns 8.0).
+// more blocks an SM: 16 rows over 12 of 16 experts of 2048 x 4096 33 us in a
+// graph, eight turns 35, four 36, one 41), with fewer, eight (one row: 7.2 us, two
+// turns 8.3).
 constexpr int kFewRows = 16, kFewWarps = 8, kFewTiles = 4;  // up to 4 x 8 tokens a pass
 
 __device__ __forceinline__ uint4 ld_once(const uint4* p) {

@@ -98,9 +98,10 @@ cudaError_t launch_tc_grouped_long(int mode, int sdt, const CUtensorMap& a, cons
 cudaError_t launch_grouped(bool dgrad, const CUtensorMap& w, const CUtensorMap (&tok)[4],
                            const GroupedParams& p, int grid, cudaStream_t s);
 // grouped.cu: the forward product of at most kFewMaxT token rows (K: reduction
-// length).  Against the tensor-core tiles, us for experts of 2048 x 4096: one
-// row 7 and 21; 32 rows of one expert 20 to 22 and 22, over 16 experts 43 and 49;
-// 64 rows of one expert (read twice here) 37 and 22, over 16 experts 46 and 50.
+// length).  Against the tensor-core tiles, us in a graph for experts of 2048 x
+// 4096: one row 7 and 21; 32 rows of one expert 24 to 26 and 22, over 16 experts
+// 43 and 48; 64 rows of one expert (read twice here) 37 and 22, over 16 experts 46
+// and 48.
 constexpr int64_t kFewMaxT = 32;
 cudaError_t launch_grouped_few(const void* W, const void* X, const GroupedParams& p, int K, int num_sms,
                                cudaStream_t s);

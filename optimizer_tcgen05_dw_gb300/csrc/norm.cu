@@ -12,7 +12,7 @@
 //
 // The floor of each is its traffic: x, residual, h, y 2 B an element each,
 // codes 1 B.  So a row is read once and held in registers (or, for the token-contiguous
-// codes, shared memory between its reduction and its output.
+// codes, shared memory) between its reduction and its output.
 #include <cuda_bf16.h>
 #include <cuda_fp8.h>
 
@@ -576,7 +576,7 @@ cudaError_t run_fwd_t(const NormParams& p, cudaStream_t s) {
   const int seg = (V + cluster - 1) / cluster * 8;
   const int smem = kTransTokens * seg * 2;
   // Five blocks of four warps an SM overlap their passes better than three of
-  // eight (16384 x 4096: 88 and 94 us) as long as their memory lets five in;
+  // eight (16384 x 4096: 90 and 102 us) as long as their memory lets five in;
   // where it lets one in (K > 8192), sixteen warps (2048 x 16384: 74 and 84).
   const int warps = smem <= 40960 ? 4 : (smem <= 65536 ? 8 : 16);
   auto* k = warps == 4 ? norm_fwd_t_kernel<RES, 4> : (warps == 8 ? norm_fwd_t_kernel<RES, 8> : norm_fwd_t_kernel<RES, 16>);
@@ -652,7 +652,7 @@ cudaError_t launch_norm_bwd(const NormParams& p, int num_sms, cudaStream_t s) {
   // Loading a row ahead pays where its registers leave room for it: with one
   // vector a thread (16384 x 2048: 60 us, 69 without) and with two in one block
   // an SM (4096 x 8192: 50 and 69); two blocks of two vectors a thread are
-  // faster without (12289 x 5120: 87 and 107, spilled), and four do not fit.
+  // faster without (12289 x 5120: 88 and 106, spilled), and four do not fit.
   const int nv = V <= 256 ? 1 : (V <= 1024 ? 2 : 4);
   const int threads = round32((V + nv - 1) / nv);
   const int grid = static_cast<int>(norm_bwd_blocks(p.T, p.K, num_sms));
