@@ -502,7 +502,9 @@ def make_tensors(weights, grads, s1=None, s2=None, s1_scale=None, s2_scale=None,
     states (float32, bfloat16, or int8 s1 / uint8 s2 codes with float32 absmax
     of ceil(n / block) blocks of the flattened tensor), any shapes and lengths,
     contiguous.  The gradients' values may change between steps, their storage
-    may not: build a table again after replacing a tensor."""
+    may not: the table holds (and keeps alive) the tensors it was built from, and
+    a step after one was replaced still reads the old one, so build a table again
+    then (or zero gradients in place instead of dropping them)."""
     weights, grads = list(weights), list(grads)
     n = len(weights)
 
