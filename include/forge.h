@@ -421,6 +421,90 @@ FORGE_API forge_status_t forge_rmsnorm_bwd(const forge_rmsnorm_grad_t* grad, voi
  * (with a message) when the shape is not supported or there is no device. */
 FORGE_API int64_t forge_rmsnorm_bwd_workspace(int64_t T, int64_t K);
 
+/* ---------------------------------------------------------------------------
+ * The gated feed-forward block, and activations in 8 bits: E4M3 codes in blocks
+ * of 128, read by the gradient and by a matrix product of their own.
+ * ------------------------------------------------------------------------- */
+
+/* The gate's activation: g sigma(g), or its tanh form of GELU,
+ * g (1 + tanh z) / 2 with z = sqrt(2 / pi) (g + 0.044715 g^3). */
+typedef enum forge_act { FORGE_ACT_SILU = 0, FORGE_ACT_GELU_TANH = 1 } forge_act_t;
+
+/* Both projections of T tokens, the gate's activation and the product:
+ *   G = X Wg^T,  U = X Wu^T,  Y = act(G) * U
+ * with W = [Wg; Wu] [2F x K], the gate's F rows first (one matrix: its step is
+ * one forge_linear_bwd_step with dY = dGU).  G and U are float32; Y and what is
+ * kept of them are rounded from there.  Kept for the gradient, one or none:
+ *   gu        bf16 [T x 2F]: row t is G[t], then U[t]
+ *   gu_codes  E4M3 codes [T x 2F] with gu_scale [T x 2 x ceil(F / 128)]: the
+ *             format of forge_quantize_e4m3 over the [2T x F] matrix
+ * F % 8 == 0, K % 8 == 0; T, 2F and K within 31 bits; T == 0 or F == 0 does
+ * nothing, K == 0 gives zeros.  An infinite G or U gives what the formula
+ * does (inf * 0 is NaN).  The outputs overlap neither the inputs nor each other. */
+typedef struct forge_gated {
+  int64_t T, F, K;        /* tokens, gated features, in-features               */
+  int32_t act;            /* forge_act_t                                       */
+  const void* X;          /* bf16 [T x K]                                      */
+  const void* W;          /* bf16 [2F x K]                                     */
+  void* Y;                /* bf16 [T x F]                                      */
+  void* gu;
+  void* gu_codes;
+  float* gu_scale;
+} forge_gated_t;
+FORGE_API forge_status_t forge_gated_linear(const forge_gated_t* gated, void* stream);
+
+/* Its gradient, through the down projection Z = Y Wd^T, Wd [N x F]: from dY
+ * [T x N] (the gradient of Z) and what forge_gated_linear kept,
+ *   dA = dY Wd,   dGU = [dA * U * act'(G),  dA * act(G)],   Y = act(G) * U
+ * (dA is float32 and never written; Y, if asked for, is formed again from what
+ * was kept, so that the forward's need not be).  What follows are two
+ * steps of the linears: Wd's from Y and dY (call it after this one: it updates
+ * Wd), W's from X and dGU, with dX.  dGU may be gu itself; other outputs overlap
+ * neither the inputs nor each other.  N > 0, N % 8 == 0, F % 8 == 0. */
+typedef struct forge_gated_grad {
+  int64_t T, F, N;        /* tokens, gated features, out-features of Wd        */
+  int32_t act;
+  const void* dY;         /* bf16 [T x N]                                      */
+  const void* Wd;         /* bf16 [N x F]                                      */
+  const void* gu;         /* as kept: gu, or gu_codes and gu_scale             */
+  const void* gu_codes;
+  const float* gu_scale;
+  void* dGU;              /* bf16 [T x 2F]                                     */
+  void* Y;                /* bf16 [T x F] or NULL                              */
+} forge_gated_grad_t;
+FORGE_API forge_status_t forge_gated_dgrad(const forge_gated_grad_t* grad, void* stream);
+
+/* Values x [rows x cols] (bf16 or float32: forge_g_dtype_t) to E4M3 codes
+ * [rows x cols] with a float32 scale for each block: 1 x 128 (block_rows 1,
+ * activations; scale [rows x ceil(cols / 128)]) or 128 x 128 (block_rows 128,
+ * weights; scale [ceil(rows / 128) x ceil(cols / 128)]).  Blocks at the end of
+ * a row or of the rows may be short.
+ *   scale = max|x| / 448, at least 2^-126 (so that small blocks lose codes, not
+ *           the scale's bits); 0 for a block of zeros; NaN, with NaN codes, for
+ *           one that holds a value that is not finite
+ *   code  = E4M3(x / scale), to the nearest (x / scale is formed to within
+ *           three float32 roundings)
+ * cols % 8 == 0. */
+FORGE_API forge_status_t forge_quantize_e4m3(const void* x, int32_t x_dtype, void* codes, float* scale,
+                                             int64_t rows, int64_t cols, int32_t block_rows, void* stream);
+/* And back: x = code * scale, a float32 product rounded once to x_dtype. */
+FORGE_API forge_status_t forge_dequantize_e4m3(const void* codes, const float* scale, void* x, int32_t x_dtype,
+                                               int64_t rows, int64_t cols, int32_t block_rows, void* stream);
+
+/* Y = X W^T of values in that format:
+ *   Y[t, n] = sum_b x_scale[t, b] w_scale[n / 128, b] sum_{k in b} Xq[t, k] Wq[n, k]
+ * with the inner sums and the outer one in float32 and one rounding to bf16.
+ * N % 8 == 0, K % 16 == 0; T, N and K within 31 bits; K == 0 gives zeros. */
+typedef struct forge_linear_e4m3 {
+  int64_t T, N, K;
+  const void* Xq;         /* E4M3 [T x K]                                      */
+  const float* x_scale;   /* [T x ceil(K / 128)]                               */
+  const void* Wq;         /* E4M3 [N x K]                                      */
+  const float* w_scale;   /* [ceil(N / 128) x ceil(K / 128)]                   */
+  void* Y;                /* bf16 [T x N]                                      */
+} forge_linear_e4m3_t;
+FORGE_API forge_status_t forge_linear_e4m3(const forge_linear_e4m3_t* lin, void* stream);
+
 /* Synchronises `stream`, then returns and clears the current device's status
  * word: FORGE_OK, FORGE_ERR_TIMEOUT (a bounded wait expired in a kernel),
  * FORGE_ERR_INVALID_ARG (group offsets out of order or range) or

@@ -26,6 +26,8 @@ STATE_INT8_B32, STATE_INT8_B128, STATE_INT8_B256 = 3, 4, 5
 INT8_STATE_OF_BLOCK = {32: STATE_INT8_B32, 64: STATE_INT8_B64, 128: STATE_INT8_B128,
                        256: STATE_INT8_B256}
 G_FP32, G_BF16 = 0, 1
+ACT_KINDS = {"silu": 0, "gelu_tanh": 1}
+CODE_BLOCK = 128  # elements of a row that share a scale of the E4M3 codes
 USES_S1 = {"adamw", "nadam", "radam", "lion", "sgd_momentum"}
 USES_S2 = {"adamw", "nadam", "radam", "rmsprop", "adagrad"}
 
@@ -74,6 +76,21 @@ class ForgeRmsnormGrad(ctypes.Structure):
     _fields_ = [("T", c_int64), ("K", c_int64), ("dy", c_void_p), ("h", c_void_p), ("w", c_void_p),
                 ("rstd", c_void_p), ("dh", c_void_p), ("dx", c_void_p), ("dw", c_void_p),
                 ("workspace", c_void_p)]
+
+
+class ForgeGated(ctypes.Structure):
+    _fields_ = [("T", c_int64), ("F", c_int64), ("K", c_int64), ("act", c_int32), ("X", c_void_p), ("W", c_void_p),
+                ("Y", c_void_p), ("gu", c_void_p), ("gu_codes", c_void_p), ("gu_scale", c_void_p)]
+
+
+class ForgeGatedGrad(ctypes.Structure):
+    _fields_ = [("T", c_int64), ("F", c_int64), ("N", c_int64), ("act", c_int32), ("dY", c_void_p), ("Wd", c_void_p),
+                ("gu", c_void_p), ("gu_codes", c_void_p), ("gu_scale", c_void_p), ("dGU", c_void_p), ("Y", c_void_p)]
+
+
+class ForgeLinearE4m3(ctypes.Structure):
+    _fields_ = [("T", c_int64), ("N", c_int64), ("K", c_int64), ("Xq", c_void_p), ("x_scale", c_void_p),
+                ("Wq", c_void_p), ("w_scale", c_void_p), ("Y", c_void_p)]
 
 
 HPARAM_DEFAULTS = dict(lr=1e-3, beta1=0.9, beta2=0.999, eps=1e-8, weight_decay=0.0, alpha=0.99,
@@ -125,6 +142,11 @@ _SIGNATURES = {
     "forge_rmsnorm_fwd": (c_int32, [ctypes.POINTER(ForgeRmsnorm), c_void_p]),
     "forge_rmsnorm_bwd": (c_int32, [ctypes.POINTER(ForgeRmsnormGrad), c_void_p]),
     "forge_rmsnorm_bwd_workspace": (c_int64, [c_int64, c_int64]),
+    "forge_gated_linear": (c_int32, [ctypes.POINTER(ForgeGated), c_void_p]),
+    "forge_gated_dgrad": (c_int32, [ctypes.POINTER(ForgeGatedGrad), c_void_p]),
+    "forge_quantize_e4m3": (c_int32, [c_void_p, c_int32, c_void_p, c_void_p, c_int64, c_int64, c_int32, c_void_p]),
+    "forge_dequantize_e4m3": (c_int32, [c_void_p, c_void_p, c_void_p, c_int32, c_int64, c_int64, c_int32, c_void_p]),
+    "forge_linear_e4m3": (c_int32, [ctypes.POINTER(ForgeLinearE4m3), c_void_p]),
     "forge_get_device_status": (c_int32, [c_void_p]),
     "forge_set_wait_limit_ns": (c_int32, [c_uint64]),
     "forge_debug_skip_loads": (c_int32, [c_int32]),
@@ -623,6 +645,108 @@ def forge_rmsnorm_bwd(dy, h, w, rstd, dx, dw, workspace, dh=None, stream=None):
     p = ForgeRmsnormGrad(T, K, dy.data_ptr(), h.data_ptr(), w.data_ptr(), rstd.data_ptr(), _ptr(dh), dx.data_ptr(),
                          dw.data_ptr(), workspace.data_ptr())
     _check(lib().forge_rmsnorm_bwd(ctypes.byref(p), _stream(stream)))
+
+
+def _act(act):
+    if act not in ACT_KINDS:
+        raise ValueError(f"act: expected one of {', '.join(ACT_KINDS)}, got {act!r}")
+    return ACT_KINDS[act]
+
+
+def _kept(T, F, gu, gu_codes, gu_scale):
+    """The checks of what forge_gated_linear keeps for its gradient."""
+    if gu is not None and gu_codes is not None:
+        raise ValueError("gu and gu_codes: one of them")
+    if gu is not None:
+        _need(gu, "gu", torch.bfloat16, (T, 2 * F))
+    if gu_codes is not None:
+        _need(gu_codes, "gu_codes", torch.float8_e4m3fn, (T, 2 * F))
+    if gu_codes is not None or gu_scale is not None:
+        _need(gu_scale, "gu_scale", torch.float32, (T, 2, (F + CODE_BLOCK - 1) // CODE_BLOCK))
+
+
+def forge_gated_linear(X, W, Y, act: str = "silu", gu=None, gu_codes=None, gu_scale=None, stream=None):
+    """Y = act(X Wg^T) * (X Wu^T): X [T, K], W [2F, K] (the gate's F rows, then
+    the up projection's), Y [T, F], all bf16; act "silu" or "gelu_tanh".  For
+    forge_gated_dgrad it keeps the two projections side by side in gu [T, 2F]
+    bf16, or in gu_codes [T, 2F] (torch.float8_e4m3fn) with gu_scale
+    [T, 2, ceil(F / 128)]."""
+    T, K = _rows(X, "X")
+    F = _rows(W, "W")[0] // 2
+    _need(X, "X", torch.bfloat16, (T, K))
+    _need(W, "W", torch.bfloat16, (2 * F, K))
+    _need(Y, "Y", torch.bfloat16, (T, F))
+    _kept(T, F, gu, gu_codes, gu_scale)
+    g = ForgeGated(T, F, K, _act(act), X.data_ptr(), W.data_ptr(), Y.data_ptr(), _ptr(gu), _ptr(gu_codes), _ptr(gu_scale))
+    _check(lib().forge_gated_linear(ctypes.byref(g), _stream(stream)))
+
+
+def forge_gated_dgrad(dY, Wd, dGU, act: str = "silu", gu=None, gu_codes=None, gu_scale=None, Y=None, stream=None):
+    """The gradient of forge_gated_linear through the down projection Wd [N, F]:
+    from dY [T, N] and what was kept (gu, or gu_codes and gu_scale), dGU
+    [T, 2F] (the gradients of both projections side by side; may be gu itself)
+    and, if given, Y [T, F] formed again.  Then forge_linear_bwd_step(Y, dY, Wd, ..)
+    and forge_linear_bwd_step(X, dGU, W, .., dX=dX) step the weights."""
+    T, N = _rows(dY, "dY")
+    F = _rows(Wd, "Wd")[1]
+    _need(dY, "dY", torch.bfloat16, (T, N))
+    _need(Wd, "Wd", torch.bfloat16, (N, F))
+    _need(dGU, "dGU", torch.bfloat16, (T, 2 * F))
+    if gu is None and gu_codes is None:
+        raise ValueError("gu or gu_codes is required")
+    _kept(T, F, gu, gu_codes, gu_scale)
+    if Y is not None:
+        _need(Y, "Y", torch.bfloat16, (T, F))
+    g = ForgeGatedGrad(T, F, N, _act(act), dY.data_ptr(), Wd.data_ptr(), _ptr(gu), _ptr(gu_codes), _ptr(gu_scale),
+                       dGU.data_ptr(), _ptr(Y))
+    _check(lib().forge_gated_dgrad(ctypes.byref(g), _stream(stream)))
+
+
+def _coded(codes, scale, x, block_rows):
+    """(rows, cols, x's dtype code) of x [rows, cols] and its codes and scales."""
+    shape = rows, cols = _rows(x, "x")
+    if block_rows not in (1, CODE_BLOCK):
+        raise ValueError(f"block_rows must be 1 or {CODE_BLOCK}, got {block_rows}")
+    if x.dtype not in (torch.float32, torch.bfloat16):
+        raise TypeError(f"x: expected torch.bfloat16 or torch.float32, got {x.dtype}")
+    _need(x, "x", x.dtype, shape)
+    _need(codes, "codes", torch.float8_e4m3fn, shape)
+    _need(scale, "scale", torch.float32, (rows if block_rows == 1 else (rows + CODE_BLOCK - 1) // CODE_BLOCK,
+                                          (cols + CODE_BLOCK - 1) // CODE_BLOCK))
+    return rows, cols, G_FP32 if x.dtype == torch.float32 else G_BF16
+
+
+def forge_quantize_e4m3(x, codes, scale, block_rows: int = 1, stream=None):
+    """x [rows, cols] (bf16 or float32) -> codes (torch.float8_e4m3fn) and a
+    float32 scale for each 128 elements of a row (block_rows 1: scale
+    [rows, ceil(cols / 128)]) or each 128 x 128 (block_rows 128: scale
+    [ceil(rows / 128), ceil(cols / 128)])."""
+    rows, cols, dt = _coded(codes, scale, x, block_rows)
+    _check(lib().forge_quantize_e4m3(x.data_ptr(), dt, codes.data_ptr(), scale.data_ptr(), rows, cols, int(block_rows),
+                                     _stream(stream)))
+
+
+def forge_dequantize_e4m3(codes, scale, x, block_rows: int = 1, stream=None):
+    """The inverse map: x = codes * scale, rounded to x's dtype."""
+    rows, cols, dt = _coded(codes, scale, x, block_rows)
+    _check(lib().forge_dequantize_e4m3(codes.data_ptr(), scale.data_ptr(), x.data_ptr(), dt, rows, cols, int(block_rows),
+                                       _stream(stream)))
+
+
+def forge_linear_e4m3(Xq, x_scale, Wq, w_scale, Y, stream=None):
+    """Y [T, N] bf16 = X W^T from codes Xq [T, K] with x_scale [T, ceil(K / 128)]
+    and Wq [N, K] with w_scale [ceil(N / 128), ceil(K / 128)], as
+    forge_quantize_e4m3 writes them (block_rows 1 and 128)."""
+    T, K = _rows(Xq, "Xq")
+    N = _rows(Wq, "Wq")[0]
+    blocks = lambda n: (n + CODE_BLOCK - 1) // CODE_BLOCK  # noqa: E731
+    _need(Xq, "Xq", torch.float8_e4m3fn, (T, K))
+    _need(x_scale, "x_scale", torch.float32, (T, blocks(K)))
+    _need(Wq, "Wq", torch.float8_e4m3fn, (N, K))
+    _need(w_scale, "w_scale", torch.float32, (blocks(N), blocks(K)))
+    _need(Y, "Y", torch.bfloat16, (T, N))
+    g = ForgeLinearE4m3(T, N, K, Xq.data_ptr(), x_scale.data_ptr(), Wq.data_ptr(), w_scale.data_ptr(), Y.data_ptr())
+    _check(lib().forge_linear_e4m3(ctypes.byref(g), _stream(stream)))
 
 
 def forge_get_device_status(stream=None):

@@ -1,0 +1,258 @@
+// The gated feed-forward products.
+//
+// Forward, both projections of a token, the gate's activation and the product
+// in one kernel:
+//   G = X Wg^T,  U = X Wu^T,  Y = act(G) U          (W = [Wg; Wu], 2F x K)
+// The pair's two CTAs hold the two halves of the matrix instruction's B
+// operand, so one loads gate rows and the other up rows of the same features:
+// every CTA's accumulator then has G in its first W columns and U in the next,
+// and the activation meets its factor in one thread.  What the gradient needs
+// (G and U) leaves in bf16 or as E4M3 codes; the 128 features of a tile are one
+// block of the codes.
+//
+// Gradient, through the down projection's weight Wd [N x F], the product dY Wd
+// with the activation's gradient as its epilogue (dA never reaches memory):
+//   dA = dY Wd,  dU = dA act(G),  dG = dA U act'(G),  and Y = act(G) U again,
+// which the down projection's own step reads: the forward need not keep it.
+//
+// The activations are g s with a sigmoid s:  SiLU: s = sigma(g);  GELU (tanh
+// form): (1 + tanh z) / 2 = sigma(2 z), z = sqrt(2 / pi) (g + 0.044715 g^3).
+// So act' = s + g s (1 - s) d with d = 1 or 2 z'(g): no difference of nearly
+// equal numbers at either end, as 1 + tanh would be.
+#include <cuda_bf16.h>
+
+#include "codes.cuh"
+#include "pair_gemm.cuh"
+
+namespace forge {
+
+namespace {
+
+// s and d of g (see above).  Past |g| = 50 the polynomial's sigmoid is 0 or 1
+// to the last bit: the bound keeps its powers finite (an infinite d times a
+// zero 1 - s would be NaN).
+__device__ __forceinline__ float gate_sigmoid(int act, float g, float& d) {
+  float z = g;
+  d = 1.f;
+  if (act == kActGeluTanh) {
+    constexpr float c = 1.5957691216057308f, k = 0.044715f;  // 2 sqrt(2 / pi)
+    const float b = fminf(fmaxf(g, -50.f), 50.f), b2 = b * b;
+    z = c * b * (1.f + k * b2);
+    d = c * (1.f + 3.f * k * b2);
+  }
+  return __fdiv_rn(1.f, 1.f + expf(-z));
+}
+
+__device__ __forceinline__ float gated(int act, float g, float u) {
+  float d;
+  return g * gate_sigmoid(act, g, d) * u;
+}
+
+// From dA, G and U: dG, dU and Y.
+__device__ __forceinline__ void gated_gradient(int act, float da, float g, float u, float& dg, float& du, float& y) {
+  float d;
+  const float s = gate_sigmoid(act, g, d), a = g * s;
+  du = da * a;
+  dg = da * u * (s + a * (1.f - s) * d);
+  y = a * u;
+}
+
+constexpr int kQuarterBarrier = 2;  // + 0 .. 3: the four warps of a tensor-memory quarter
+
+// ---------------------------------------------------------------- forward
+
+template <int W, bool CODES>
+struct GatedOp {
+  static_assert(!CODES || W == codes::kBlock, "a block of the codes is a tile's features");
+  using Params = GatedParams;
+  struct Maps { int unused; };
+  static constexpr int kW = W, kStg = 6, kEpiBytes = CODES ? 2 * 4 * kTileM * 4 : 0;
+  static constexpr bool kFp8 = false, kBMajorMN = false, kBlockwise = false;
+
+  // rank 0: gate rows, rank 1: up rows of the same features (rows of another
+  // half past a ragged end give columns that are not stored)
+  static __device__ __forceinline__ int b_row(int tn, int rank, const Params& p) { return rank * p.F + tn * W; }
+
+  static __device__ __forceinline__ void epilogue(const Maps&, const Params& p, SharedState* ss, uint8_t* epi, int warp,
+                                                  int lane, uint32_t rank) {
+    constexpr int NC = W / 4;  // features a warp takes
+    const int quarter = warp & 3, sub = (warp - 2) >> 2, r = quarter * 32 + lane;
+    const uint32_t empty0 = ptx::mapa(ptx::smem_addr(&ss->tmem_empty[0]), 0);
+    float* red = reinterpret_cast<float*>(epi);  // [gate, up][warp of the quarter][row]
+    uint32_t local = 0;
+    for (int tile = pair_id(); tile < p.num_tiles; tile += num_pairs(), ++local) {
+      int tm, tn;
+      tile_coords_of(tile, p.tiles_m, p.tiles_n, tm, tn);
+      const int64_t row = static_cast<int64_t>(tm) * kPairM + static_cast<int>(rank) * kTileM + r;
+      const int f0 = tn * W + sub * NC;
+      const uint32_t acc = local & 1u;
+      const bool ok = pairs::warp_wait(&ss->tmem_full[acc], (local >> 1) & 1u, p, ss, lane);
+      if (CODES) {  // the quarter's warps meet below: they stop together
+        if (ptx::bar_red_or(kQuarterBarrier + quarter, 128, !ok)) return;
+        __syncwarp();
+      } else if (!ok) {
+        return;
+      }
+      ptx::tc_fence_after();
+      const uint32_t taddr = ss->tmem_base + (static_cast<uint32_t>(quarter * 32) << 16) + acc * kTileN +
+                             static_cast<uint32_t>(sub * NC);
+      float g[NC], u[NC];
+      pairs::tmem_load<NC>(taddr, g);
+      pairs::tmem_load<NC>(taddr + W, u);
+      ptx::tc_fence_before();
+      __syncwarp();
+      if (lane == 0) ptx::mbar_arrive_cluster_tmem(empty0 + acc * 8u);
+      float gs = 0.f, us = 0.f;
+      if (CODES) {
+        float ga = 0.f, ua = 0.f;
+#pragma unroll
+        for (int j = 0; j < NC; ++j) {  // (columns past F are of other rows)
+          if (f0 + j < p.F) {
+            ga = codes::max_nan(ga, fabsf(g[j]));
+            ua = codes::max_nan(ua, fabsf(u[j]));
+          }
+        }
+        red[sub * kTileM + r] = ga;
+        red[(4 + sub) * kTileM + r] = ua;
+        ptx::bar_sync(kQuarterBarrier + quarter, 128);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          ga = codes::max_nan(ga, red[i * kTileM + r]);
+          ua = codes::max_nan(ua, red[(4 + i) * kTileM + r]);
+        }
+        gs = codes::block_scale(ga);
+        us = codes::block_scale(ua);
+        // (the next tile's first barrier keeps its sums from overtaking these reads)
+      }
+      if (row < p.T) {
+        if (p.gu != nullptr) {
+          uint16_t* out = static_cast<uint16_t*>(p.gu) + row * 2 * p.F + f0;
+#pragma unroll
+          for (int j = 0; j < NC / 8; ++j) {
+            if (f0 + 8 * j >= p.F) break;
+            *reinterpret_cast<uint4*>(out + 8 * j) = pack_rne_bf16x8(reinterpret_cast<const float(&)[8]>(g[8 * j]));
+            *reinterpret_cast<uint4*>(out + p.F + 8 * j) = pack_rne_bf16x8(reinterpret_cast<const float(&)[8]>(u[8 * j]));
+          }
+        }
+        if (CODES) {
+          const float gi = codes::inverse_scale(gs), ui = codes::inverse_scale(us);
+          uint8_t* out = static_cast<uint8_t*>(p.codes) + row * 2 * p.F + f0;
+#pragma unroll
+          for (int j = 0; j < NC / 8; ++j) {
+            if (f0 + 8 * j >= p.F) break;
+            const float* a = g + 8 * j;
+            const float* b = u + 8 * j;
+            *reinterpret_cast<uint2*>(out + 8 * j) = make_uint2(codes::encode4(a[0] * gi, a[1] * gi, a[2] * gi, a[3] * gi),
+                                                                codes::encode4(a[4] * gi, a[5] * gi, a[6] * gi, a[7] * gi));
+            *reinterpret_cast<uint2*>(out + p.F + 8 * j) =
+                make_uint2(codes::encode4(b[0] * ui, b[1] * ui, b[2] * ui, b[3] * ui),
+                           codes::encode4(b[4] * ui, b[5] * ui, b[6] * ui, b[7] * ui));
+          }
+          if (sub < 2) p.scale[(row * 2 + sub) * p.tiles_n + tn] = sub == 0 ? gs : us;
+        }
+        uint16_t* y = static_cast<uint16_t*>(p.Y) + row * p.F + f0;
+#pragma unroll
+        for (int j = 0; j < NC / 8; ++j) {
+          if (f0 + 8 * j >= p.F) break;
+          float v[8];
+#pragma unroll
+          for (int i = 0; i < 8; ++i) v[i] = gated(p.act, g[8 * j + i], u[8 * j + i]);
+          *reinterpret_cast<uint4*>(y + 8 * j) = pack_rne_bf16x8(v);
+        }
+      }
+    }
+  }
+};
+
+// ---------------------------------------------------------------- gradient
+
+template <int W, bool CODES>
+struct GatedGradOp {
+  using Params = GatedParams;
+  struct Maps { int unused; };
+  static constexpr int kW = W, kStg = 6, kEpiBytes = 0;
+  static constexpr bool kFp8 = false, kBMajorMN = true, kBlockwise = false;
+
+  static __device__ __forceinline__ int b_row(int tn, int rank, const Params&) { return (2 * tn + rank) * W; }
+
+  static __device__ __forceinline__ void epilogue(const Maps&, const Params& p, SharedState* ss, uint8_t*, int warp,
+                                                  int lane, uint32_t rank) {
+    constexpr int NC = W / 2;  // features a warp takes
+    const int quarter = warp & 3, sub = (warp - 2) >> 2, r = quarter * 32 + lane;
+    const uint32_t empty0 = ptx::mapa(ptx::smem_addr(&ss->tmem_empty[0]), 0);
+    const int NB = (p.F + codes::kBlock - 1) / codes::kBlock;
+    uint32_t local = 0;
+    for (int tile = pair_id(); tile < p.num_tiles; tile += num_pairs(), ++local) {
+      int tm, tn;
+      tile_coords_of(tile, p.tiles_m, p.tiles_n, tm, tn);
+      const int64_t row = static_cast<int64_t>(tm) * kPairM + static_cast<int>(rank) * kTileM + r;
+      const int f0 = tn * 2 * W + sub * NC;
+      const uint32_t acc = local & 1u;
+      if (!pairs::warp_wait(&ss->tmem_full[acc], (local >> 1) & 1u, p, ss, lane)) return;
+      ptx::tc_fence_after();
+      const uint32_t taddr = ss->tmem_base + (static_cast<uint32_t>(quarter * 32) << 16) + acc * kTileN +
+                             static_cast<uint32_t>(sub * NC);
+      const bool live = row < p.T && f0 < p.F;
+      float gs = 0.f, us = 0.f;
+      if (CODES && live) {
+        gs = p.scale[row * 2 * NB + f0 / codes::kBlock];
+        us = p.scale[(row * 2 + 1) * NB + f0 / codes::kBlock];
+      }
+#pragma unroll 1
+      for (int c = 0; c < NC; c += 8) {
+        float da[8];
+        pairs::tmem_load<8>(taddr + c, da);
+        if (row >= p.T || f0 + c >= p.F) continue;
+        const int64_t at = row * 2 * p.F + f0 + c;
+        float g[8], u[8], y[8];
+        if (CODES) {
+          const uint2 gc = *reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(p.codes) + at);
+          const uint2 uc = *reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(p.codes) + at + p.F);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const float2 a = codes::decode2((j < 2 ? gc.x : gc.y) >> (16 * (j & 1)));
+            const float2 b = codes::decode2((j < 2 ? uc.x : uc.y) >> (16 * (j & 1)));
+            g[2 * j] = a.x * gs;
+            g[2 * j + 1] = a.y * gs;
+            u[2 * j] = b.x * us;
+            u[2 * j + 1] = b.y * us;
+          }
+        } else {
+          load_bf16x8(p.gu, at, g);
+          load_bf16x8(p.gu, at + p.F, u);
+        }
+#pragma unroll
+        for (int j = 0; j < 8; ++j) gated_gradient(p.act, da[j], g[j], u[j], g[j], u[j], y[j]);
+        // (dGU may be gu itself: this thread alone reads and writes these eight of each)
+        store_bf16x8_rne(p.dGU, at, g);
+        store_bf16x8_rne(p.dGU, at + p.F, u);
+        if (p.Y != nullptr) store_bf16x8_rne(p.Y, row * p.F + f0 + c, y);
+      }
+      ptx::tc_fence_before();
+      __syncwarp();
+      if (lane == 0) ptx::mbar_arrive_cluster_tmem(empty0 + acc * 8u);
+    }
+  }
+};
+
+}  // namespace
+
+cudaError_t launch_gated(int width, const CUtensorMap& x, const CUtensorMap& w, const GatedParams& p, int pairs_n,
+                         cudaStream_t s) {
+  if (p.codes != nullptr) return pairs::launch<GatedOp<128, true>>(x, w, {}, p, pairs_n, s);
+  if (width == 128) return pairs::launch<GatedOp<128, false>>(x, w, {}, p, pairs_n, s);
+  if (width == 64) return pairs::launch<GatedOp<64, false>>(x, w, {}, p, pairs_n, s);
+  return pairs::launch<GatedOp<32, false>>(x, w, {}, p, pairs_n, s);
+}
+
+cudaError_t launch_gated_grad(int width, const CUtensorMap& dy, const CUtensorMap& w, const GatedParams& p, int pairs_n,
+                              cudaStream_t s) {
+  const bool kept8 = p.codes != nullptr;
+  if (width == 128)
+    return kept8 ? pairs::launch<GatedGradOp<128, true>>(dy, w, {}, p, pairs_n, s)
+                 : pairs::launch<GatedGradOp<128, false>>(dy, w, {}, p, pairs_n, s);
+  return kept8 ? pairs::launch<GatedGradOp<64, true>>(dy, w, {}, p, pairs_n, s)
+               : pairs::launch<GatedGradOp<64, false>>(dy, w, {}, p, pairs_n, s);
+}
+
+}  // namespace forge

@@ -162,4 +162,55 @@ cudaError_t launch_norm_bwd(const NormParams& p, int num_sms, cudaStream_t s);
 // Rows of p.partial that launch_norm_bwd uses.
 int64_t norm_bwd_blocks(int64_t T, int K, int num_sms);
 
+// Activation kinds (values match forge_act_t).
+enum ActKind : int32_t { kActSilu = 0, kActGeluTanh = 1 };
+
+// What the kernels of pair_gemm.cuh have in common: 256-token rows of tiles,
+// `num_kb` ring stages of 128 bytes of the reduction.
+struct PairParams {
+  int32_t T;
+  int32_t tiles_m, tiles_n, num_tiles, num_kb;
+  int32_t op3d;            // a column-major B: described as 3-D, one copy a stage
+  int32_t skip_loads;
+  uint64_t wait_limit_ns;
+  uint32_t* status;
+};
+
+// Gated feed-forward products (gated.cu).
+struct GatedParams : PairParams {
+  int32_t F, act;
+  void* Y;                 // bf16 [T x F] (gradient: or nullptr)
+  void* gu;                // bf16 [T x 2F], or nullptr; the gradient reads it
+  void* codes;             // E4M3 [T x 2F], or nullptr; likewise
+  float* scale;            // [T x 2 x ceil(F / 128)]
+  void* dGU;               // gradient: bf16 [T x 2F]
+};
+// width: features of a tile (128, 64 or 32; the gradient's tiles have two
+// widths of 128 or 64).  With p.codes the forward takes 128.
+cudaError_t launch_gated(int width, const CUtensorMap& x, const CUtensorMap& w, const GatedParams& p, int pairs,
+                         cudaStream_t s);
+cudaError_t launch_gated_grad(int width, const CUtensorMap& dy, const CUtensorMap& w, const GatedParams& p, int pairs,
+                              cudaStream_t s);
+
+// The product of block-scaled codes (product.cu); num_kb blocks of 128.
+struct ProductParams : PairParams {
+  int32_t N;
+  const float* x_scale;    // [T x num_kb]
+  const float* w_scale;    // [ceil(N / 128) x num_kb]
+  void* Y;                 // bf16 [T x N]
+};
+cudaError_t launch_product(int width, const CUtensorMap& x, const CUtensorMap& w, const ProductParams& p, int pairs,
+                           cudaStream_t s);
+
+// Values to E4M3 codes in blocks of 128 and back (codes.cu).
+struct CodesParams {
+  const void* x;           // bf16 or float32 [rows x cols] (written by the way back)
+  uint8_t* codes;          // [rows x cols]
+  float* scale;            // [rows or ceil(rows / 128), ceil(cols / 128)]
+  int64_t rows, cols;
+  int32_t square;          // blocks of 128 x 128, not 1 x 128
+};
+cudaError_t launch_quantize_e4m3(bool fp32, const CodesParams& p, int num_sms, cudaStream_t s);
+cudaError_t launch_dequantize_e4m3(bool fp32, const CodesParams& p, int num_sms, cudaStream_t s);
+
 }  // namespace forge
