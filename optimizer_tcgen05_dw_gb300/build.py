@@ -28,10 +28,10 @@ NVCC_FLAGS = ARCH + ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC",
 LIBS = {
     "libforge.so": ["api.cu", "ops_api.cu", "tc_fused.cu", "tc_step.cu", "tc_fp8.cu", "tc_plain.cu", "elementwise.cu",
                     "tc_grouped.cu", "tc_grouped_long.cu", "grouped.cu", "multi.cu", "norm.cu", "ffn_api.cu", "gated.cu",
-                    "codes.cu", "product.cu"],
+                    "codes.cu", "product.cu", "few_rows.cu"],
     "libforge_testkit.so": ["testkit.cu"],
 }
-HEADERS = ["codes.cuh", "common.h", "elem.cuh", "host.h", "launch.h", "optim.cuh", "pair_gemm.cuh", "ptx.cuh",
+HEADERS = ["codes.cuh", "common.h", "elem.cuh", "gate.cuh", "host.h", "launch.h", "optim.cuh", "pair_gemm.cuh", "ptx.cuh",
            "tc_grouped.cuh", "tc_kernel.cuh"]
 
 

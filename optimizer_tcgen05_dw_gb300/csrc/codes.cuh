@@ -47,5 +47,24 @@ __device__ __forceinline__ float2 decode2(uint32_t c) {
   return __half22float2(*reinterpret_cast<const __half2*>(&h));
 }
 
+// A sum of code products is scaled by its blocks' two scales.  Their product
+// may leave float32's range where the value does not, so the factor comes in
+// two parts, value = (sum * p) * f, p a power of two: 1 unless xs * ws is below
+// 2^-100 or above 2^100.  (Past the largest float f is that: sums that are not
+// 0 go to infinity, 0 stays.)  A scale that is 0 or NaN gives that factor.
+struct Factor {
+  float f, p;
+};
+__device__ __forceinline__ Factor factor(float xs, float ws) {
+  Factor r = {xs * ws, 1.f};
+  if ((r.f <= 0x1p-100f || r.f >= 0x1p100f) && xs > 0.f && ws > 0.f) {
+    const bool low = r.f < 1.f;
+    const float k = low ? 0x1p32f : 0x1p-32f;
+    r.f = fminf((xs * k) * (ws * k), 0x1.fffffep127f);
+    r.p = low ? 0x1p-64f : 0x1p64f;
+  }
+  return r;
+}
+
 }  // namespace codes
 }  // namespace forge

@@ -1,0 +1,252 @@
+// The gated product and the product of block-scaled codes for a few token rows
+// (decoding).  The weights are read once for a handful of tokens, so the floor
+// is that read and what matters is to spread it evenly and keep it streaming:
+// a block takes the weight rows of 8 (gated: gate and up) or 16 features, its
+// eight warps share the reduction, and the warp-level matrix instruction takes
+// the weights from the registers they were loaded to (each is used once: staging
+// it through shared memory for a larger instruction would only lengthen its way).
+// The instruction's k order is free as long as both operands agree: a lane loads
+// 16 contiguous bytes of its row and of its token and feeds them to two
+// instructions.  The warps' sums meet in shared memory, in warp order.
+//
+// Tokens past the last repeat it, rows past the last feature repeat it; their
+// results are not stored.
+#include <cuda_bf16.h>
+
+#include "codes.cuh"
+#include "gate.cuh"
+#include "launch.h"
+#include "optim.cuh"
+
+namespace forge {
+
+namespace {
+
+constexpr int kWarps = 8, kThreads = 32 * kWarps;
+
+__device__ __forceinline__ uint4 ld_once(const uint4* p) {
+  uint4 v;
+  asm("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
+  return v;
+}
+
+// Rows 0-7 (lane >> 2) and 8-15 of the first operand against eight columns:
+// c[0], c[1] are row lane >> 2, columns 2 (lane & 3) and the next, c[2], c[3] row + 8.
+__device__ __forceinline__ void mma_bf16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                         uint32_t b1) {
+  asm(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+      "{%0, %1, %2, %3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                        uint32_t b1) {
+  asm(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+      "{%0, %1, %2, %3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// Sixteen codes as half pairs (every E4M3 value is a half).
+__device__ __forceinline__ void halves16(uint4 c, uint32_t (&h)[8]) {
+  const uint32_t w[4] = {c.x, c.y, c.z, c.w};
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    const __half2_raw r = __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>((w[j >> 1] >> (16 * (j & 1))) & 0xFFFFu), __NV_E4M3);
+    h[j] = static_cast<uint32_t>(r.x) | (static_cast<uint32_t>(r.y) << 16);
+  }
+}
+
+__device__ __forceinline__ uint16_t bf16_bits(float v) {
+  const __nv_bfloat16 b = __float2bfloat16_rn(v);
+  return *reinterpret_cast<const uint16_t*>(&b);
+}
+
+// ---------------------------------------------------------------- gated
+
+// Features 8 MT blockIdx.x .. of up to 8 NT tokens.  The gate's rows are rows
+// 0-7 of the instruction and the up projection's rows 8-15, so a lane holds
+// both projections of a feature.
+template <int MT, int NT, int AHEAD>
+__global__ void __launch_bounds__(kThreads) gated_few_kernel(const uint16_t* W, const uint16_t* X, const GatedParams p,
+                                                             const int K) {
+  constexpr int kTok = 8 * NT, kRow = 16 * MT;
+  __shared__ float s_sum[kWarps * kTok * kRow];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, q = lane & 3;
+  const int V = K >> 3, f0 = blockIdx.x * 8 * MT;
+  const uint4 *wg[MT], *wu[MT], *x[NT];
+  float acc[MT][NT][4];
+#pragma unroll
+  for (int m = 0; m < MT; ++m) {
+    const int64_t f = min(f0 + 8 * m + g, p.F - 1);
+    wg[m] = reinterpret_cast<const uint4*>(W + f * K);
+    wu[m] = reinterpret_cast<const uint4*>(W + (p.F + f) * K);
+#pragma unroll
+    for (int i = 0; i < NT; ++i)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) acc[m][i][j] = 0.f;
+  }
+#pragma unroll
+  for (int i = 0; i < NT; ++i) x[i] = reinterpret_cast<const uint4*>(X + static_cast<int64_t>(min(8 * i + g, p.T - 1)) * K);
+  const uint4 zero = make_uint4(0, 0, 0, 0);
+#pragma unroll AHEAD
+  for (int v = warp * 4 + q; v - q < V; v += kWarps * 4) {  // uniform over the warp
+    const bool in = v < V;
+    uint4 a[MT], b[MT];
+#pragma unroll
+    for (int m = 0; m < MT; ++m) {
+      a[m] = in ? ld_once(wg[m] + v) : zero;
+      b[m] = in ? ld_once(wu[m] + v) : zero;
+    }
+#pragma unroll
+    for (int i = 0; i < NT; ++i) {
+      const uint4 t = in ? x[i][v] : zero;
+#pragma unroll
+      for (int m = 0; m < MT; ++m) {
+        mma_bf16(acc[m][i], a[m].x, b[m].x, a[m].y, b[m].y, t.x, t.y);
+        mma_bf16(acc[m][i], a[m].z, b[m].z, a[m].w, b[m].w, t.z, t.w);
+      }
+    }
+  }
+  // [warp][token][gate's features, then the up projection's]
+#pragma unroll
+  for (int m = 0; m < MT; ++m)
+#pragma unroll
+    for (int i = 0; i < NT; ++i)
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        s_sum[(warp * kTok + 8 * i + 2 * q + (j & 1)) * kRow + (j >> 1) * (8 * MT) + 8 * m + g] = acc[m][i][j];
+  __syncthreads();
+  for (int o = threadIdx.x; o < kTok * 8 * MT; o += kThreads) {
+    const int t = o / (8 * MT), c = o % (8 * MT), f = f0 + c;
+    if (t >= p.T || f >= p.F) continue;
+    float gate = 0.f, up = 0.f;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) {
+      gate += s_sum[(w * kTok + t) * kRow + c];
+      up += s_sum[(w * kTok + t) * kRow + 8 * MT + c];
+    }
+    static_cast<uint16_t*>(p.Y)[static_cast<int64_t>(t) * p.F + f] = bf16_bits(gated(p.act, gate, up));
+    if (p.gu != nullptr) {
+      uint16_t* kept = static_cast<uint16_t*>(p.gu) + static_cast<int64_t>(t) * 2 * p.F + f;
+      kept[0] = bf16_bits(gate);
+      kept[p.F] = bf16_bits(up);
+    }
+  }
+}
+
+// ---------------------------------------------------------------- codes
+
+// Features 16 blockIdx.x .. of up to 8 NT tokens; a warp takes a block of 128
+// of the reduction at a time, and its sum meets the block's two scales.  The
+// codes are multiplied as halves: the warp-level instruction on E4M3 itself ran
+// at a fraction of that one's rate (5 rows of 4096 x 14336: 33 us and more).
+template <int NT, int AHEAD>
+__global__ void __launch_bounds__(kThreads) product_few_kernel(const uint8_t* W, const uint8_t* X, const ProductParams p,
+                                                               const int K) {
+  constexpr int kTok = 8 * NT;
+  __shared__ float s_sum[kWarps * kTok * 16];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, q = lane & 3;
+  const int f0 = blockIdx.x * 16, V = K >> 4;
+  const uint4* w0 = reinterpret_cast<const uint4*>(W + static_cast<int64_t>(min(f0 + g, p.N - 1)) * K);
+  const uint4* w1 = reinterpret_cast<const uint4*>(W + static_cast<int64_t>(min(f0 + g + 8, p.N - 1)) * K);
+  const float* sw = p.w_scale + static_cast<int64_t>(f0 / codes::kBlock) * p.num_kb;
+  const uint4* x[NT];
+  const float* sx[NT][2];
+  float acc[NT][4];
+#pragma unroll
+  for (int i = 0; i < NT; ++i) {
+    x[i] = reinterpret_cast<const uint4*>(X + static_cast<int64_t>(min(8 * i + g, p.T - 1)) * K);
+#pragma unroll
+    for (int j = 0; j < 2; ++j) sx[i][j] = p.x_scale + static_cast<int64_t>(min(8 * i + 2 * q + j, p.T - 1)) * p.num_kb;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) acc[i][j] = 0.f;
+  }
+  const uint4 zero = make_uint4(0, 0, 0, 0);
+#pragma unroll AHEAD
+  for (int b = warp; b < p.num_kb; b += kWarps) {
+    uint4 a0[2], a1[2];
+    const float ws = sw[b];
+    float c[NT][4];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int v = b * 8 + h * 4 + q;
+      a0[h] = v < V ? ld_once(w0 + v) : zero;
+      a1[h] = v < V ? ld_once(w1 + v) : zero;
+    }
+#pragma unroll
+    for (int i = 0; i < NT; ++i)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) c[i][j] = 0.f;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int v = b * 8 + h * 4 + q;
+      uint32_t r0[8], r1[8];
+      halves16(a0[h], r0);
+      halves16(a1[h], r1);
+#pragma unroll
+      for (int i = 0; i < NT; ++i) {
+        uint32_t t[8];
+        halves16(v < V ? x[i][v] : zero, t);
+#pragma unroll
+        for (int k = 0; k < 8; k += 2) mma_f16(c[i], r0[k], r1[k], r0[k + 1], r1[k + 1], t[k], t[k + 1]);
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < NT; ++i)
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        const codes::Factor f = codes::factor(sx[i][j][b], ws);
+        acc[i][j] = fmaf(c[i][j] * f.p, f.f, acc[i][j]);
+        acc[i][j + 2] = fmaf(c[i][j + 2] * f.p, f.f, acc[i][j + 2]);
+      }
+  }
+  // [warp][token][feature]
+#pragma unroll
+  for (int i = 0; i < NT; ++i)
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      s_sum[(warp * kTok + 8 * i + 2 * q + (j & 1)) * 16 + g + 8 * (j >> 1)] = acc[i][j];
+  __syncthreads();
+  for (int o = threadIdx.x; o < kTok * 16; o += kThreads) {
+    const int t = o / 16, f = f0 + o % 16;
+    if (t >= p.T || f >= p.N) continue;
+    float sum = 0.f;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) sum += s_sum[w * kTok * 16 + o];
+    static_cast<uint16_t*>(p.Y)[static_cast<int64_t>(t) * p.N + f] = bf16_bits(sum);
+  }
+}
+
+template <int MT, int NT>
+cudaError_t run_gated(const void* W, const void* X, const GatedParams& p, int K, cudaStream_t s) {
+  const unsigned grid = static_cast<unsigned>((p.F + 8 * MT - 1) / (8 * MT));
+  gated_few_kernel<MT, NT, 4><<<grid, kThreads, 0, s>>>(static_cast<const uint16_t*>(W), static_cast<const uint16_t*>(X), p, K);
+  return cudaGetLastError();
+}
+
+template <int NT>
+cudaError_t run_product(const void* W, const void* X, const ProductParams& p, int K, cudaStream_t s) {
+  const unsigned grid = static_cast<unsigned>((p.N + 15) / 16);
+  product_few_kernel<NT, 4><<<grid, kThreads, 0, s>>>(static_cast<const uint8_t*>(W), static_cast<const uint8_t*>(X), p, K);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_gated_few(const void* W, const void* X, const GatedParams& p, int K, cudaStream_t s) {
+  if (p.T <= 8) return run_gated<1, 1>(W, X, p, K, s);
+  if (p.T <= 16) return run_gated<2, 2>(W, X, p, K, s);
+  return run_gated<2, 4>(W, X, p, K, s);
+}
+
+cudaError_t launch_product_few(const void* W, const void* X, const ProductParams& p, int K, cudaStream_t s) {
+  if (p.T <= 8) return run_product<1>(W, X, p, K, s);
+  if (p.T <= 16) return run_product<2>(W, X, p, K, s);
+  return run_product<4>(W, X, p, K, s);
+}
+
+}  // namespace forge

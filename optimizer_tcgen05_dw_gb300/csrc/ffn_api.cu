@@ -78,6 +78,8 @@ forge_status_t check_tiles(int64_t rows, int64_t cols, int64_t narrowest) {
     return fail(FORGE_ERR_UNSUPPORTED, "too many output tiles (%lld x %lld)", (long long)rows, (long long)cols);
   return FORGE_OK;
 }
+// Token rows of a copy of the A operand.
+uint32_t box_rows(int64_t T) { return T <= kShortRows ? kShortRows : kTileM; }
 int pairs_of(const PairParams& p, const DeviceInfo& d) { return p.num_tiles < d.num_sms / 2 ? p.num_tiles : d.num_sms / 2; }
 
 // The checks that both directions of the gated product share: shapes, the
@@ -144,8 +146,12 @@ forge_status_t forge_gated_linear(const forge_gated_t* g, void* stream) {
   p.gu = g->gu;
   p.codes = g->gu_codes;
   p.scale = g->gu_scale;
+  if (T <= kFewGated && g->gu_codes == nullptr && p.skip_loads == 0) {  // (that hook is for the pipelined kernels' waits)
+    const cudaError_t e = launch_gated_few(g->W, g->X, p, static_cast<int>(K), s);
+    return e == cudaSuccess ? FORGE_OK : cuda_fail(e, "gated product launch");
+  }
   CUtensorMap mx, mw;
-  if ((st = tensor_map(&mx, g->X, kBf16, 2, K, T, kBlockK, kTileM, CU_TENSOR_MAP_SWIZZLE_128B)) != FORGE_OK ||
+  if ((st = tensor_map(&mx, g->X, kBf16, 2, K, T, kBlockK, g->gu_codes != nullptr ? kTileM : box_rows(T), CU_TENSOR_MAP_SWIZZLE_128B)) != FORGE_OK ||
       (st = tensor_map(&mw, g->W, kBf16, 2, K, 2 * F, kBlockK, static_cast<uint32_t>(width), CU_TENSOR_MAP_SWIZZLE_128B)) != FORGE_OK)
     return st;
   const cudaError_t e = launch_gated(width, mx, mw, p, pairs_of(p, d), s);
@@ -254,12 +260,18 @@ forge_status_t forge_linear_e4m3(const forge_linear_e4m3_t* lin, void* stream) {
   p.x_scale = lin->x_scale;
   p.w_scale = lin->w_scale;
   p.Y = lin->Y;
+  if (T <= kFewProduct && p.skip_loads == 0) {
+    const cudaError_t e = launch_product_few(lin->Wq, lin->Xq, p, static_cast<int>(K), s);
+    return e == cudaSuccess ? FORGE_OK : cuda_fail(e, "block-scaled product launch");
+  }
   CUtensorMap mx, mw;
-  if ((st = tensor_map(&mx, lin->Xq, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, K, T, kBlock, kTileM, CU_TENSOR_MAP_SWIZZLE_128B)) != FORGE_OK ||
+  if ((st = tensor_map(&mx, lin->Xq, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, K, T, kBlock, box_rows(T), CU_TENSOR_MAP_SWIZZLE_128B)) != FORGE_OK ||
       (st = tensor_map(&mw, lin->Wq, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, K, N, kBlock, static_cast<uint32_t>(width),
                        CU_TENSOR_MAP_SWIZZLE_128B)) != FORGE_OK)
     return st;
-  const cudaError_t e = launch_product(width, mx, mw, p, pairs_of(p, d), s);
+  CUtensorMap my = mx;
+  if (width == 128 && (st = tensor_map(&my, lin->Y, kBf16, 2, N, T, 64, 32, CU_TENSOR_MAP_SWIZZLE_128B)) != FORGE_OK) return st;
+  const cudaError_t e = launch_product(width, mx, mw, my, p, pairs_of(p, d), s);
   return e == cudaSuccess ? FORGE_OK : cuda_fail(e, "block-scaled product launch");
 }
 

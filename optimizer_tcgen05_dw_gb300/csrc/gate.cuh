@@ -1,0 +1,42 @@
+// The gate's activation and its gradient, in float32.
+//
+// The activations are g s with a sigmoid s:  SiLU: s = sigma(g);  GELU (tanh
+// form): (1 + tanh z) / 2 = sigma(2 z), z = sqrt(2 / pi) (g + 0.044715 g^3).
+// So act' = s + g s (1 - s) d with d = 1 or 2 z'(g): no difference of nearly
+// equal numbers at either end, as 1 + tanh would be.
+#pragma once
+
+#include "launch.h"
+
+namespace forge {
+
+// s and d of g (see above).  Past |g| = 50 the polynomial's sigmoid is 0 or 1
+// to the last bit: the bound keeps its powers finite (an infinite d times a
+// zero 1 - s would be NaN).
+__device__ __forceinline__ float gate_sigmoid(int act, float g, float& d) {
+  float z = g;
+  d = 1.f;
+  if (act == kActGeluTanh) {
+    constexpr float c = 1.5957691216057308f, k = 0.044715f;  // 2 sqrt(2 / pi)
+    const float b = fminf(fmaxf(g, -50.f), 50.f), b2 = b * b;
+    z = c * b * (1.f + k * b2);
+    d = c * (1.f + 3.f * k * b2);
+  }
+  return __fdiv_rn(1.f, 1.f + expf(-z));
+}
+
+__device__ __forceinline__ float gated(int act, float g, float u) {
+  float d;
+  return g * gate_sigmoid(act, g, d) * u;
+}
+
+// From dA, G and U: dG, dU and Y.
+__device__ __forceinline__ void gated_gradient(int act, float da, float g, float u, float& dg, float& du, float& y) {
+  float d;
+  const float s = gate_sigmoid(act, g, d), a = g * s;
+  du = da * a;
+  dg = da * u * (s + a * (1.f - s) * d);
+  y = a * u;
+}
+
+}  // namespace forge

@@ -14,79 +14,47 @@
 // with the activation's gradient as its epilogue (dA never reaches memory):
 //   dA = dY Wd,  dU = dA act(G),  dG = dA U act'(G),  and Y = act(G) U again,
 // which the down projection's own step reads: the forward need not keep it.
-//
-// The activations are g s with a sigmoid s:  SiLU: s = sigma(g);  GELU (tanh
-// form): (1 + tanh z) / 2 = sigma(2 z), z = sqrt(2 / pi) (g + 0.044715 g^3).
-// So act' = s + g s (1 - s) d with d = 1 or 2 z'(g): no difference of nearly
-// equal numbers at either end, as 1 + tanh would be.
 #include <cuda_bf16.h>
 
 #include "codes.cuh"
+#include "gate.cuh"
 #include "pair_gemm.cuh"
 
 namespace forge {
 
 namespace {
 
-// s and d of g (see above).  Past |g| = 50 the polynomial's sigmoid is 0 or 1
-// to the last bit: the bound keeps its powers finite (an infinite d times a
-// zero 1 - s would be NaN).
-__device__ __forceinline__ float gate_sigmoid(int act, float g, float& d) {
-  float z = g;
-  d = 1.f;
-  if (act == kActGeluTanh) {
-    constexpr float c = 1.5957691216057308f, k = 0.044715f;  // 2 sqrt(2 / pi)
-    const float b = fminf(fmaxf(g, -50.f), 50.f), b2 = b * b;
-    z = c * b * (1.f + k * b2);
-    d = c * (1.f + 3.f * k * b2);
-  }
-  return __fdiv_rn(1.f, 1.f + expf(-z));
-}
-
-__device__ __forceinline__ float gated(int act, float g, float u) {
-  float d;
-  return g * gate_sigmoid(act, g, d) * u;
-}
-
-// From dA, G and U: dG, dU and Y.
-__device__ __forceinline__ void gated_gradient(int act, float da, float g, float u, float& dg, float& du, float& y) {
-  float d;
-  const float s = gate_sigmoid(act, g, d), a = g * s;
-  du = da * a;
-  dg = da * u * (s + a * (1.f - s) * d);
-  y = a * u;
-}
-
 constexpr int kQuarterBarrier = 2;  // + 0 .. 3: the four warps of a tensor-memory quarter
 
 // ---------------------------------------------------------------- forward
 
-template <int W, bool CODES>
+template <int W, bool CODES, int AROWS = kTileM>
 struct GatedOp {
   static_assert(!CODES || W == codes::kBlock, "a block of the codes is a tile's features");
   using Params = GatedParams;
   struct Maps { int unused; };
-  static constexpr int kW = W, kStg = 6, kEpiBytes = CODES ? 2 * 4 * kTileM * 4 : 0;
+  static constexpr int kW = W, kARows = AROWS, kBufs = W == 128 ? 2 : 4, kEpiWarps = 16;
+  static constexpr int kStg = AROWS < kTileM ? (W == 128 ? 10 : W == 64 ? 16 : 24) : (W == 128 ? 6 : W == 64 ? 9 : 11);
+  static constexpr int kEpiBytes = CODES ? 2 * 4 * kTileM * 4 : 0;
   static constexpr bool kFp8 = false, kBMajorMN = false, kBlockwise = false;
 
   // rank 0: gate rows, rank 1: up rows of the same features (rows of another
   // half past a ragged end give columns that are not stored)
   static __device__ __forceinline__ int b_row(int tn, int rank, const Params& p) { return rank * p.F + tn * W; }
 
-  static __device__ __forceinline__ void epilogue(const Maps&, const Params& p, SharedState* ss, uint8_t* epi, int warp,
+  static __device__ __forceinline__ void epilogue(const Maps&, const Params& p, pairs::Shared* ss, uint8_t* epi, int warp,
                                                   int lane, uint32_t rank) {
     constexpr int NC = W / 4;  // features a warp takes
-    const int quarter = warp & 3, sub = (warp - 2) >> 2, r = quarter * 32 + lane;
+    const int quarter = warp & 3, sub = (warp - pairs::kFirstEpiWarp) >> 2, r = quarter * 32 + lane;
     const uint32_t empty0 = ptx::mapa(ptx::smem_addr(&ss->tmem_empty[0]), 0);
     float* red = reinterpret_cast<float*>(epi);  // [gate, up][warp of the quarter][row]
-    uint32_t local = 0;
-    for (int tile = pair_id(); tile < p.num_tiles; tile += num_pairs(), ++local) {
+    uint32_t acc = 0, ph = 0;
+    for (int tile = pair_id(); tile < p.num_tiles; tile += num_pairs()) {
       int tm, tn;
       tile_coords_of(tile, p.tiles_m, p.tiles_n, tm, tn);
       const int64_t row = static_cast<int64_t>(tm) * kPairM + static_cast<int>(rank) * kTileM + r;
       const int f0 = tn * W + sub * NC;
-      const uint32_t acc = local & 1u;
-      const bool ok = pairs::warp_wait(&ss->tmem_full[acc], (local >> 1) & 1u, p, ss, lane);
+      const bool ok = pairs::warp_wait(&ss->tmem_full[acc], ph, p, ss, lane);
       if (CODES) {  // the quarter's warps meet below: they stop together
         if (ptx::bar_red_or(kQuarterBarrier + quarter, 128, !ok)) return;
         __syncwarp();
@@ -94,7 +62,7 @@ struct GatedOp {
         return;
       }
       ptx::tc_fence_after();
-      const uint32_t taddr = ss->tmem_base + (static_cast<uint32_t>(quarter * 32) << 16) + acc * kTileN +
+      const uint32_t taddr = ss->tmem_base + (static_cast<uint32_t>(quarter * 32) << 16) + acc * (kTmemCols / kBufs) +
                              static_cast<uint32_t>(sub * NC);
       float g[NC], u[NC];
       pairs::tmem_load<NC>(taddr, g);
@@ -102,6 +70,10 @@ struct GatedOp {
       ptx::tc_fence_before();
       __syncwarp();
       if (lane == 0) ptx::mbar_arrive_cluster_tmem(empty0 + acc * 8u);
+      if (++acc == kBufs) {
+        acc = 0;
+        ph ^= 1u;
+      }
       float gs = 0.f, us = 0.f;
       if (CODES) {
         float ga = 0.f, ua = 0.f;
@@ -170,27 +142,26 @@ template <int W, bool CODES>
 struct GatedGradOp {
   using Params = GatedParams;
   struct Maps { int unused; };
-  static constexpr int kW = W, kStg = 6, kEpiBytes = 0;
+  static constexpr int kW = W, kARows = kTileM, kStg = W == 128 ? 6 : 9, kBufs = W == 128 ? 2 : 4, kEpiWarps = 16, kEpiBytes = 0;
   static constexpr bool kFp8 = false, kBMajorMN = true, kBlockwise = false;
 
   static __device__ __forceinline__ int b_row(int tn, int rank, const Params&) { return (2 * tn + rank) * W; }
 
-  static __device__ __forceinline__ void epilogue(const Maps&, const Params& p, SharedState* ss, uint8_t*, int warp,
+  static __device__ __forceinline__ void epilogue(const Maps&, const Params& p, pairs::Shared* ss, uint8_t*, int warp,
                                                   int lane, uint32_t rank) {
     constexpr int NC = W / 2;  // features a warp takes
-    const int quarter = warp & 3, sub = (warp - 2) >> 2, r = quarter * 32 + lane;
+    const int quarter = warp & 3, sub = (warp - pairs::kFirstEpiWarp) >> 2, r = quarter * 32 + lane;
     const uint32_t empty0 = ptx::mapa(ptx::smem_addr(&ss->tmem_empty[0]), 0);
     const int NB = (p.F + codes::kBlock - 1) / codes::kBlock;
-    uint32_t local = 0;
-    for (int tile = pair_id(); tile < p.num_tiles; tile += num_pairs(), ++local) {
+    uint32_t acc = 0, ph = 0;
+    for (int tile = pair_id(); tile < p.num_tiles; tile += num_pairs()) {
       int tm, tn;
       tile_coords_of(tile, p.tiles_m, p.tiles_n, tm, tn);
       const int64_t row = static_cast<int64_t>(tm) * kPairM + static_cast<int>(rank) * kTileM + r;
       const int f0 = tn * 2 * W + sub * NC;
-      const uint32_t acc = local & 1u;
-      if (!pairs::warp_wait(&ss->tmem_full[acc], (local >> 1) & 1u, p, ss, lane)) return;
+      if (!pairs::warp_wait(&ss->tmem_full[acc], ph, p, ss, lane)) return;
       ptx::tc_fence_after();
-      const uint32_t taddr = ss->tmem_base + (static_cast<uint32_t>(quarter * 32) << 16) + acc * kTileN +
+      const uint32_t taddr = ss->tmem_base + (static_cast<uint32_t>(quarter * 32) << 16) + acc * (kTmemCols / kBufs) +
                              static_cast<uint32_t>(sub * NC);
       const bool live = row < p.T && f0 < p.F;
       float gs = 0.f, us = 0.f;
@@ -231,6 +202,10 @@ struct GatedGradOp {
       ptx::tc_fence_before();
       __syncwarp();
       if (lane == 0) ptx::mbar_arrive_cluster_tmem(empty0 + acc * 8u);
+      if (++acc == kBufs) {
+        acc = 0;
+        ph ^= 1u;
+      }
     }
   }
 };
@@ -240,6 +215,11 @@ struct GatedGradOp {
 cudaError_t launch_gated(int width, const CUtensorMap& x, const CUtensorMap& w, const GatedParams& p, int pairs_n,
                          cudaStream_t s) {
   if (p.codes != nullptr) return pairs::launch<GatedOp<128, true>>(x, w, {}, p, pairs_n, s);
+  if (p.T <= kShortRows) {
+    if (width == 128) return pairs::launch<GatedOp<128, false, kShortRows>>(x, w, {}, p, pairs_n, s);
+    if (width == 64) return pairs::launch<GatedOp<64, false, kShortRows>>(x, w, {}, p, pairs_n, s);
+    return pairs::launch<GatedOp<32, false, kShortRows>>(x, w, {}, p, pairs_n, s);
+  }
   if (width == 128) return pairs::launch<GatedOp<128, false>>(x, w, {}, p, pairs_n, s);
   if (width == 64) return pairs::launch<GatedOp<64, false>>(x, w, {}, p, pairs_n, s);
   return pairs::launch<GatedOp<32, false>>(x, w, {}, p, pairs_n, s);

@@ -165,6 +165,9 @@ int64_t norm_bwd_blocks(int64_t T, int K, int num_sms);
 // Activation kinds (values match forge_act_t).
 enum ActKind : int32_t { kActSilu = 0, kActGeluTanh = 1 };
 
+// Token rows up to which the pair kernels' ring holds that many of A (kARows).
+constexpr int kShortRows = 32;
+
 // What the kernels of pair_gemm.cuh have in common: 256-token rows of tiles,
 // `num_kb` ring stages of 128 bytes of the reduction.
 struct PairParams {
@@ -189,6 +192,9 @@ struct GatedParams : PairParams {
 // widths of 128 or 64).  With p.codes the forward takes 128.
 cudaError_t launch_gated(int width, const CUtensorMap& x, const CUtensorMap& w, const GatedParams& p, int pairs,
                          cudaStream_t s);
+// few_rows.cu: the forward of at most kFewGated rows, without codes.
+constexpr int64_t kFewGated = 32;
+cudaError_t launch_gated_few(const void* W, const void* X, const GatedParams& p, int K, cudaStream_t s);
 cudaError_t launch_gated_grad(int width, const CUtensorMap& dy, const CUtensorMap& w, const GatedParams& p, int pairs,
                               cudaStream_t s);
 
@@ -199,8 +205,12 @@ struct ProductParams : PairParams {
   const float* w_scale;    // [ceil(N / 128) x num_kb]
   void* Y;                 // bf16 [T x N]
 };
-cudaError_t launch_product(int width, const CUtensorMap& x, const CUtensorMap& w, const ProductParams& p, int pairs,
-                           cudaStream_t s);
+// y: 64-column x 32-row boxes, 128-byte swizzle (width 128; else any valid map).
+cudaError_t launch_product(int width, const CUtensorMap& x, const CUtensorMap& w, const CUtensorMap& y,
+                           const ProductParams& p, int pairs, cudaStream_t s);
+// few_rows.cu: the product of at most kFewProduct rows.
+constexpr int64_t kFewProduct = 32;
+cudaError_t launch_product_few(const void* W, const void* X, const ProductParams& p, int K, cudaStream_t s);
 
 // Values to E4M3 codes in blocks of 128 and back (codes.cu).
 struct CodesParams {

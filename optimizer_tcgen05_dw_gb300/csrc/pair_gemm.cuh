@@ -8,17 +8,29 @@
 //               W columns of B, 128 bytes of the reduction each (64 bf16 or 128
 //               E4M3 elements);
 //   warp 1      tcgen05.mma of the pair, 256 x 2 W x (16 or 32);
-//   warps 2..17 the epilogue, four warps to each 32-lane quarter of tensor memory.
+//   warps 4..   the epilogue, two or four warps to each 32-lane quarter of
+//               tensor memory (warps 2 and 3 idle: registers are dealt by
+//               warpgroups of four, and the epilogue has what the first gives up).
 // An operator (Op) says what its B rows are and what its epilogue does:
 //   Op::Params                    with PairParams as its base
 //   kW, kFp8, kBMajorMN           columns of B per CTA; E4M3 operands; B stored
 //                                 with its columns contiguous
 //   kBlockwise                    the accumulator is handed over after every
 //                                 stage (and starts from zero), not after a tile
-//   kStg, kEpiBytes, kMaps        ring stages, epilogue's shared memory
+//   kEpiWarps, kEpiBytes          the epilogue's warps (8 or 16) and shared memory
+//   kStg, kBufs                   ring stages, accumulators
+//   kARows                        128, or fewer token rows that a stage holds when
+//                                 there are no more: the stages of A then lie
+//                                 kARows rows apart, so the ring is deeper.  The
+//                                 instruction reads 128 rows all the same, the next
+//                                 stages' (or, in the second CTA, which loads no A,
+//                                 whatever lies there): rows of the accumulator that
+//                                 belong to no token, and rows do not mix.
+//   Maps                          tensor maps of the epilogue
 //   b_row(tile_n, rank, p)        first B row (or column) of this CTA's half
 //   epilogue(...)                 see pair_kernel
-// W narrower than 128 gives more and smaller units when there are few.
+// W narrower than 128 gives more and smaller units when there are few; the ring
+// then has more stages, so that as many bytes are on their way.
 #pragma once
 
 #include "launch.h"
@@ -27,105 +39,220 @@
 namespace forge {
 namespace pairs {
 
-constexpr int kEpiWarps = 16;
-constexpr int kThreads = 32 * (2 + kEpiWarps);
+constexpr int kFirstEpiWarp = 4;
+constexpr int kMaxStages = 24, kMaxBufs = 8;
 constexpr int kA = kTileM * 128;  // bytes of A per stage and CTA
+
+struct Shared {
+  uint64_t full[kMaxStages];
+  uint64_t empty[kMaxStages];
+  uint64_t tmem_full[kMaxBufs];
+  uint64_t tmem_empty[kMaxBufs];
+  uint64_t mma_done;
+  uint64_t epi_full[32];  // the epilogue warps' own copies
+  uint32_t tmem_base;
+  int32_t abort;
+};
+constexpr int kSharedBytes = 1024;
+static_assert(sizeof(Shared) <= kSharedBytes, "shared state region");
+
+// Bounded wait on an mbarrier phase.  Returns false if the CTA is aborting
+// or the wait expired (the first expiry records the timeout).
+__device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, const PairParams& p, Shared* ss,
+                                     bool honour_abort = true) {
+  if (ptx::mbar_try_wait(bar, parity)) return true;
+  const uint64_t t0 = ptx::global_timer_ns();
+  while (true) {
+    if (ptx::mbar_try_wait(bar, parity)) return true;
+    if (honour_abort && *reinterpret_cast<volatile int32_t*>(&ss->abort)) return false;
+    if (ptx::global_timer_ns() - t0 > p.wait_limit_ns) {
+      *reinterpret_cast<volatile int32_t*>(&ss->abort) = 1;
+      atomicCAS(p.status, 0u, static_cast<uint32_t>(kStatusTimeout));
+      return false;
+    }
+  }
+}
+
+// The same for a whole warp, which gets one verdict.  Every lane looks for
+// itself first (what it saw is then ordered before its own reads); only when
+// some lane saw nothing does lane 0 wait for all of them.
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, const PairParams& p, Shared* ss, int lane) {
+  if (__all_sync(0xFFFFFFFFu, ptx::mbar_try_wait(bar, parity))) return true;
+  const bool ok = __all_sync(0xFFFFFFFFu, lane != 0 || wait(bar, parity, p, ss));
+  __syncwarp();
+  return ok;
+}
 
 template <class Op>
 struct Layout {
   static constexpr int kBK = Op::kFp8 ? 128 : 64;
-  static constexpr int kB = Op::kW * 128;  // bytes of B per stage and CTA
-  static constexpr int kSmem = Op::kStg * (kA + kB) + Op::kEpiBytes + 512 + 1024;
+  static constexpr bool kShort = Op::kARows < kTileM;
+  static constexpr int kAStage = Op::kARows * 128;  // bytes of A per stage and CTA
+  static constexpr int kABytes = (Op::kStg - 1) * kAStage + kA;
+  static constexpr int kB = Op::kW * 128;           // of B
+  static constexpr uint32_t kTx = kShort ? kAStage + 2 * kB : 2 * (kAStage + kB);  // a stage's bytes, both CTAs'
+  static constexpr int kSmem = kABytes + Op::kStg * kB + Op::kEpiBytes + kSharedBytes + 1024;
   static_assert(kSmem <= 232448, "dynamic shared memory limit");
-  static_assert(Op::kStg <= 8, "barrier arrays");
+  static_assert(Op::kStg <= kMaxStages && Op::kBufs <= kMaxBufs, "barrier arrays");
+  static constexpr int kBufCols = kTmemCols / Op::kBufs;  // tensor-memory columns of an accumulator
+  static_assert(kBufCols >= 2 * Op::kW, "accumulators");
+  static_assert(Op::kEpiWarps == 8 || Op::kEpiWarps == 16, "two or four warps a quarter");
+  static constexpr int kThreads = 32 * (kFirstEpiWarp + Op::kEpiWarps);
+  // 65536 registers give 640 threads 96 each, and so they stay; of 384 threads'
+  // 168, three warpgroups' 504, the first keeps 56 and the epilogue's take 224
+  // (56 + 2 x 224 = 504).
+  static constexpr int kLoadRegs = 56, kEpiRegs = 224;
 };
 
+// One lane of the warp, which arrives converged.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t e;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(e));
+  return e != 0;
+}
+
+// Both roles below run on their whole warp, one lane elected for each copy or
+// instruction: addresses and descriptors are then the same in all lanes by
+// construction, and live in the uniform registers these instructions read.
+// (One lane alone in a branch had them moved there for every instruction: a
+// stage's four narrow instructions, its wait and its commit took 389 clocks to
+// issue, 212 so.)
 template <class Op>
-__device__ void producer(const CUtensorMap* mA, const CUtensorMap* mB, const typename Op::Params& p, uint8_t* smA,
-                         uint8_t* smB, SharedState* ss, uint32_t rank) {
-  constexpr int STG = Op::kStg, BK = Layout<Op>::kBK, kB = Layout<Op>::kB, W = Op::kW;
-  uint32_t it = 0, issued_mask = 0, last_parity = 0;
-  const uint32_t full0 = ptx::mapa(ptx::smem_addr(&ss->full[0]), 0);
+__device__ __forceinline__ void producer(const CUtensorMap* mA, const CUtensorMap* mB, const typename Op::Params& p,
+                                         uint8_t* smA, uint8_t* smB, Shared* ss, int lane, uint32_t rank) {
+  using L = Layout<Op>;
+  constexpr int STG = Op::kStg, BK = L::kBK, kB = L::kB, W = Op::kW;
+  uint32_t s = 0, ph = 0, issued_mask = 0, last_parity = 0;
+  const uint32_t full0 = ptx::mapa(ptx::smem_addr(&ss->full[0]), 0);  // the leader's barriers
   if (!p.skip_loads) {
     for (int tile = pair_id(); tile < p.num_tiles; tile += num_pairs()) {
       int tm, tn;
       tile_coords_of(tile, p.tiles_m, p.tiles_n, tm, tn);
       const int m0 = tm * kPairM + static_cast<int>(rank) * kTileM;
       const int b0 = Op::b_row(tn, static_cast<int>(rank), p);
-      for (int kb = 0; kb < p.num_kb; ++kb, ++it) {
-        const int s = static_cast<int>(it % STG);
-        const uint32_t ph = (it / STG) & 1u;
-        if (!bounded_wait(&ss->empty[s], ph ^ 1u, p, ss)) goto drain;
-        const uint32_t bar = full0 + static_cast<uint32_t>(s) * 8u;
-        if (rank == 0) ptx::mbar_arrive_expect_tx(&ss->full[s], 2u * (kA + kB));
+      for (int kb = 0; kb < p.num_kb; ++kb) {
+        if (!warp_wait(&ss->empty[s], ph ^ 1u, p, ss, lane)) goto drain;
+        const uint32_t bar = full0 + s * 8u;
+        uint8_t* a = smA + s * L::kAStage;
         uint8_t* b = smB + s * kB;
-        ptx::tma_load_2d_pair(mA, bar, smA + s * kA, kb * BK, m0);
-        if (!Op::kBMajorMN) {
-          ptx::tma_load_2d_pair(mB, bar, b, kb * BK, b0);
-        } else if (p.op3d) {  // [W / 64 column blocks][64 rows][64 columns] in one copy
-          ptx::tma_load_3d_pair(mB, bar, b, 0, kb * BK, b0 / 64);
-        } else {
+        if (elect_one()) {
+          if (rank == 0) ptx::mbar_arrive_expect_tx(&ss->full[s], L::kTx);
+          if (!L::kShort || rank == 0) ptx::tma_load_2d_pair(mA, bar, a, kb * BK, m0);
+          if (!Op::kBMajorMN) {
+            ptx::tma_load_2d_pair(mB, bar, b, kb * BK, b0);
+          } else if (p.op3d) {  // [W / 64 column blocks][64 rows][64 columns] in one copy
+            ptx::tma_load_3d_pair(mB, bar, b, 0, kb * BK, b0 / 64);
+          } else {
 #pragma unroll
-          for (int i = 0; i < W / 64; ++i) ptx::tma_load_2d_pair(mB, bar, b + i * 64 * BK * 2, b0 + 64 * i, kb * BK);
+            for (int i = 0; i < W / 64; ++i) ptx::tma_load_2d_pair(mB, bar, b + i * 64 * BK * 2, b0 + 64 * i, kb * BK);
+          }
         }
+        __syncwarp();
         issued_mask |= 1u << s;
         last_parity = (last_parity & ~(1u << s)) | (ph << s);
+        if (++s == STG) {
+          s = 0;
+          ph ^= 1u;
+        }
       }
     }
   }
 drain:
-  if (rank == 0)  // every issued copy lands before the pair can exit
-    for (int s = 0; s < STG; ++s)
-      if (issued_mask & (1u << s)) bounded_wait(&ss->full[s], (last_parity >> s) & 1u, p, ss, false);
+  if (rank == 0 && lane == 0)  // every issued copy lands before the pair can exit
+    for (int i = 0; i < STG; ++i)
+      if (issued_mask & (1u << i)) wait(&ss->full[i], (last_parity >> i) & 1u, p, ss, false);
+  __syncwarp();
+}
+
+// A stage's four instructions of the pair (32 bytes of the reduction each) and
+// the commits that free its ring stage and, with `last`, hand the accumulator
+// over.  The upper halves of the descriptors are constant; the lower ones
+// (address and leading offset) move by additions.
+template <bool FP8, uint32_t BSTEP>
+__device__ __forceinline__ void issue_stage(uint32_t d, uint32_t alo, uint32_t blo, uint32_t hi, uint32_t idesc, uint32_t add,
+                                            uint32_t empty, uint32_t full, uint32_t last) {
+#define FORGE_STAGE(KIND)                                                                                              \
+  asm volatile(                                                                                                        \
+      "{\n\t.reg .pred e, f, p, t;\n\t.reg .b64 a, b;\n\t.reg .b32 x, y;\n\t.reg .b16 m;\n\t"                            \
+      "mov.b16 m, 3;\n\tsetp.ne.b32 p, %5, 0;\n\tsetp.eq.u32 t, 0, 0;\n\telect.sync _|e, 0xffffffff;\n\t"              \
+      "setp.ne.and.b32 f, %8, 0, e;\n\t"                                                                               \
+      "mov.b64 a, {%1, %3};\n\tmov.b64 b, {%2, %3};\n\t@e tcgen05.mma.cta_group::2.kind::" KIND " [%0], a, b, %4, p;\n\t" \
+      "add.u32 x, %1, 2;\n\tadd.u32 y, %2, %9;\n\tmov.b64 a, {x, %3};\n\tmov.b64 b, {y, %3};\n\t"                    \
+      "@e tcgen05.mma.cta_group::2.kind::" KIND " [%0], a, b, %4, t;\n\t"                                             \
+      "add.u32 x, %1, 4;\n\tadd.u32 y, %2, %10;\n\tmov.b64 a, {x, %3};\n\tmov.b64 b, {y, %3};\n\t"                   \
+      "@e tcgen05.mma.cta_group::2.kind::" KIND " [%0], a, b, %4, t;\n\t"                                             \
+      "add.u32 x, %1, 6;\n\tadd.u32 y, %2, %11;\n\tmov.b64 a, {x, %3};\n\tmov.b64 b, {y, %3};\n\t"                   \
+      "@e tcgen05.mma.cta_group::2.kind::" KIND " [%0], a, b, %4, t;\n\t"                                             \
+      "@e tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%6], m;\n\t"       \
+      "@f tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%7], m;\n\t}"      \
+      ::"r"(d), "r"(alo), "r"(blo), "r"(hi), "r"(idesc), "r"(add), "r"(empty), "r"(full), "r"(last), "n"(BSTEP),       \
+      "n"(2 * BSTEP), "n"(3 * BSTEP)                                                                                   \
+      : "memory")
+  if constexpr (FP8) FORGE_STAGE("f8f6f4");
+  else FORGE_STAGE("f16");
+#undef FORGE_STAGE
 }
 
 // Leader CTA only.
 template <class Op>
-__device__ void mma(const typename Op::Params& p, uint8_t* smA, uint8_t* smB, SharedState* ss) {
-  constexpr int STG = Op::kStg, BK = Layout<Op>::kBK, kB = Layout<Op>::kB;
+__device__ __forceinline__ void mma(const typename Op::Params& p, uint8_t* smA, uint8_t* smB, Shared* ss, int lane) {
+  using L = Layout<Op>;
+  constexpr int STG = Op::kStg, BK = L::kBK;
   constexpr uint32_t idesc = Op::kFp8 ? ptx::idesc_e4m3_f32(kPairM, 2 * Op::kW)
                                       : ptx::idesc_bf16_f32(kPairM, 2 * Op::kW, false, Op::kBMajorMN);
-  uint32_t it = 0, use = 0;  // use: accumulators handed over
+  // 8-row (or 8-column-atom) groups 1 KiB apart; B stored by columns: atoms of
+  // 64 columns BK * 128 bytes apart, 16 rows of the reduction 2 KiB.
+  const uint64_t ad = ptx::smem_desc_sw128(ptx::smem_addr(smA), 16, 1024);
+  const uint64_t bd = ptx::smem_desc_sw128(ptx::smem_addr(smB), Op::kBMajorMN ? BK * 128 : 16, 1024);
+  const uint32_t alo = static_cast<uint32_t>(ad), blo = static_cast<uint32_t>(bd), hi = static_cast<uint32_t>(ad >> 32);
+  const uint32_t tmem = ss->tmem_base, empty0 = ptx::smem_addr(&ss->empty[0]), full0 = ptx::smem_addr(&ss->tmem_full[0]);
+  uint32_t s = 0, ph = 0, acc = 0, aph = 0;
   for (int tile = pair_id(); tile < p.num_tiles; tile += num_pairs()) {
-    for (int kb = 0; kb < p.num_kb; ++kb, ++it) {
-      const uint32_t acc = use & 1u;
-      if (Op::kBlockwise || kb == 0) {
-        if (!bounded_wait(&ss->tmem_empty[acc], ((use >> 1) & 1u) ^ 1u, p, ss)) goto done;
-        ptx::tc_fence_after();
-      }
-      const int s = static_cast<int>(it % STG);
-      if (!bounded_wait(&ss->full[s], (it / STG) & 1u, p, ss)) goto done;
+    for (int kb = 0; kb < p.num_kb; ++kb) {
+      if ((Op::kBlockwise || kb == 0) && !warp_wait(&ss->tmem_empty[acc], aph ^ 1u, p, ss, lane)) goto done;
+      if (!warp_wait(&ss->full[s], ph, p, ss, lane)) goto done;
       ptx::tc_fence_after();
-      const uint32_t d_tmem = ss->tmem_base + acc * kTileN;
-      const uint32_t a0 = ptx::smem_addr(smA + s * kA), b0 = ptx::smem_addr(smB + s * kB);
-#pragma unroll
-      for (int kk = 0; kk < 4; ++kk) {  // 32 bytes of the reduction an instruction
-        const uint64_t adesc = ptx::smem_desc_sw128(a0 + kk * 32, 16, 1024);
-        const uint64_t bdesc = Op::kBMajorMN ? ptx::smem_desc_sw128(b0 + kk * 2048, BK * 128, 1024)
-                                             : ptx::smem_desc_sw128(b0 + kk * 32, 16, 1024);
-        const uint32_t add = Op::kBlockwise ? (kk != 0 ? 1u : 0u) : ((kb | kk) != 0 ? 1u : 0u);
-        if (Op::kFp8) ptx::mma_e4m3_pair(d_tmem, adesc, bdesc, idesc, add);
-        else ptx::mma_bf16_pair(d_tmem, adesc, bdesc, idesc, add);
+      const bool last = Op::kBlockwise || kb == p.num_kb - 1;
+      issue_stage<Op::kFp8, Op::kBMajorMN ? 2048 / 16 : 2>(
+          tmem + acc * L::kBufCols, alo + s * (L::kAStage / 16), blo + s * (L::kB / 16), hi, idesc,
+          Op::kBlockwise || kb == 0 ? 0u : 1u, empty0 + s * 8u, full0 + acc * 8u, last ? 1u : 0u);
+      if (last && ++acc == Op::kBufs) {
+        acc = 0;
+        aph ^= 1u;
       }
-      ptx::mma_commit_pair_multicast(&ss->empty[s], 0x3);
-      if (Op::kBlockwise || kb == p.num_kb - 1) {
-        ptx::mma_commit_pair_multicast(&ss->tmem_full[acc], 0x3);
-        ++use;
+      if (++s == STG) {
+        s = 0;
+        ph ^= 1u;
       }
     }
   }
 done:
-  ptx::mma_commit_pair_multicast(&ss->mma_done, 0x1);
-  bounded_wait(&ss->mma_done, 0u, p, ss, false);
+  if (elect_one()) ptx::mma_commit_pair_multicast(&ss->mma_done, 0x1);
+  __syncwarp();
+  if (lane == 0) wait(&ss->mma_done, 0u, p, ss, false);
+  __syncwarp();
 }
 
-// A warp's wait: lane 0 waits, the warp gets its verdict together, and what
-// lane 0 saw is ordered before the other lanes' reads.
-template <class P>
-__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, const P& p, SharedState* ss, int lane) {
-  const bool ok = __all_sync(0xFFFFFFFFu, lane != 0 || bounded_wait(bar, parity, p, ss));
-  __syncwarp();
-  return ok;
+// Split form of a 32-column load: issued, and waited for by naming its registers.
+__device__ __forceinline__ void tmem_issue32(uint32_t taddr, uint32_t (&r)[32]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+      "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
+        "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
+        "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(taddr));
+}
+__device__ __forceinline__ void tmem_wait32(uint32_t (&r)[32]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]), "+r"(r[8]),
+                 "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]), "+r"(r[16]),
+                 "+r"(r[17]), "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]), "+r"(r[22]), "+r"(r[23]), "+r"(r[24]),
+                 "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]), "+r"(r[29]), "+r"(r[30]), "+r"(r[31])
+               :
+               : "memory");
 }
 
 // NC consecutive fp32 columns of this warp's 32 tensor-memory lanes.
@@ -138,7 +265,7 @@ __device__ __forceinline__ void tmem_load(uint32_t taddr, float (&v)[NC]) {
 }
 
 template <class Op>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(Layout<Op>::kThreads, 1)
     pair_kernel(const __grid_constant__ CUtensorMap mapA, const __grid_constant__ CUtensorMap mapB,
                 const __grid_constant__ typename Op::Maps maps, const typename Op::Params p) {
   using L = Layout<Op>;
@@ -146,20 +273,21 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint8_t* smem = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
   uint8_t* smA = smem;
-  uint8_t* smB = smem + Op::kStg * kA;
+  uint8_t* smB = smem + L::kABytes;
   uint8_t* epi = smB + Op::kStg * L::kB;
-  SharedState* ss = reinterpret_cast<SharedState*>(epi + Op::kEpiBytes);
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  Shared* ss = reinterpret_cast<Shared*>(epi + Op::kEpiBytes);
+  const int warp = __shfl_sync(0xFFFFFFFFu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;  // (the same in a warp's lanes)
   const uint32_t rank = ptx::cluster_ctarank();
   if (threadIdx.x == 0) {
     for (int s = 0; s < Op::kStg; ++s) {
       ptx::mbar_init(&ss->full[s], 1);
       ptx::mbar_init(&ss->empty[s], 1);
     }
-    for (int a = 0; a < 2; ++a) {
+    for (int a = 0; a < Op::kBufs; ++a) {
       ptx::mbar_init(&ss->tmem_full[a], 1);
-      ptx::mbar_init(&ss->tmem_empty[a], 2 * kEpiWarps);
+      ptx::mbar_init(&ss->tmem_empty[a], 2 * Op::kEpiWarps);
     }
+    for (int w = 0; w < 32; ++w) ptx::mbar_init(&ss->epi_full[w], 1);
     ptx::mbar_init(&ss->mma_done, 1);
     ss->abort = 0;
     ptx::fence_mbar_init();
@@ -176,11 +304,12 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   ptx::cluster_sync();  // both CTAs' barriers exist before either signals the other's
   ptx::tc_fence_after();
-  if (warp == 0) {
-    if (lane == 0) producer<Op>(&mapA, &mapB, p, smA, smB, ss, rank);
-  } else if (warp == 1) {
-    if (lane == 0 && rank == 0) mma<Op>(p, smA, smB, ss);
+  if (warp < kFirstEpiWarp) {
+    if (Op::kEpiWarps == 8) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(L::kLoadRegs));
+    if (warp == 0) producer<Op>(&mapA, &mapB, p, smA, smB, ss, lane, rank);
+    else if (warp == 1 && rank == 0) mma<Op>(p, smA, smB, ss, lane);
   } else {
+    if (Op::kEpiWarps == 8) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(L::kEpiRegs));
     Op::epilogue(maps, p, ss, epi, warp, lane, rank);
   }
   __syncwarp();
@@ -202,7 +331,7 @@ inline cudaError_t launch(const CUtensorMap& a, const CUtensorMap& b, const type
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(2 * pairs), 1, 1);
-  cfg.blockDim = dim3(kThreads, 1, 1);
+  cfg.blockDim = dim3(Layout<Op>::kThreads, 1, 1);
   cfg.dynamicSmemBytes = Layout<Op>::kSmem;
   cfg.stream = s;
   cudaLaunchAttribute attr[1];
