@@ -270,7 +270,7 @@ forge_status_t forge_linear_e4m3(const forge_linear_e4m3_t* lin, void* stream) {
                        CU_TENSOR_MAP_SWIZZLE_128B)) != FORGE_OK)
     return st;
   CUtensorMap my = mx;
-  if (width == 128 && (st = tensor_map(&my, lin->Y, kBf16, 2, N, T, 64, 32, CU_TENSOR_MAP_SWIZZLE_128B)) != FORGE_OK) return st;
+  if (width == 128 && (st = tensor_map(&my, lin->Y, kBf16, 2, N, T, 32, 32, CU_TENSOR_MAP_SWIZZLE_64B)) != FORGE_OK) return st;
   const cudaError_t e = launch_product(width, mx, mw, my, p, pairs_of(p, d), s);
   return e == cudaSuccess ? FORGE_OK : cuda_fail(e, "block-scaled product launch");
 }

@@ -33,14 +33,17 @@ struct GatedOp {
   static_assert(!CODES || W == codes::kBlock, "a block of the codes is a tile's features");
   using Params = GatedParams;
   struct Maps { int unused; };
-  static constexpr int kW = W, kARows = AROWS, kBufs = W == 128 ? 2 : 4, kEpiWarps = 16;
+  static constexpr int kW = W, kARows = AROWS, kBufs = W == 128 ? 2 : 4, kSplit = 1;
   static constexpr int kStg = AROWS < kTileM ? (W == 128 ? 10 : W == 64 ? 16 : 24) : (W == 128 ? 6 : W == 64 ? 9 : 11);
   static constexpr int kEpiBytes = CODES ? 2 * 4 * kTileM * 4 : 0;
-  static constexpr bool kFp8 = false, kBMajorMN = false, kBlockwise = false;
+  static constexpr bool kMoreRegs = false, kFp8 = false, kBMajorMN = false, kBlockwise = false;
 
   // rank 0: gate rows, rank 1: up rows of the same features (rows of another
   // half past a ragged end give columns that are not stored)
   static __device__ __forceinline__ int b_row(int tn, int rank, const Params& p) { return rank * p.F + tn * W; }
+
+  static __device__ __forceinline__ void init_barriers(pairs::Shared*) {}
+  static __device__ __forceinline__ void helper(const Params&, pairs::Shared*, uint8_t*, int, int, uint32_t) {}
 
   static __device__ __forceinline__ void epilogue(const Maps&, const Params& p, pairs::Shared* ss, uint8_t* epi, int warp,
                                                   int lane, uint32_t rank) {
@@ -142,10 +145,13 @@ template <int W, bool CODES>
 struct GatedGradOp {
   using Params = GatedParams;
   struct Maps { int unused; };
-  static constexpr int kW = W, kARows = kTileM, kStg = W == 128 ? 6 : 9, kBufs = W == 128 ? 2 : 4, kEpiWarps = 16, kEpiBytes = 0;
-  static constexpr bool kFp8 = false, kBMajorMN = true, kBlockwise = false;
+  static constexpr int kW = W, kARows = kTileM, kStg = W == 128 ? 6 : 9, kBufs = W == 128 ? 2 : 4, kSplit = 1, kEpiBytes = 0;
+  static constexpr bool kMoreRegs = false, kFp8 = false, kBMajorMN = true, kBlockwise = false;
 
   static __device__ __forceinline__ int b_row(int tn, int rank, const Params&) { return (2 * tn + rank) * W; }
+
+  static __device__ __forceinline__ void init_barriers(pairs::Shared*) {}
+  static __device__ __forceinline__ void helper(const Params&, pairs::Shared*, uint8_t*, int, int, uint32_t) {}
 
   static __device__ __forceinline__ void epilogue(const Maps&, const Params& p, pairs::Shared* ss, uint8_t*, int warp,
                                                   int lane, uint32_t rank) {

@@ -205,7 +205,7 @@ struct ProductParams : PairParams {
   const float* w_scale;    // [ceil(N / 128) x num_kb]
   void* Y;                 // bf16 [T x N]
 };
-// y: 64-column x 32-row boxes, 128-byte swizzle (width 128; else any valid map).
+// y: 32-column x 32-row boxes, 64-byte swizzle (width 128; else any valid map).
 cudaError_t launch_product(int width, const CUtensorMap& x, const CUtensorMap& w, const CUtensorMap& y,
                            const ProductParams& p, int pairs, cudaStream_t s);
 // few_rows.cu: the product of at most kFewProduct rows.

@@ -8,17 +8,23 @@
 //               W columns of B, 128 bytes of the reduction each (64 bf16 or 128
 //               E4M3 elements);
 //   warp 1      tcgen05.mma of the pair, 256 x 2 W x (16 or 32);
-//   warps 4..   the epilogue, two or four warps to each 32-lane quarter of
-//               tensor memory (warps 2 and 3 idle: registers are dealt by
-//               warpgroups of four, and the epilogue has what the first gives up).
+//   warps 2, 3  what an operator has for them (Op::helper);
+//   warps 4..19 the epilogue, four warps to each 32-lane quarter of tensor
+//               memory (registers are dealt by warpgroups of four, and the
+//               epilogue may have what the first gives up).
 // An operator (Op) says what its B rows are and what its epilogue does:
 //   Op::Params                    with PairParams as its base
 //   kW, kFp8, kBMajorMN           columns of B per CTA; E4M3 operands; B stored
 //                                 with its columns contiguous
 //   kBlockwise                    the accumulator is handed over after every
 //                                 stage (and starts from zero), not after a tile
-//   kEpiWarps, kEpiBytes          the epilogue's warps (8 or 16) and shared memory
+//   kEpiBytes, kMoreRegs          the epilogue's shared memory; whether it takes
+//                                 registers from the first warpgroup
 //   kStg, kBufs                   ring stages, accumulators
+//   kSplit                        2: a stage is multiplied in two halves of W
+//                                 columns, an accumulator each (columns [0, W / 2)
+//                                 are of this CTA's half of B's rows, or the other's
+//                                 for the next), so that more of them are under way
 //   kARows                        128, or fewer token rows that a stage holds when
 //                                 there are no more: the stages of A then lie
 //                                 kARows rows apart, so the ring is deeper.  The
@@ -28,7 +34,8 @@
 //                                 belong to no token, and rows do not mix.
 //   Maps                          tensor maps of the epilogue
 //   b_row(tile_n, rank, p)        first B row (or column) of this CTA's half
-//   epilogue(...)                 see pair_kernel
+//   epilogue(...), helper(...)    see pair_kernel
+//   init_barriers(ss)             the epilogue's own mbarriers (Shared::epi)
 // W narrower than 128 gives more and smaller units when there are few; the ring
 // then has more stages, so that as many bytes are on their way.
 #pragma once
@@ -39,7 +46,7 @@
 namespace forge {
 namespace pairs {
 
-constexpr int kFirstEpiWarp = 4;
+constexpr int kEpiWarps = 16, kFirstEpiWarp = 4;
 constexpr int kMaxStages = 24, kMaxBufs = 8;
 constexpr int kA = kTileM * 128;  // bytes of A per stage and CTA
 
@@ -49,7 +56,7 @@ struct Shared {
   uint64_t tmem_full[kMaxBufs];
   uint64_t tmem_empty[kMaxBufs];
   uint64_t mma_done;
-  uint64_t epi_full[32];  // the epilogue warps' own copies
+  uint64_t epi[32];  // the epilogue's own
   uint32_t tmem_base;
   int32_t abort;
 };
@@ -73,11 +80,22 @@ __device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, const PairP
   }
 }
 
+// try_wait without a time to suspend for: 15 clocks where the phase is over, 50 with.
+__device__ __forceinline__ bool try_once(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok) : "r"(bar), "r"(parity) : "memory");
+  return ok != 0;
+}
+
 // The same for a whole warp, which gets one verdict.  Every lane looks for
 // itself first (what it saw is then ordered before its own reads); only when
 // some lane saw nothing does lane 0 wait for all of them.
 __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, const PairParams& p, Shared* ss, int lane) {
-  if (__all_sync(0xFFFFFFFFu, ptx::mbar_try_wait(bar, parity))) return true;
+  if (__all_sync(0xFFFFFFFFu, try_once(ptx::smem_addr(bar), parity))) return true;
   const bool ok = __all_sync(0xFFFFFFFFu, lane != 0 || wait(bar, parity, p, ss));
   __syncwarp();
   return ok;
@@ -95,13 +113,12 @@ struct Layout {
   static_assert(kSmem <= 232448, "dynamic shared memory limit");
   static_assert(Op::kStg <= kMaxStages && Op::kBufs <= kMaxBufs, "barrier arrays");
   static constexpr int kBufCols = kTmemCols / Op::kBufs;  // tensor-memory columns of an accumulator
-  static_assert(kBufCols >= 2 * Op::kW, "accumulators");
-  static_assert(Op::kEpiWarps == 8 || Op::kEpiWarps == 16, "two or four warps a quarter");
-  static constexpr int kThreads = 32 * (kFirstEpiWarp + Op::kEpiWarps);
-  // 65536 registers give 640 threads 96 each, and so they stay; of 384 threads'
-  // 168, three warpgroups' 504, the first keeps 56 and the epilogue's take 224
-  // (56 + 2 x 224 = 504).
-  static constexpr int kLoadRegs = 56, kEpiRegs = 224;
+  static_assert(kBufCols * Op::kSplit >= 2 * Op::kW && Op::kBufs % Op::kSplit == 0, "accumulators");
+  static_assert(Op::kSplit == 1 || (Op::kBlockwise && !Op::kBMajorMN), "halves of a stage");
+  static constexpr int kThreads = 32 * (kFirstEpiWarp + kEpiWarps);
+  // 65536 registers give 640 threads 96 each, five warpgroups 480; kMoreRegs:
+  // the first keeps 32 and the epilogue's take 112 (32 + 4 x 112 = 480).
+  static constexpr int kLoadRegs = 32, kEpiRegs = 112;
 };
 
 // One lane of the warp, which arrives converged.
@@ -165,17 +182,17 @@ drain:
 }
 
 // A stage's four instructions of the pair (32 bytes of the reduction each) and
-// the commits that free its ring stage and, with `last`, hand the accumulator
-// over.  The upper halves of the descriptors are constant; the lower ones
+// the commits that free its ring stage (with `free`) and hand the accumulator
+// over (with `last`).  The upper halves of the descriptors are constant; the lower ones
 // (address and leading offset) move by additions.
 template <bool FP8, uint32_t BSTEP>
 __device__ __forceinline__ void issue_stage(uint32_t d, uint32_t alo, uint32_t blo, uint32_t hi, uint32_t idesc, uint32_t add,
-                                            uint32_t empty, uint32_t full, uint32_t last) {
+                                            uint32_t empty, uint32_t full, uint32_t free, uint32_t last) {
 #define FORGE_STAGE(KIND)                                                                                              \
   asm volatile(                                                                                                        \
-      "{\n\t.reg .pred e, f, p, t;\n\t.reg .b64 a, b;\n\t.reg .b32 x, y;\n\t.reg .b16 m;\n\t"                            \
+      "{\n\t.reg .pred e, f, g, p, t;\n\t.reg .b64 a, b;\n\t.reg .b32 x, y;\n\t.reg .b16 m;\n\t"                            \
       "mov.b16 m, 3;\n\tsetp.ne.b32 p, %5, 0;\n\tsetp.eq.u32 t, 0, 0;\n\telect.sync _|e, 0xffffffff;\n\t"              \
-      "setp.ne.and.b32 f, %8, 0, e;\n\t"                                                                               \
+      "setp.ne.and.b32 f, %8, 0, e;\n\tsetp.ne.and.b32 g, %12, 0, e;\n\t"                                              \
       "mov.b64 a, {%1, %3};\n\tmov.b64 b, {%2, %3};\n\t@e tcgen05.mma.cta_group::2.kind::" KIND " [%0], a, b, %4, p;\n\t" \
       "add.u32 x, %1, 2;\n\tadd.u32 y, %2, %9;\n\tmov.b64 a, {x, %3};\n\tmov.b64 b, {y, %3};\n\t"                    \
       "@e tcgen05.mma.cta_group::2.kind::" KIND " [%0], a, b, %4, t;\n\t"                                             \
@@ -183,10 +200,10 @@ __device__ __forceinline__ void issue_stage(uint32_t d, uint32_t alo, uint32_t b
       "@e tcgen05.mma.cta_group::2.kind::" KIND " [%0], a, b, %4, t;\n\t"                                             \
       "add.u32 x, %1, 6;\n\tadd.u32 y, %2, %11;\n\tmov.b64 a, {x, %3};\n\tmov.b64 b, {y, %3};\n\t"                   \
       "@e tcgen05.mma.cta_group::2.kind::" KIND " [%0], a, b, %4, t;\n\t"                                             \
-      "@e tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%6], m;\n\t"       \
+      "@g tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%6], m;\n\t"       \
       "@f tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%7], m;\n\t}"      \
       ::"r"(d), "r"(alo), "r"(blo), "r"(hi), "r"(idesc), "r"(add), "r"(empty), "r"(full), "r"(last), "n"(BSTEP),       \
-      "n"(2 * BSTEP), "n"(3 * BSTEP)                                                                                   \
+      "n"(2 * BSTEP), "n"(3 * BSTEP), "r"(free)                                                                        \
       : "memory")
   if constexpr (FP8) FORGE_STAGE("f8f6f4");
   else FORGE_STAGE("f16");
@@ -198,7 +215,7 @@ template <class Op>
 __device__ __forceinline__ void mma(const typename Op::Params& p, uint8_t* smA, uint8_t* smB, Shared* ss, int lane) {
   using L = Layout<Op>;
   constexpr int STG = Op::kStg, BK = L::kBK;
-  constexpr uint32_t idesc = Op::kFp8 ? ptx::idesc_e4m3_f32(kPairM, 2 * Op::kW)
+  constexpr uint32_t idesc = Op::kFp8 ? ptx::idesc_e4m3_f32(kPairM, 2 * Op::kW / Op::kSplit)
                                       : ptx::idesc_bf16_f32(kPairM, 2 * Op::kW, false, Op::kBMajorMN);
   // 8-row (or 8-column-atom) groups 1 KiB apart; B stored by columns: atoms of
   // 64 columns BK * 128 bytes apart, 16 rows of the reduction 2 KiB.
@@ -209,16 +226,20 @@ __device__ __forceinline__ void mma(const typename Op::Params& p, uint8_t* smA, 
   uint32_t s = 0, ph = 0, acc = 0, aph = 0;
   for (int tile = pair_id(); tile < p.num_tiles; tile += num_pairs()) {
     for (int kb = 0; kb < p.num_kb; ++kb) {
-      if ((Op::kBlockwise || kb == 0) && !warp_wait(&ss->tmem_empty[acc], aph ^ 1u, p, ss, lane)) goto done;
-      if (!warp_wait(&ss->full[s], ph, p, ss, lane)) goto done;
-      ptx::tc_fence_after();
       const bool last = Op::kBlockwise || kb == p.num_kb - 1;
-      issue_stage<Op::kFp8, Op::kBMajorMN ? 2048 / 16 : 2>(
-          tmem + acc * L::kBufCols, alo + s * (L::kAStage / 16), blo + s * (L::kB / 16), hi, idesc,
-          Op::kBlockwise || kb == 0 ? 0u : 1u, empty0 + s * 8u, full0 + acc * 8u, last ? 1u : 0u);
-      if (last && ++acc == Op::kBufs) {
-        acc = 0;
-        aph ^= 1u;
+#pragma unroll
+      for (uint32_t h = 0; h < Op::kSplit; ++h) {
+        if ((Op::kBlockwise || kb == 0) && !warp_wait(&ss->tmem_empty[acc], aph ^ 1u, p, ss, lane)) goto done;
+        if (h == 0 && !warp_wait(&ss->full[s], ph, p, ss, lane)) goto done;
+        ptx::tc_fence_after();
+        issue_stage<Op::kFp8, Op::kBMajorMN ? 2048 / 16 : 2>(
+            tmem + acc * L::kBufCols, alo + s * (L::kAStage / 16), blo + s * (L::kB / 16) + h * (L::kB / Op::kSplit / 16), hi,
+            idesc, Op::kBlockwise || kb == 0 ? 0u : 1u, empty0 + s * 8u, full0 + acc * 8u, h == Op::kSplit - 1 ? 1u : 0u,
+            last ? 1u : 0u);
+        if (last && ++acc == Op::kBufs) {
+          acc = 0;
+          aph ^= 1u;
+        }
       }
       if (++s == STG) {
         s = 0;
@@ -233,27 +254,15 @@ done:
   __syncwarp();
 }
 
-// Split form of a 32-column load: issued, and waited for by naming its registers.
-__device__ __forceinline__ void tmem_issue32(uint32_t taddr, uint32_t (&r)[32]) {
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
-      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
-      "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
-        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
-        "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
-        "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
-      : "r"(taddr));
+// Four bytes global -> shared, without a register on the way, and an arrival on
+// `bar` (counted in its expected arrivals) when this thread's copies so far are there.
+__device__ __forceinline__ void copy4(uint32_t to, const float* from) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(to), "l"(from) : "memory");
 }
-__device__ __forceinline__ void tmem_wait32(uint32_t (&r)[32]) {
-  asm volatile("tcgen05.wait::ld.sync.aligned;"
-               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]), "+r"(r[8]),
-                 "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]), "+r"(r[16]),
-                 "+r"(r[17]), "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]), "+r"(r[22]), "+r"(r[23]), "+r"(r[24]),
-                 "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]), "+r"(r[29]), "+r"(r[30]), "+r"(r[31])
-               :
-               : "memory");
+__device__ __forceinline__ void arrive_when_copied(uint64_t* bar) {
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(ptx::smem_addr(bar)) : "memory");
 }
+__device__ __forceinline__ void copies_wait() { asm volatile("cp.async.wait_all;" ::: "memory"); }
 
 // NC consecutive fp32 columns of this warp's 32 tensor-memory lanes.
 template <int NC>
@@ -285,9 +294,9 @@ __global__ void __launch_bounds__(Layout<Op>::kThreads, 1)
     }
     for (int a = 0; a < Op::kBufs; ++a) {
       ptx::mbar_init(&ss->tmem_full[a], 1);
-      ptx::mbar_init(&ss->tmem_empty[a], 2 * Op::kEpiWarps);
+      ptx::mbar_init(&ss->tmem_empty[a], 2 * kEpiWarps / Op::kSplit);
     }
-    for (int w = 0; w < 32; ++w) ptx::mbar_init(&ss->epi_full[w], 1);
+    Op::init_barriers(ss);
     ptx::mbar_init(&ss->mma_done, 1);
     ss->abort = 0;
     ptx::fence_mbar_init();
@@ -305,11 +314,12 @@ __global__ void __launch_bounds__(Layout<Op>::kThreads, 1)
   ptx::cluster_sync();  // both CTAs' barriers exist before either signals the other's
   ptx::tc_fence_after();
   if (warp < kFirstEpiWarp) {
-    if (Op::kEpiWarps == 8) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(L::kLoadRegs));
+    if (Op::kMoreRegs) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(L::kLoadRegs));
     if (warp == 0) producer<Op>(&mapA, &mapB, p, smA, smB, ss, lane, rank);
-    else if (warp == 1 && rank == 0) mma<Op>(p, smA, smB, ss, lane);
+    else if (warp >= 2) Op::helper(p, ss, epi, warp, lane, rank);
+    else if (rank == 0) mma<Op>(p, smA, smB, ss, lane);
   } else {
-    if (Op::kEpiWarps == 8) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(L::kEpiRegs));
+    if (Op::kMoreRegs) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(L::kEpiRegs));
     Op::epilogue(maps, p, ss, epi, warp, lane, rank);
   }
   __syncwarp();

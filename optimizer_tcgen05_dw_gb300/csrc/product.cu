@@ -4,9 +4,8 @@
 //
 // The inner sum is one ring stage on the tensor cores (128 E4M3 of the
 // reduction: 128-byte rows), float32 in tensor memory; the outer one is kept in
-// registers: after every stage the accumulator changes hands, and eight
-// epilogue warps of each CTA fold it in with the block's factor while the next
-// stage fills the other one.
+// registers: after every stage the accumulator changes hands, and the epilogue
+// warps fold it in with the block's factor while the next ones are filled.
 #include <cuda_bf16.h>
 
 #include "codes.cuh"
@@ -16,131 +15,181 @@ namespace forge {
 
 namespace {
 
-using dev::f2;
-
-__device__ __forceinline__ f2 fma2(f2 a, f2 b, f2 c) {
-  f2 r;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
-  return r;
-}
-
-__device__ __forceinline__ f2 mul2(f2 a, f2 b) { return dev::mul(a, b); }
-
-// A warp holds 32 token rows x W columns of the sum in registers.  The row
-// is a lane of tensor memory and the columns lie in one block of W's scales, so
-// a lane has one factor a stage.
+// An epilogue warp holds 32 token rows (the lanes of its quarter of tensor
+// memory) x W / 2 columns of the sum in registers.  What it does besides folding is
+// kept small, as it is this loop that the tensor cores wait for: the scales come
+// through shared memory, kGroup stages at a time, by asynchronous copies of the
+// two helper warps (a lane's loads of its own row, a line each, took 300 ns and
+// more every few stages; registers to wait in there are none).
+// At W = 128 a stage is multiplied in two halves (kSplit), each with accumulators
+// of its own, so that four are under way: an accumulator's way through commit,
+// epilogue and back is longer than the instructions of two.
 template <int W, int AROWS = kTileM>
 struct ProductOp {
   using Params = ProductParams;
   struct Maps { CUtensorMap y; };
-  static constexpr int kW = W, kARows = AROWS, kBufs = 256 / W, kEpiWarps = 8;
-  static constexpr int kStg = AROWS < kTileM ? (W == 128 ? 10 : W == 64 ? 16 : 24) : (W == 128 ? 5 : W == 64 ? 8 : 10);
-  static constexpr int NC = W;                              // columns a warp holds
+  static constexpr int kW = W, kARows = AROWS, kSplit = W == 128 ? 2 : 1, kBufs = W == 32 ? 8 : 4, kEpiWarps = pairs::kEpiWarps;
+  static constexpr int kStg = AROWS < kTileM ? (W == 128 ? 9 : W == 64 ? 14 : 22) : (W == 128 ? 5 : W == 64 ? 8 : 10);
+  static constexpr int NC = W / 2, LD = NC < 32 ? NC : 32;     // columns a warp holds, and takes at a time
+  static constexpr int kBlk = W == 128 ? 2 : 1;                // blocks of W's scales they lie in
   static constexpr bool kStaged = W == 128 && AROWS == kTileM;
-  static constexpr int kStage = kStaged ? 32 * NC * 2 : 0;  // bytes a warp stages its rows in
-  static constexpr int kEpiBytes = kEpiWarps * kStage;
-  static constexpr bool kFp8 = true, kBMajorMN = false, kBlockwise = true;
+  static constexpr int kStage = kStaged ? 32 * LD * 2 : 0;     // bytes a warp stages its rows in
+  static constexpr int kGroup = 4, kSlots = 4;                 // stages in a slot of scales, slots
+  static constexpr int kStageFloats = kTileM + kBlk;           // a stage's scales: 128 rows', W's blocks'
+  static constexpr int kSlotFloats = kGroup * kStageFloats;
+  static constexpr int kEpiBytes = kEpiWarps * kStage + ((kSlots * kSlotFloats * 4 + 127) & ~127);
+  static constexpr bool kMoreRegs = true, kFp8 = true, kBMajorMN = false, kBlockwise = true;
 
   static __device__ __forceinline__ int b_row(int tn, int rank, const Params&) { return (2 * tn + rank) * W; }
 
-  // acc += v times the block's factor f = xs ws (codes::factor where that is not
-  // an ordinary number in some lane).
-  static __device__ __forceinline__ void fold(f2* acc, const uint32_t (&v)[32], float f, float xs, float ws, bool ordinary) {
-    if (ordinary) {
-#pragma unroll
-      for (int j = 0; j < 16; ++j)
-        acc[j] = fma2(dev::pair(__uint_as_float(v[2 * j]), __uint_as_float(v[2 * j + 1])), dev::pair(f, f), acc[j]);
-    } else {
-      const codes::Factor c = codes::factor(xs, ws);
-#pragma unroll
-      for (int j = 0; j < 16; ++j)
-        acc[j] = fma2(mul2(dev::pair(__uint_as_float(v[2 * j]), __uint_as_float(v[2 * j + 1])), dev::pair(c.p, c.p)),
-                      dev::pair(c.f, c.f), acc[j]);
+  static __device__ __forceinline__ void init_barriers(pairs::Shared* ss) {
+    for (int i = 0; i < kSlots; ++i) {
+      ptx::mbar_init(&ss->epi[i], 64);                  // a slot's scales are there: both helper warps' lanes
+      ptx::mbar_init(&ss->epi[kSlots + i], kEpiWarps);  // and have been read
     }
+  }
+  static __device__ __forceinline__ float* scales(uint8_t* epi) { return reinterpret_cast<float*>(epi + kEpiWarps * kStage); }
+
+  // Helper warp 2 + i copies the scales of rows 64 i .. 64 i + 63, two a lane.
+  // Rows and columns past the end repeat the last one's; nothing of theirs is stored.
+  static __device__ __forceinline__ void helper(const Params& p, pairs::Shared* ss, uint8_t* epi, int warp, int lane,
+                                                uint32_t rank) {
+    const int row = (warp - 2) * 64 + lane;
+    const uint32_t out = ptx::smem_addr(scales(epi)) + row * 4;
+    int slot = 0;
+    uint32_t ph = 0;
+    for (int tile = pair_id(); tile < p.num_tiles; tile += num_pairs()) {
+      int tm, tn;
+      tile_coords_of(tile, p.tiles_m, p.tiles_n, tm, tn);
+      const int row0 = tm * kPairM + static_cast<int>(rank) * kTileM + row;
+      const float* sx0 = p.x_scale + static_cast<int64_t>(min(row0, p.T - 1)) * p.num_kb;
+      const float* sx1 = p.x_scale + static_cast<int64_t>(min(row0 + 32, p.T - 1)) * p.num_kb;
+      const float* sw = p.w_scale + static_cast<int64_t>(min(tn * 2 * W + (lane % kBlk) * W, p.N - 1) / codes::kBlock) * p.num_kb;
+      for (int kb = 0; kb < p.num_kb; kb += kGroup) {
+        if (!pairs::warp_wait(&ss->epi[kSlots + slot], ph ^ 1u, p, ss, lane)) {
+          pairs::copies_wait();
+          return;
+        }
+        const uint32_t to = out + slot * kSlotFloats * 4;
+#pragma unroll
+        for (int j = 0; j < kGroup; ++j)
+          if (kb + j < p.num_kb) {
+            pairs::copy4(to + j * kStageFloats * 4, sx0 + kb + j);
+            pairs::copy4(to + (j * kStageFloats + 32) * 4, sx1 + kb + j);
+          }
+        if (warp == 2 && lane < kGroup * kBlk && kb + lane / kBlk < p.num_kb)
+          pairs::copy4(out + (slot * kSlotFloats + (lane / kBlk) * kStageFloats + kTileM + lane % kBlk - lane) * 4, sw + kb + lane / kBlk);
+        pairs::arrive_when_copied(&ss->epi[slot]);
+        if (++slot == kSlots) {
+          slot = 0;
+          ph ^= 1u;
+        }
+      }
+    }
+    pairs::copies_wait();
+  }
+
+  // acc += v f; where some lane's factor is not an ordinary number, in two parts.
+  // (One column an instruction: in pairs every value was moved once more, to
+  // where a pair of registers begins, and a block took 173 instructions of the
+  // multiply pipe in place of 128.)
+  static __device__ __forceinline__ void fold(float* acc, const float (&v)[LD], float f) {
+#pragma unroll
+    for (int j = 0; j < LD; ++j) acc[j] = fmaf(v[j], f, acc[j]);
+  }
+  static __device__ __forceinline__ void fold_wide(float* acc, const float (&v)[LD], const Params& p, int row, int col, int kb) {
+    const codes::Factor c = codes::factor(p.x_scale[static_cast<int64_t>(min(row, p.T - 1)) * p.num_kb + kb],
+                                          p.w_scale[static_cast<int64_t>(min(col, p.N - 1) / codes::kBlock) * p.num_kb + kb]);
+#pragma unroll
+    for (int j = 0; j < LD; ++j) acc[j] = fmaf(v[j] * c.p, c.f, acc[j]);
   }
 
   static __device__ __forceinline__ void epilogue(const Maps& maps, const Params& p, pairs::Shared* ss, uint8_t* epi,
                                                   int warp, int lane, uint32_t rank) {
-    const int quarter = warp & 3, sub = (warp - pairs::kFirstEpiWarp) >> 2;
+    constexpr int kBufCols = pairs::Layout<ProductOp>::kBufCols;
+    const int quarter = warp & 3, w = warp - pairs::kFirstEpiWarp, sub = w >> 2;
+    // With kSplit, warps 2 h and 2 h + 1 of a quarter take half h: 64 columns in each block of W's scales.
+    const int half = kSplit == 2 ? sub >> 1 : 0, blk = kSplit == 2 ? sub & 1 : 0;
+    const int first = kSplit == 2 ? blk * W + half * NC : sub * NC;  // its first column of the tile
     const uint32_t empty0 = ptx::mapa(ptx::smem_addr(&ss->tmem_empty[0]), 0);
-    const uint32_t tbase = ss->tmem_base + (static_cast<uint32_t>(quarter * 32) << 16) + static_cast<uint32_t>(sub * NC);
-    uint8_t* stage = epi + (warp - pairs::kFirstEpiWarp) * kStage;
-    uint32_t buf = 0, ph = 0;
+    const uint32_t tbase = ss->tmem_base + (static_cast<uint32_t>(quarter * 32) << 16) +
+                           static_cast<uint32_t>(kSplit == 2 ? blk * NC : sub * NC);
+    uint8_t* stage = epi + w * kStage;
+    const float* own = scales(epi) + quarter * 32 + lane;
+    uint32_t buf = half, ph = 0, slot_ph = 0;
+    int slot = 0;
     for (int tile = pair_id(); tile < p.num_tiles; tile += num_pairs()) {
       int tm, tn;
       tile_coords_of(tile, p.tiles_m, p.tiles_n, tm, tn);
-      const int row0 = tm * kPairM + static_cast<int>(rank) * kTileM + quarter * 32, col = tn * 2 * W + sub * NC;
-      const bool live = row0 < p.T && col < p.N;  // else the warp hands the accumulators on unread
-      // rows past the end repeat the last one's scales; nothing of theirs is stored
-      const float* sx = p.x_scale + static_cast<int64_t>(min(row0 + lane, p.T - 1)) * p.num_kb;
-      const float* sw = p.w_scale + static_cast<int64_t>(min(col, p.N - 1) / codes::kBlock) * p.num_kb;
-      f2 acc[NC / 2];
+      const int row0 = tm * kPairM + static_cast<int>(rank) * kTileM + quarter * 32, col0 = tn * 2 * W + first;
+      const bool live = row0 < p.T && col0 < p.N;  // else the warp hands the accumulators on unread
+      float acc[NC];
 #pragma unroll
-      for (int i = 0; i < NC / 2; ++i) acc[i] = dev::pair(0.f, 0.f);
-      float ax = sx[0], aw = sw[0];
-      for (int kb = 0; kb < p.num_kb; ++kb) {
-        const float xs = ax, ws = aw;
-        const float f = xs * ws;
-        if (kb + 1 < p.num_kb) {
-          ax = sx[kb + 1];
-          aw = sw[kb + 1];
+      for (int i = 0; i < NC; ++i) acc[i] = 0.f;
+#pragma unroll 1
+      for (int kb0 = 0; kb0 < p.num_kb; kb0 += kGroup) {
+        if (!pairs::warp_wait(&ss->epi[slot], slot_ph, p, ss, lane)) return;
+        const float* at = own + slot * kSlotFloats;
+        float f[kGroup];
+        bool mine = true;
+#pragma unroll
+        for (int j = 0; j < kGroup; ++j) {
+          f[j] = at[j * kStageFloats] * (at - own + scales(epi))[j * kStageFloats + kTileM + blk];
+          mine = mine && ((f[j] > 0x1p-100f && f[j] < 0x1p100f) || kb0 + j >= p.num_kb);
         }
-        const bool ordinary = __all_sync(0xFFFFFFFFu, f > 0x1p-100f && f < 0x1p100f);
-        if (!pairs::warp_wait(&ss->tmem_full[buf], ph, p, ss, lane)) return;
-        ptx::tc_fence_after();
-        if (live) {
-          const uint32_t taddr = tbase + buf * pairs::Layout<ProductOp>::kBufCols;
-          uint32_t v[2][32];
-          pairs::tmem_issue32(taddr, v[0]);
-          pairs::tmem_wait32(v[0]);
+        const bool wide = !__all_sync(0xFFFFFFFFu, mine);
+        __syncwarp();  // the slot has been read
+        if (lane == 0) ptx::mbar_arrive(&ss->epi[kSlots + slot]);
+        if (++slot == kSlots) {
+          slot = 0;
+          slot_ph ^= 1u;
+        }
 #pragma unroll
-          for (int h = 0; h < NC / 32; ++h) {
-            if (h + 1 < NC / 32) pairs::tmem_issue32(taddr + (h + 1) * 32, v[(h + 1) & 1]);
-            if (h + 1 == NC / 32) {  // all of it is in registers
+        for (int j = 0; j < kGroup; ++j) {
+          if (kb0 + j >= p.num_kb) break;
+          if (!pairs::warp_wait(&ss->tmem_full[buf], ph, p, ss, lane)) return;
+          ptx::tc_fence_after();
+          const uint32_t taddr = tbase + buf * kBufCols;
+#pragma unroll
+          for (int c = 0; c < NC / LD; ++c) {
+            float v[LD];
+            pairs::tmem_load<LD>(taddr + c * LD, v);
+            if (c == NC / LD - 1) {  // all of it is in registers
               ptx::tc_fence_before();
-              __syncwarp();
               if (lane == 0) ptx::mbar_arrive_cluster_tmem(empty0 + buf * 8u);
             }
-            fold(acc + h * 16, v[h & 1], f, xs, ws, ordinary);
-            if (h + 1 < NC / 32) pairs::tmem_wait32(v[(h + 1) & 1]);
+            if (!wide) fold(acc + c * LD, v, f[j]);
+            else fold_wide(acc + c * LD, v, p, row0 + lane, col0, kb0 + j);
           }
-        } else {
-          ptx::tc_fence_before();
-          __syncwarp();
-          if (lane == 0) ptx::mbar_arrive_cluster_tmem(empty0 + buf * 8u);
-        }
-        if (++buf == kBufs) {
-          buf = 0;
-          ph ^= 1u;
+          buf += kSplit;
+          if (buf >= kBufs) {
+            buf -= kBufs;
+            ph ^= 1u;
+          }
         }
       }
       if constexpr (kStaged) {
-        // 32 rows x 64 columns of bf16 a copy: 128-byte rows
-        if (lane == 0) ptx::bulk_wait_group_read0();  // the last tile's copies have read them
-        __syncwarp();
+        // 32 rows x 32 columns of bf16 a copy: 64-byte rows, one half of the columns after the other
 #pragma unroll
-        for (int i = 0; i < NC / 8; ++i) {
-          float v[8];
+        for (int h = 0; h < NC / LD; ++h) {
+          if (lane == 0) ptx::bulk_wait_group_read0();  // the last copy has read them
+          __syncwarp();
 #pragma unroll
-          for (int j = 0; j < 4; ++j) dev::unpair(acc[i * 4 + j], v[2 * j], v[2 * j + 1]);
-          *reinterpret_cast<uint4*>(stage + (i >> 3) * 4096 + sw128(lane, i & 7)) = pack_rne_bf16x8(v);
-        }
-        ptx::fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0 && live) {
-          ptx::tma_store_2d(&maps.y, stage, col, row0);
-          if (col + 64 < p.N) ptx::tma_store_2d(&maps.y, stage + 4096, col + 64, row0);
-          ptx::bulk_commit_group();
+          for (int i = 0; i < LD / 8; ++i)
+            *reinterpret_cast<uint4*>(stage + sw64(lane, i)) = pack_rne_bf16x8(reinterpret_cast<const float(&)[8]>(acc[h * LD + i * 8]));
+          ptx::fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0 && live && col0 + h * LD < p.N) {
+            ptx::tma_store_2d(&maps.y, stage, col0 + h * LD, row0);
+            ptx::bulk_commit_group();
+          }
         }
       } else if (row0 + lane < p.T) {
-        uint16_t* out = static_cast<uint16_t*>(p.Y) + static_cast<int64_t>(row0 + lane) * p.N + col;
+        uint16_t* out = static_cast<uint16_t*>(p.Y) + static_cast<int64_t>(row0 + lane) * p.N + col0;
 #pragma unroll
         for (int i = 0; i < NC / 8; ++i) {
-          if (col + i * 8 >= p.N) break;
-          float v[8];
-#pragma unroll
-          for (int j = 0; j < 4; ++j) dev::unpair(acc[i * 4 + j], v[2 * j], v[2 * j + 1]);
-          *reinterpret_cast<uint4*>(out + i * 8) = pack_rne_bf16x8(v);
+          if (col0 + i * 8 >= p.N) break;
+          *reinterpret_cast<uint4*>(out + i * 8) = pack_rne_bf16x8(reinterpret_cast<const float(&)[8]>(acc[i * 8]));
         }
       }
     }
