@@ -67,74 +67,45 @@ __device__ __forceinline__ uint16_t bf16_bits(float v) {
 
 // ---------------------------------------------------------------- gated
 
-// Features 8 MT blockIdx.x .. of up to 8 NT tokens.  The gate's rows are rows
-// 0-7 of the instruction and the up projection's rows 8-15, so a lane holds
-// both projections of a feature.
-template <int MT, int NT, int AHEAD>
+// Features 8 blockIdx.x .. of up to 8 tokens.  The gate's rows are rows 0-7 of
+// the instruction and the up projection's rows 8-15, so a lane holds both
+// projections of a feature.
 __global__ void __launch_bounds__(kThreads) gated_few_kernel(const uint16_t* W, const uint16_t* X, const GatedParams p,
                                                              const int K) {
-  constexpr int kTok = 8 * NT, kRow = 16 * MT;
-  __shared__ float s_sum[kWarps * kTok * kRow];
+  constexpr int kTok = 8;
+  __shared__ float s_sum[kWarps * kTok * 16];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, q = lane & 3;
-  const int V = K >> 3, f0 = blockIdx.x * 8 * MT;
-  const uint4 *wg[MT], *wu[MT], *x[NT];
-  float acc[MT][NT][4];
-#pragma unroll
-  for (int m = 0; m < MT; ++m) {
-    const int64_t f = min(f0 + 8 * m + g, p.F - 1);
-    wg[m] = reinterpret_cast<const uint4*>(W + f * K);
-    wu[m] = reinterpret_cast<const uint4*>(W + (p.F + f) * K);
-#pragma unroll
-    for (int i = 0; i < NT; ++i)
-#pragma unroll
-      for (int j = 0; j < 4; ++j) acc[m][i][j] = 0.f;
-  }
-#pragma unroll
-  for (int i = 0; i < NT; ++i) x[i] = reinterpret_cast<const uint4*>(X + static_cast<int64_t>(min(8 * i + g, p.T - 1)) * K);
+  const int V = K >> 3, f0 = blockIdx.x * 8;
+  const int64_t f_own = min(f0 + g, p.F - 1);
+  const uint4* wg = reinterpret_cast<const uint4*>(W + f_own * K);
+  const uint4* wu = reinterpret_cast<const uint4*>(W + (p.F + f_own) * K);
+  const uint4* x = reinterpret_cast<const uint4*>(X + static_cast<int64_t>(min(g, p.T - 1)) * K);
+  float acc[4] = {0.f, 0.f, 0.f, 0.f};
   const uint4 zero = make_uint4(0, 0, 0, 0);
-#pragma unroll AHEAD
+#pragma unroll 2
   for (int v = warp * 4 + q; v - q < V; v += kWarps * 4) {  // uniform over the warp
     const bool in = v < V;
-    uint4 a[MT], b[MT];
-#pragma unroll
-    for (int m = 0; m < MT; ++m) {
-      a[m] = in ? ld_once(wg[m] + v) : zero;
-      b[m] = in ? ld_once(wu[m] + v) : zero;
-    }
-#pragma unroll
-    for (int i = 0; i < NT; ++i) {
-      const uint4 t = in ? x[i][v] : zero;
-#pragma unroll
-      for (int m = 0; m < MT; ++m) {
-        mma_bf16(acc[m][i], a[m].x, b[m].x, a[m].y, b[m].y, t.x, t.y);
-        mma_bf16(acc[m][i], a[m].z, b[m].z, a[m].w, b[m].w, t.z, t.w);
-      }
-    }
+    const uint4 a = in ? ld_once(wg + v) : zero, b = in ? ld_once(wu + v) : zero, t = in ? x[v] : zero;
+    mma_bf16(acc, a.x, b.x, a.y, b.y, t.x, t.y);
+    mma_bf16(acc, a.z, b.z, a.w, b.w, t.z, t.w);
   }
   // [warp][token][gate's features, then the up projection's]
 #pragma unroll
-  for (int m = 0; m < MT; ++m)
-#pragma unroll
-    for (int i = 0; i < NT; ++i)
-#pragma unroll
-      for (int j = 0; j < 4; ++j)
-        s_sum[(warp * kTok + 8 * i + 2 * q + (j & 1)) * kRow + (j >> 1) * (8 * MT) + 8 * m + g] = acc[m][i][j];
+  for (int j = 0; j < 4; ++j) s_sum[(warp * kTok + 2 * q + (j & 1)) * 16 + (j >> 1) * 8 + g] = acc[j];
   __syncthreads();
-  for (int o = threadIdx.x; o < kTok * 8 * MT; o += kThreads) {
-    const int t = o / (8 * MT), c = o % (8 * MT), f = f0 + c;
-    if (t >= p.T || f >= p.F) continue;
-    float gate = 0.f, up = 0.f;
+  const int t = threadIdx.x >> 3, c = threadIdx.x & 7, f = f0 + c;
+  if (t >= p.T || t >= kTok || f >= p.F) return;
+  float gate = 0.f, up = 0.f;
 #pragma unroll
-    for (int w = 0; w < kWarps; ++w) {
-      gate += s_sum[(w * kTok + t) * kRow + c];
-      up += s_sum[(w * kTok + t) * kRow + 8 * MT + c];
-    }
-    static_cast<uint16_t*>(p.Y)[static_cast<int64_t>(t) * p.F + f] = bf16_bits(gated(p.act, gate, up));
-    if (p.gu != nullptr) {
-      uint16_t* kept = static_cast<uint16_t*>(p.gu) + static_cast<int64_t>(t) * 2 * p.F + f;
-      kept[0] = bf16_bits(gate);
-      kept[p.F] = bf16_bits(up);
-    }
+  for (int w = 0; w < kWarps; ++w) {
+    gate += s_sum[(w * kTok + t) * 16 + c];
+    up += s_sum[(w * kTok + t) * 16 + 8 + c];
+  }
+  static_cast<uint16_t*>(p.Y)[static_cast<int64_t>(t) * p.F + f] = bf16_bits(gated(p.act, gate, up));
+  if (p.gu != nullptr) {
+    uint16_t* kept = static_cast<uint16_t*>(p.gu) + static_cast<int64_t>(t) * 2 * p.F + f;
+    kept[0] = bf16_bits(gate);
+    kept[p.F] = bf16_bits(up);
   }
 }
 
@@ -221,13 +192,6 @@ __global__ void __launch_bounds__(kThreads) product_few_kernel(const uint8_t* W,
   }
 }
 
-template <int MT, int NT>
-cudaError_t run_gated(const void* W, const void* X, const GatedParams& p, int K, cudaStream_t s) {
-  const unsigned grid = static_cast<unsigned>((p.F + 8 * MT - 1) / (8 * MT));
-  gated_few_kernel<MT, NT, 4><<<grid, kThreads, 0, s>>>(static_cast<const uint16_t*>(W), static_cast<const uint16_t*>(X), p, K);
-  return cudaGetLastError();
-}
-
 template <int NT>
 cudaError_t run_product(const void* W, const void* X, const ProductParams& p, int K, cudaStream_t s) {
   const unsigned grid = static_cast<unsigned>((p.N + 15) / 16);
@@ -238,9 +202,9 @@ cudaError_t run_product(const void* W, const void* X, const ProductParams& p, in
 }  // namespace
 
 cudaError_t launch_gated_few(const void* W, const void* X, const GatedParams& p, int K, cudaStream_t s) {
-  if (p.T <= 8) return run_gated<1, 1>(W, X, p, K, s);
-  if (p.T <= 16) return run_gated<2, 2>(W, X, p, K, s);
-  return run_gated<2, 4>(W, X, p, K, s);
+  const unsigned grid = static_cast<unsigned>((p.F + 7) / 8);
+  gated_few_kernel<<<grid, kThreads, 0, s>>>(static_cast<const uint16_t*>(W), static_cast<const uint16_t*>(X), p, K);
+  return cudaGetLastError();
 }
 
 cudaError_t launch_product_few(const void* W, const void* X, const ProductParams& p, int K, cudaStream_t s) {

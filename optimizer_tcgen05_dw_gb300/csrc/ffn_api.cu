@@ -78,6 +78,16 @@ forge_status_t check_tiles(int64_t rows, int64_t cols, int64_t narrowest) {
     return fail(FORGE_ERR_UNSUPPORTED, "too many output tiles (%lld x %lld)", (long long)rows, (long long)cols);
   return FORGE_OK;
 }
+// A tensor [T x 2F] as [T x 2 x F], in boxes of 32 features of both halves of 32
+// rows (so that a ragged end of the first half is an end).
+forge_status_t halves_map(CUtensorMap* m, const void* base, CUtensorMapDataType dtype, int esize, int64_t T, int64_t F,
+                          CUtensorMapSwizzle swizzle) {
+  const cuuint64_t dims[3] = {static_cast<cuuint64_t>(F), 2, static_cast<cuuint64_t>(T)};
+  const cuuint64_t strides[2] = {static_cast<cuuint64_t>(F) * esize, static_cast<cuuint64_t>(F) * 2 * esize};
+  const cuuint32_t box[3] = {32, 2, 32};
+  return tensor_map_nd(m, base, dtype, 3, dims, strides, box, swizzle);
+}
+
 // Token rows of a copy of the A operand.
 uint32_t box_rows(int64_t T) { return T <= kShortRows ? kShortRows : kTileM; }
 int pairs_of(const PairParams& p, const DeviceInfo& d) { return p.num_tiles < d.num_sms / 2 ? p.num_tiles : d.num_sms / 2; }
@@ -198,7 +208,13 @@ forge_status_t forge_gated_dgrad(const forge_gated_grad_t* g, void* stream) {
     st = tensor_map(&mw, g->Wd, kBf16, 2, F, N, 64, kBlockK, CU_TENSOR_MAP_SWIZZLE_128B);
   }
   if (st != FORGE_OK) return st;
-  const cudaError_t e = launch_gated_grad(width, my, mw, p, pairs_of(p, d), static_cast<cudaStream_t>(stream));
+  CUtensorMap kept = my, dgu, y = my;
+  if ((st = halves_map(&dgu, g->dGU, kBf16, 2, T, F, CU_TENSOR_MAP_SWIZZLE_64B)) != FORGE_OK) return st;
+  if (g->gu != nullptr) st = halves_map(&kept, g->gu, kBf16, 2, T, F, CU_TENSOR_MAP_SWIZZLE_64B);
+  else if (F % 16 == 0) st = halves_map(&kept, g->gu_codes, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, T, F, CU_TENSOR_MAP_SWIZZLE_32B);
+  if (st != FORGE_OK) return st;
+  if (g->Y != nullptr && (st = tensor_map(&y, g->Y, kBf16, 2, F, T, 32, 32, CU_TENSOR_MAP_SWIZZLE_64B)) != FORGE_OK) return st;
+  const cudaError_t e = launch_gated_grad(width, my, mw, kept, dgu, y, p, pairs_of(p, d), static_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? FORGE_OK : cuda_fail(e, "gated gradient launch");
 }
 
@@ -213,7 +229,7 @@ forge_status_t forge_quantize_e4m3(const void* x, int32_t x_dtype, void* codes, 
   DeviceInfo d;
   if ((st = ready(&d)) != FORGE_OK) return st;
   const CodesParams p = {x, static_cast<uint8_t*>(codes), scale, rows, cols, block_rows != 1};
-  const cudaError_t e = launch_quantize_e4m3(x_dtype == FORGE_G_FP32, p, d.num_sms, static_cast<cudaStream_t>(stream));
+  const cudaError_t e = launch_quantize_e4m3(x_dtype == FORGE_G_FP32, p, static_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? FORGE_OK : cuda_fail(e, "quantise launch");
 }
 
@@ -228,7 +244,7 @@ forge_status_t forge_dequantize_e4m3(const void* codes, const float* scale, void
   DeviceInfo d;
   if ((st = ready(&d)) != FORGE_OK) return st;
   const CodesParams p = {x, static_cast<uint8_t*>(const_cast<void*>(codes)), const_cast<float*>(scale), rows, cols, block_rows != 1};
-  const cudaError_t e = launch_dequantize_e4m3(x_dtype == FORGE_G_FP32, p, d.num_sms, static_cast<cudaStream_t>(stream));
+  const cudaError_t e = launch_dequantize_e4m3(x_dtype == FORGE_G_FP32, p, static_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? FORGE_OK : cuda_fail(e, "dequantise launch");
 }
 

@@ -24,6 +24,9 @@ namespace forge {
 
 namespace {
 
+// Byte offset of 16-byte chunk c of row r in a box of 32-byte rows stored with the 32-byte swizzle.
+__device__ __forceinline__ uint32_t sw32(int r, int c) { return static_cast<uint32_t>(r * 32 + ((c ^ ((r >> 2) & 1)) << 4)); }
+
 constexpr int kQuarterBarrier = 2;  // + 0 .. 3: the four warps of a tensor-memory quarter
 
 // ---------------------------------------------------------------- forward
@@ -131,7 +134,7 @@ struct GatedOp {
           if (f0 + 8 * j >= p.F) break;
           float v[8];
 #pragma unroll
-          for (int i = 0; i < 8; ++i) v[i] = gated(p.act, g[8 * j + i], u[8 * j + i]);
+          for (int i = 0; i < 8; ++i) v[i] = gated(p.act, g[8 * j + i], u[8 * j + i]);  // (the branch is uniform)
           *reinterpret_cast<uint4*>(y + 8 * j) = pack_rne_bf16x8(v);
         }
       }
@@ -141,70 +144,123 @@ struct GatedOp {
 
 // ---------------------------------------------------------------- gradient
 
-template <int W, bool CODES>
+// What was kept is read and dGU and Y are written through shared memory by the
+// tensor-memory accelerator, chunk by chunk, every warp its own 32 rows x 32
+// features: a row is a lane, so direct accesses would touch 32 lines an
+// instruction (16384 x 14336 through 4096: 1946 us so, %STAGED% staged).  A warp's
+// first chunk of a tile is loaded while the tile's products are formed; the
+// chunks' [gate, up] lie side by side in one box ([row][gate, up][32 features]),
+// and dG and dU replace what they came from.
+// Codes with F % 16 != 0, whose rows the accelerator cannot address, are loaded
+// directly (VIA false).
+template <int W, bool CODES, bool VIA>
 struct GatedGradOp {
   using Params = GatedParams;
-  struct Maps { int unused; };
-  static constexpr int kW = W, kARows = kTileM, kStg = W == 128 ? 6 : 9, kBufs = W == 128 ? 2 : 4, kSplit = 1, kEpiBytes = 0;
+  struct Maps { CUtensorMap kept, dgu, y; };
+  static constexpr int kW = W, kARows = kTileM, kStg = W == 128 ? 4 : 5, kBufs = W == 128 ? 2 : 4, kSplit = 1;
+  static constexpr int NC = W / 2, kChunk = 32;        // features a warp takes, and at a time
+  static constexpr int kPair = 32 * 2 * kChunk * 2;    // bytes of a chunk of dG and dU (and of G and U in bf16)
+  static constexpr int kOne = 32 * kChunk * 2;         // of Y (and of G's and U's codes together)
+  static constexpr int kEpiBytes = pairs::kEpiWarps * (kPair + kOne);
   static constexpr bool kMoreRegs = false, kFp8 = false, kBMajorMN = true, kBlockwise = false;
 
   static __device__ __forceinline__ int b_row(int tn, int rank, const Params&) { return (2 * tn + rank) * W; }
-
-  static __device__ __forceinline__ void init_barriers(pairs::Shared*) {}
+  static __device__ __forceinline__ void init_barriers(pairs::Shared* ss) {
+    for (int i = 0; i < pairs::kEpiWarps; ++i) ptx::mbar_init(&ss->epi[i], 1);
+  }
   static __device__ __forceinline__ void helper(const Params&, pairs::Shared*, uint8_t*, int, int, uint32_t) {}
 
-  static __device__ __forceinline__ void epilogue(const Maps&, const Params& p, pairs::Shared* ss, uint8_t*, int warp,
-                                                  int lane, uint32_t rank) {
-    constexpr int NC = W / 2;  // features a warp takes
-    const int quarter = warp & 3, sub = (warp - pairs::kFirstEpiWarp) >> 2, r = quarter * 32 + lane;
+  static __device__ __forceinline__ void epilogue(const Maps& maps, const Params& p, pairs::Shared* ss, uint8_t* epi,
+                                                  int warp, int lane, uint32_t rank) {
+    const int quarter = warp & 3, w = warp - pairs::kFirstEpiWarp, sub = w >> 2;
     const uint32_t empty0 = ptx::mapa(ptx::smem_addr(&ss->tmem_empty[0]), 0);
     const int NB = (p.F + codes::kBlock - 1) / codes::kBlock;
-    uint32_t acc = 0, ph = 0;
-    for (int tile = pair_id(); tile < p.num_tiles; tile += num_pairs()) {
+    // Both buffers have 128 and 64 bytes a row, and a lane touches its own row's alone.
+    uint8_t* both = epi + w * (kPair + kOne);  // [row][gate, up][32] bf16, 64-byte swizzle
+    uint8_t* one = both + kPair;               // [row][32] bf16, 64-byte swizzle; or codes [row][gate, up][32], 32-byte swizzle
+    uint64_t* bar = &ss->epi[w];
+    uint32_t acc = 0, ph = 0, kept_ph = 0;
+    auto origin = [&](int tile, int& row0, int& f0) {
       int tm, tn;
       tile_coords_of(tile, p.tiles_m, p.tiles_n, tm, tn);
-      const int64_t row = static_cast<int64_t>(tm) * kPairM + static_cast<int>(rank) * kTileM + r;
-      const int f0 = tn * 2 * W + sub * NC;
-      if (!pairs::warp_wait(&ss->tmem_full[acc], ph, p, ss, lane)) return;
+      row0 = tm * kPairM + static_cast<int>(rank) * kTileM + quarter * 32;
+      f0 = tn * 2 * W + sub * NC;
+    };
+    // Begins the load of what was kept for the chunk at (row0, f); whether there is any of it.
+    auto load = [&](int row0, int f) -> bool {
+      const bool any = row0 < p.T && f < p.F;
+      if (VIA && any && lane == 0) {
+        ptx::mbar_arrive_expect_tx(bar, CODES ? kOne : kPair);
+        ptx::tma_load_3d(&maps.kept, bar, CODES ? one : both, f, 0, row0);
+      }
+      return VIA && any;
+    };
+    bool loaded = false;  // a load is under way
+    for (int tile = pair_id(); tile < p.num_tiles; tile += num_pairs()) {
+      int row0, f0;
+      origin(tile, row0, f0);
+      if (!loaded) loaded = load(row0, f0);
+      if (!pairs::warp_wait(&ss->tmem_full[acc], ph, p, ss, lane)) break;
       ptx::tc_fence_after();
       const uint32_t taddr = ss->tmem_base + (static_cast<uint32_t>(quarter * 32) << 16) + acc * (kTmemCols / kBufs) +
                              static_cast<uint32_t>(sub * NC);
-      const bool live = row < p.T && f0 < p.F;
-      float gs = 0.f, us = 0.f;
-      if (CODES && live) {
-        gs = p.scale[row * 2 * NB + f0 / codes::kBlock];
-        us = p.scale[(row * 2 + 1) * NB + f0 / codes::kBlock];
-      }
+      const int64_t row = row0 + lane;
+      bool ok = true;
 #pragma unroll 1
-      for (int c = 0; c < NC; c += 8) {
-        float da[8];
-        pairs::tmem_load<8>(taddr + c, da);
-        if (row >= p.T || f0 + c >= p.F) continue;
-        const int64_t at = row * 2 * p.F + f0 + c;
-        float g[8], u[8], y[8];
-        if (CODES) {
-          const uint2 gc = *reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(p.codes) + at);
-          const uint2 uc = *reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(p.codes) + at + p.F);
+      for (int c = 0; c < NC && row0 < p.T && f0 + c < p.F; c += kChunk) {
+        const int f = f0 + c;
+        float gs = 0.f, us = 0.f;
+        if (CODES && row < p.T) {
+          gs = p.scale[row * 2 * NB + f / codes::kBlock];
+          us = p.scale[(row * 2 + 1) * NB + f / codes::kBlock];
+        }
+        uint4 gc[2], uc[2];  // CODES: this row's
+        if (VIA) {
+          if (!(ok = pairs::warp_wait(bar, kept_ph, p, ss, lane))) break;
+          kept_ph ^= 1u;
+          loaded = false;
+          if (CODES) {
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const float2 a = codes::decode2((j < 2 ? gc.x : gc.y) >> (16 * (j & 1)));
-            const float2 b = codes::decode2((j < 2 ? uc.x : uc.y) >> (16 * (j & 1)));
-            g[2 * j] = a.x * gs;
-            g[2 * j + 1] = a.y * gs;
-            u[2 * j] = b.x * us;
-            u[2 * j + 1] = b.y * us;
+            for (int h = 0; h < 2; ++h) {
+              gc[h] = *reinterpret_cast<const uint4*>(one + sw32(2 * lane, h));
+              uc[h] = *reinterpret_cast<const uint4*>(one + sw32(2 * lane + 1, h));
+            }
           }
         } else {
-          load_bf16x8(p.gu, at, g);
-          load_bf16x8(p.gu, at + p.F, u);
-        }
 #pragma unroll
-        for (int j = 0; j < 8; ++j) gated_gradient(p.act, da[j], g[j], u[j], g[j], u[j], y[j]);
-        // (dGU may be gu itself: this thread alone reads and writes these eight of each)
-        store_bf16x8_rne(p.dGU, at, g);
-        store_bf16x8_rne(p.dGU, at + p.F, u);
-        if (p.Y != nullptr) store_bf16x8_rne(p.Y, row * p.F + f0 + c, y);
+          for (int h = 0; h < 4; ++h) {
+            uint2 a = make_uint2(0, 0), b = a;
+            if (row < p.T && f + 8 * h < p.F) {
+              const uint8_t* at = static_cast<const uint8_t*>(p.codes) + row * 2 * p.F + f + 8 * h;
+              a = *reinterpret_cast<const uint2*>(at);
+              b = *reinterpret_cast<const uint2*>(at + p.F);
+            }
+            (h & 1 ? gc[h >> 1].z : gc[h >> 1].x) = a.x;
+            (h & 1 ? gc[h >> 1].w : gc[h >> 1].y) = a.y;
+            (h & 1 ? uc[h >> 1].z : uc[h >> 1].x) = b.x;
+            (h & 1 ? uc[h >> 1].w : uc[h >> 1].y) = b.y;
+          }
+        }
+        float da[kChunk];
+        pairs::tmem_load<kChunk>(taddr + c, da);
+        if (p.act == kActSilu) gradients<kActSilu>(da, gc, uc, gs, us, both, one, lane);
+        else gradients<kActGeluTanh>(da, gc, uc, gs, us, both, one, lane);
+        ptx::fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+          ptx::tma_store_3d(&maps.dgu, both, f, 0, row0);
+          if (p.Y != nullptr) ptx::tma_store_2d(&maps.y, one, f, row0);
+          ptx::bulk_commit_group();
+          ptx::bulk_wait_group_read0();  // before either buffer is filled again
+        }
+        __syncwarp();
+        // The next chunk: this tile's, or else the next tile's first.
+        int next_row = row0, next_f = f + kChunk;
+        const bool more = c + kChunk < NC && next_f < p.F;
+        if (!more && tile + num_pairs() < p.num_tiles) origin(tile + num_pairs(), next_row, next_f);
+        if (more || tile + num_pairs() < p.num_tiles) loaded = load(next_row, next_f);
       }
+      if (!ok) break;
       ptx::tc_fence_before();
       __syncwarp();
       if (lane == 0) ptx::mbar_arrive_cluster_tmem(empty0 + acc * 8u);
@@ -212,6 +268,42 @@ struct GatedGradOp {
         acc = 0;
         ph ^= 1u;
       }
+    }
+    if (lane == 0) {
+      if (loaded) pairs::wait(bar, kept_ph, p, ss, false);  // (a load begun before the block gave up)
+      ptx::bulk_wait_group0();
+    }
+    __syncwarp();
+  }
+
+  // A lane's 32 features: dG and dU over G and U, and Y.
+  template <int ACT>
+  static __device__ __forceinline__ void gradients(const float (&da)[kChunk], const uint4 (&gc)[2], const uint4 (&uc)[2], float gs,
+                                                   float us, uint8_t* both, uint8_t* one, int lane) {
+#pragma unroll
+    for (int q = 0; q < kChunk / 8; ++q) {
+      float g[8], u[8], y[8];
+      if (CODES) {
+        decode8(q & 1 ? make_uint2(gc[q >> 1].z, gc[q >> 1].w) : make_uint2(gc[q >> 1].x, gc[q >> 1].y), gs, g);
+        decode8(q & 1 ? make_uint2(uc[q >> 1].z, uc[q >> 1].w) : make_uint2(uc[q >> 1].x, uc[q >> 1].y), us, u);
+      } else {
+        unpack_bf16x8(*reinterpret_cast<const uint4*>(both + sw64(2 * lane, q)), g);
+        unpack_bf16x8(*reinterpret_cast<const uint4*>(both + sw64(2 * lane + 1, q)), u);
+      }
+#pragma unroll
+      for (int j = 0; j < 8; ++j) gated_gradient<ACT>(da[8 * q + j], g[j], u[j], g[j], u[j], y[j]);
+      *reinterpret_cast<uint4*>(both + sw64(2 * lane, q)) = pack_rne_bf16x8(g);
+      *reinterpret_cast<uint4*>(both + sw64(2 * lane + 1, q)) = pack_rne_bf16x8(u);
+      *reinterpret_cast<uint4*>(one + sw64(lane, q)) = pack_rne_bf16x8(y);
+    }
+  }
+
+  static __device__ __forceinline__ void decode8(uint2 c, float scale, float (&v)[8]) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const float2 d = codes::decode2((j < 2 ? c.x : c.y) >> (16 * (j & 1)));
+      v[2 * j] = d.x * scale;
+      v[2 * j + 1] = d.y * scale;
     }
   }
 };
@@ -231,14 +323,17 @@ cudaError_t launch_gated(int width, const CUtensorMap& x, const CUtensorMap& w, 
   return pairs::launch<GatedOp<32, false>>(x, w, {}, p, pairs_n, s);
 }
 
-cudaError_t launch_gated_grad(int width, const CUtensorMap& dy, const CUtensorMap& w, const GatedParams& p, int pairs_n,
-                              cudaStream_t s) {
-  const bool kept8 = p.codes != nullptr;
-  if (width == 128)
-    return kept8 ? pairs::launch<GatedGradOp<128, true>>(dy, w, {}, p, pairs_n, s)
-                 : pairs::launch<GatedGradOp<128, false>>(dy, w, {}, p, pairs_n, s);
-  return kept8 ? pairs::launch<GatedGradOp<64, true>>(dy, w, {}, p, pairs_n, s)
-               : pairs::launch<GatedGradOp<64, false>>(dy, w, {}, p, pairs_n, s);
+template <int W>
+static cudaError_t run_grad(const CUtensorMap& dy, const CUtensorMap& w, const CUtensorMap& kept, const CUtensorMap& dgu,
+                            const CUtensorMap& y, const GatedParams& p, int pairs_n, cudaStream_t s) {
+  if (p.codes == nullptr) return pairs::launch<GatedGradOp<W, false, true>>(dy, w, {kept, dgu, y}, p, pairs_n, s);
+  if (p.F % 16 == 0) return pairs::launch<GatedGradOp<W, true, true>>(dy, w, {kept, dgu, y}, p, pairs_n, s);
+  return pairs::launch<GatedGradOp<W, true, false>>(dy, w, {kept, dgu, y}, p, pairs_n, s);
+}
+
+cudaError_t launch_gated_grad(int width, const CUtensorMap& dy, const CUtensorMap& w, const CUtensorMap& kept,
+                              const CUtensorMap& dgu, const CUtensorMap& y, const GatedParams& p, int pairs_n, cudaStream_t s) {
+  return width == 128 ? run_grad<128>(dy, w, kept, dgu, y, p, pairs_n, s) : run_grad<64>(dy, w, kept, dgu, y, p, pairs_n, s);
 }
 
 }  // namespace forge

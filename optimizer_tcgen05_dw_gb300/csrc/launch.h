@@ -193,10 +193,13 @@ struct GatedParams : PairParams {
 cudaError_t launch_gated(int width, const CUtensorMap& x, const CUtensorMap& w, const GatedParams& p, int pairs,
                          cudaStream_t s);
 // few_rows.cu: the forward of at most kFewGated rows, without codes.
-constexpr int64_t kFewGated = 32;
+constexpr int64_t kFewGated = 8;
 cudaError_t launch_gated_few(const void* W, const void* X, const GatedParams& p, int K, cudaStream_t s);
-cudaError_t launch_gated_grad(int width, const CUtensorMap& dy, const CUtensorMap& w, const GatedParams& p, int pairs,
-                              cudaStream_t s);
+// kept, dgu: gu, or gu_codes, and dGU as [T x 2 x F] in boxes of 32 features x 2 x
+// 32 rows (64-byte swizzle; codes 32-byte; any valid map for codes with F % 16
+// != 0), y: Y in boxes of 32 features x 32 rows (64-byte; any valid map without).
+cudaError_t launch_gated_grad(int width, const CUtensorMap& dy, const CUtensorMap& w, const CUtensorMap& kept,
+                              const CUtensorMap& dgu, const CUtensorMap& y, const GatedParams& p, int pairs, cudaStream_t s);
 
 // The product of block-scaled codes (product.cu); num_kb blocks of 128.
 struct ProductParams : PairParams {
@@ -220,7 +223,7 @@ struct CodesParams {
   int64_t rows, cols;
   int32_t square;          // blocks of 128 x 128, not 1 x 128
 };
-cudaError_t launch_quantize_e4m3(bool fp32, const CodesParams& p, int num_sms, cudaStream_t s);
-cudaError_t launch_dequantize_e4m3(bool fp32, const CodesParams& p, int num_sms, cudaStream_t s);
+cudaError_t launch_quantize_e4m3(bool fp32, const CodesParams& p, cudaStream_t s);
+cudaError_t launch_dequantize_e4m3(bool fp32, const CodesParams& p, cudaStream_t s);
 
 }  // namespace forge

@@ -130,12 +130,15 @@ struct ProductOp {
       for (int kb0 = 0; kb0 < p.num_kb; kb0 += kGroup) {
         if (!pairs::warp_wait(&ss->epi[slot], slot_ph, p, ss, lane)) return;
         const float* at = own + slot * kSlotFloats;
+        const float* w_at = scales(epi) + slot * kSlotFloats + kTileM + blk;
         float f[kGroup];
         bool mine = true;
 #pragma unroll
         for (int j = 0; j < kGroup; ++j) {
-          f[j] = at[j * kStageFloats] * (at - own + scales(epi))[j * kStageFloats + kTileM + blk];
-          mine = mine && ((f[j] > 0x1p-100f && f[j] < 0x1p100f) || kb0 + j >= p.num_kb);
+          const float xs = at[j * kStageFloats], ws = w_at[j * kStageFloats];
+          f[j] = xs * ws;
+          // (blocks of zeros, as padding rows have, are ordinary: their factor is 0 itself)
+          mine = mine && ((f[j] > 0x1p-100f && f[j] < 0x1p100f) || xs == 0.f || ws == 0.f || kb0 + j >= p.num_kb);
         }
         const bool wide = !__all_sync(0xFFFFFFFFu, mine);
         __syncwarp();  // the slot has been read
