@@ -42,16 +42,22 @@ forge_status_t zero(void* p, int64_t bytes, cudaStream_t s) {
 constexpr int kLeastWidth = 32;
 
 // The width of a CTA's B half (128, 64 or `least`): the one whose rounds of
-// tiles over the pairs cost least.  A tile of half the width costs a little
-// over half (the token operand is loaded and read again for each).
+// tiles over the pairs cost least.  A narrow tile costs more than its share (the
+// token operand is loaded and read again for each, and its stages are short):
+// 62 and 54 where the widest costs 100.  us at widths 128, 64 and 32 (product:
+// codes; else the gated forward, of 2 F rows of weights):
+//   300 x 14336 x 4096   68  85 150      128 x 14336 x 4096   55  50  79
+//   24 x 2048 x 4096     27  21  22      product 33 x 4096 x 14336  60  41  37
+//   product 1531 x 5120 x 17408  139 179 257
 // `halves`: B halves side by side in a tile's output columns (2), or on top of
 // each other (1: gate and up).
 int pick_width(int64_t rows, int64_t cols, int halves, int least, int pairs) {
+  constexpr int kCost[3] = {100, 62, 54};
   int best = 128;
   int64_t cost = 0;
-  for (int w = 128, per = 100; w >= least; w /= 2, per = per / 2 + 6) {
+  for (int w = 128, i = 0; w >= least; w /= 2, ++i) {
     const int64_t units = ceil_div(rows, 2 * kTileM) * ceil_div(cols, halves * w);
-    const int64_t c = ceil_div(units, pairs) * per;
+    const int64_t c = ceil_div(units, pairs) * kCost[i];
     if (w == 128 || c < cost) {
       cost = c;
       best = w;
@@ -78,13 +84,13 @@ forge_status_t check_tiles(int64_t rows, int64_t cols, int64_t narrowest) {
     return fail(FORGE_ERR_UNSUPPORTED, "too many output tiles (%lld x %lld)", (long long)rows, (long long)cols);
   return FORGE_OK;
 }
-// A tensor [T x 2F] as [T x 2 x F], in boxes of 32 features of both halves of 32
+// A tensor [T x 2F] as [T x 2 x F], in boxes of 32 features of one half of 32
 // rows (so that a ragged end of the first half is an end).
 forge_status_t halves_map(CUtensorMap* m, const void* base, CUtensorMapDataType dtype, int esize, int64_t T, int64_t F,
                           CUtensorMapSwizzle swizzle) {
   const cuuint64_t dims[3] = {static_cast<cuuint64_t>(F), 2, static_cast<cuuint64_t>(T)};
   const cuuint64_t strides[2] = {static_cast<cuuint64_t>(F) * esize, static_cast<cuuint64_t>(F) * 2 * esize};
-  const cuuint32_t box[3] = {32, 2, 32};
+  const cuuint32_t box[3] = {32, 1, 32};
   return tensor_map_nd(m, base, dtype, 3, dims, strides, box, swizzle);
 }
 
@@ -208,13 +214,11 @@ forge_status_t forge_gated_dgrad(const forge_gated_grad_t* g, void* stream) {
     st = tensor_map(&mw, g->Wd, kBf16, 2, F, N, 64, kBlockK, CU_TENSOR_MAP_SWIZZLE_128B);
   }
   if (st != FORGE_OK) return st;
-  CUtensorMap kept = my, dgu, y = my;
-  if ((st = halves_map(&dgu, g->dGU, kBf16, 2, T, F, CU_TENSOR_MAP_SWIZZLE_64B)) != FORGE_OK) return st;
+  CUtensorMap kept = my;
   if (g->gu != nullptr) st = halves_map(&kept, g->gu, kBf16, 2, T, F, CU_TENSOR_MAP_SWIZZLE_64B);
   else if (F % 16 == 0) st = halves_map(&kept, g->gu_codes, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, T, F, CU_TENSOR_MAP_SWIZZLE_32B);
   if (st != FORGE_OK) return st;
-  if (g->Y != nullptr && (st = tensor_map(&y, g->Y, kBf16, 2, F, T, 32, 32, CU_TENSOR_MAP_SWIZZLE_64B)) != FORGE_OK) return st;
-  const cudaError_t e = launch_gated_grad(width, my, mw, kept, dgu, y, p, pairs_of(p, d), static_cast<cudaStream_t>(stream));
+  const cudaError_t e = launch_gated_grad(width, my, mw, kept, p, pairs_of(p, d), static_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? FORGE_OK : cuda_fail(e, "gated gradient launch");
 }
 

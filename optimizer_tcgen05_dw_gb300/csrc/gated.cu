@@ -37,9 +37,12 @@ struct GatedOp {
   using Params = GatedParams;
   struct Maps { int unused; };
   static constexpr int kW = W, kARows = AROWS, kBufs = W == 128 ? 2 : 4, kSplit = 1;
-  static constexpr int kStg = AROWS < kTileM ? (W == 128 ? 10 : W == 64 ? 16 : 24) : (W == 128 ? 6 : W == 64 ? 9 : 11);
-  static constexpr int kEpiBytes = CODES ? 2 * 4 * kTileM * 4 : 0;
-  static constexpr bool kMoreRegs = false, kFp8 = false, kBMajorMN = false, kBlockwise = false;
+  static constexpr int kStg = AROWS < kTileM ? (W == 128 ? 10 : W == 64 ? 16 : 24) : (W == 128 ? (CODES ? 5 : 6) : W == 64 ? 9 : 11);
+  static constexpr int NC = W / 4;                            // features a warp takes
+  static constexpr bool kRows = W == 128 && AROWS == kTileM;  // outputs meet in shared memory, to leave by rows
+  static constexpr int kOut = kRows ? 32 * 32 * 2 : 0;        // a warp's bytes of it: 32 rows x 32 bf16
+  static constexpr int kEpiBytes = pairs::kEpiWarps * kOut + (CODES ? 2 * 4 * kTileM * 4 : 0);
+  static constexpr bool kMoreRegs = W == 128, kFp8 = false, kBMajorMN = false, kBlockwise = false;
 
   // rank 0: gate rows, rank 1: up rows of the same features (rows of another
   // half past a ragged end give columns that are not stored)
@@ -50,10 +53,10 @@ struct GatedOp {
 
   static __device__ __forceinline__ void epilogue(const Maps&, const Params& p, pairs::Shared* ss, uint8_t* epi, int warp,
                                                   int lane, uint32_t rank) {
-    constexpr int NC = W / 4;  // features a warp takes
     const int quarter = warp & 3, sub = (warp - pairs::kFirstEpiWarp) >> 2, r = quarter * 32 + lane;
     const uint32_t empty0 = ptx::mapa(ptx::smem_addr(&ss->tmem_empty[0]), 0);
-    float* red = reinterpret_cast<float*>(epi);  // [gate, up][warp of the quarter][row]
+    float* red = reinterpret_cast<float*>(epi + pairs::kEpiWarps * kOut);  // [gate, up][warp of the quarter][row]
+    uint8_t* out = epi + (warp - pairs::kFirstEpiWarp) * kOut;
     uint32_t acc = 0, ph = 0;
     for (int tile = pair_id(); tile < p.num_tiles; tile += num_pairs()) {
       int tm, tn;
@@ -102,61 +105,111 @@ struct GatedOp {
         us = codes::block_scale(ua);
         // (the next tile's first barrier keeps its sums from overtaking these reads)
       }
-      if (row < p.T) {
+      if constexpr (CODES) {
+        if (sub < 2 && row < p.T) p.scale[(row * 2 + sub) * p.tiles_n + tn] = sub == 0 ? gs : us;
+      }
+      if constexpr (kRows) {
+        const int row0 = tm * kPairM + static_cast<int>(rank) * kTileM + quarter * 32;
+        if (row0 >= p.T || f0 >= p.F) continue;
         if (p.gu != nullptr) {
-          uint16_t* out = static_cast<uint16_t*>(p.gu) + row * 2 * p.F + f0;
+          store_rows(out, g, static_cast<uint16_t*>(p.gu), int64_t{2} * p.F, p, row0, f0, lane);
+          store_rows(out, u, static_cast<uint16_t*>(p.gu) + p.F, int64_t{2} * p.F, p, row0, f0, lane);
+        }
+        if constexpr (CODES)
+          store_codes(out, g, u, codes::inverse_scale(gs), codes::inverse_scale(us), p, row0, f0, lane);
+        gate(p.act, g, u);
+        store_rows(out, g, static_cast<uint16_t*>(p.Y), p.F, p, row0, f0, lane);
+      } else if (row < p.T) {
+        if (p.gu != nullptr) {
+          uint16_t* kept = static_cast<uint16_t*>(p.gu) + row * 2 * p.F + f0;
 #pragma unroll
           for (int j = 0; j < NC / 8; ++j) {
             if (f0 + 8 * j >= p.F) break;
-            *reinterpret_cast<uint4*>(out + 8 * j) = pack_rne_bf16x8(reinterpret_cast<const float(&)[8]>(g[8 * j]));
-            *reinterpret_cast<uint4*>(out + p.F + 8 * j) = pack_rne_bf16x8(reinterpret_cast<const float(&)[8]>(u[8 * j]));
+            *reinterpret_cast<uint4*>(kept + 8 * j) = pack_rne_bf16x8(reinterpret_cast<const float(&)[8]>(g[8 * j]));
+            *reinterpret_cast<uint4*>(kept + p.F + 8 * j) = pack_rne_bf16x8(reinterpret_cast<const float(&)[8]>(u[8 * j]));
           }
         }
-        if (CODES) {
-          const float gi = codes::inverse_scale(gs), ui = codes::inverse_scale(us);
-          uint8_t* out = static_cast<uint8_t*>(p.codes) + row * 2 * p.F + f0;
-#pragma unroll
-          for (int j = 0; j < NC / 8; ++j) {
-            if (f0 + 8 * j >= p.F) break;
-            const float* a = g + 8 * j;
-            const float* b = u + 8 * j;
-            *reinterpret_cast<uint2*>(out + 8 * j) = make_uint2(codes::encode4(a[0] * gi, a[1] * gi, a[2] * gi, a[3] * gi),
-                                                                codes::encode4(a[4] * gi, a[5] * gi, a[6] * gi, a[7] * gi));
-            *reinterpret_cast<uint2*>(out + p.F + 8 * j) =
-                make_uint2(codes::encode4(b[0] * ui, b[1] * ui, b[2] * ui, b[3] * ui),
-                           codes::encode4(b[4] * ui, b[5] * ui, b[6] * ui, b[7] * ui));
-          }
-          if (sub < 2) p.scale[(row * 2 + sub) * p.tiles_n + tn] = sub == 0 ? gs : us;
-        }
-        uint16_t* y = static_cast<uint16_t*>(p.Y) + row * p.F + f0;
+        gate(p.act, g, u);
+        uint16_t* to = static_cast<uint16_t*>(p.Y) + row * p.F + f0;
 #pragma unroll
         for (int j = 0; j < NC / 8; ++j) {
           if (f0 + 8 * j >= p.F) break;
-          float v[8];
-#pragma unroll
-          for (int i = 0; i < 8; ++i) v[i] = gated(p.act, g[8 * j + i], u[8 * j + i]);  // (the branch is uniform)
-          *reinterpret_cast<uint4*>(y + 8 * j) = pack_rne_bf16x8(v);
+          *reinterpret_cast<uint4*>(to + 8 * j) = pack_rne_bf16x8(reinterpret_cast<const float(&)[8]>(g[8 * j]));
         }
       }
     }
+  }
+
+  // Y over G.
+  static __device__ __forceinline__ void gate(int act, float (&g)[NC], const float (&u)[NC]) {
+    if (act == kActSilu) {
+#pragma unroll
+      for (int j = 0; j < NC; ++j) g[j] = gated<kActSilu>(g[j], u[j]);
+    } else {
+#pragma unroll
+      for (int j = 0; j < NC; ++j) g[j] = gated<kActGeluTanh>(g[j], u[j]);
+    }
+  }
+
+  // 32 rows x 32 features, a row a lane, to memory four lanes a row: 64
+  // contiguous bytes of eight rows a store, where a lane's own row would be one
+  // of 32 lines (16384 x 14336 with gu kept: 2419 us so, 2300 this way).
+  static __device__ __forceinline__ void store_rows(uint8_t* buf, const float* v, uint16_t* to, int64_t ld, const Params& p,
+                                                    int row0, int f0, int lane) {
+#pragma unroll
+    for (int q = 0; q < 4; ++q)
+      *reinterpret_cast<uint4*>(buf + sw64(lane, q)) = pack_rne_bf16x8(reinterpret_cast<const float(&)[8]>(v[8 * q]));
+    __syncwarp();
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int r = 8 * i + (lane >> 2), q = lane & 3;
+      if (row0 + r < p.T && f0 + 8 * q < p.F)
+        *reinterpret_cast<uint4*>(to + (row0 + r) * ld + f0 + 8 * q) = *reinterpret_cast<const uint4*>(buf + sw64(r, q));
+    }
+    __syncwarp();
+  }
+  // The codes of G and U likewise: 32 bytes of each a row.
+  static __device__ __forceinline__ void store_codes(uint8_t* buf, const float* g, const float* u, float gi, float ui,
+                                                     const Params& p, int row0, int f0, int lane) {
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      const float* v = (q < 2 ? g : u) + 16 * (q & 1);
+      const float k = q < 2 ? gi : ui;
+      *reinterpret_cast<uint4*>(buf + sw64(lane, q)) =
+          make_uint4(codes::encode4(v[0] * k, v[1] * k, v[2] * k, v[3] * k), codes::encode4(v[4] * k, v[5] * k, v[6] * k, v[7] * k),
+                     codes::encode4(v[8] * k, v[9] * k, v[10] * k, v[11] * k),
+                     codes::encode4(v[12] * k, v[13] * k, v[14] * k, v[15] * k));
+    }
+    __syncwarp();
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int r = 8 * i + (lane >> 2), q = lane & 3, f = f0 + 16 * (q & 1);
+      if (row0 + r < p.T && f < p.F) {  // (F % 8 == 0: eight codes at a time)
+        uint8_t* to = static_cast<uint8_t*>(p.codes) + (static_cast<int64_t>(row0 + r) * 2 + (q >> 1)) * p.F + f;
+        const uint4 c = *reinterpret_cast<const uint4*>(buf + sw64(r, q));
+        *reinterpret_cast<uint2*>(to) = make_uint2(c.x, c.y);
+        if (f + 8 < p.F) *reinterpret_cast<uint2*>(to + 8) = make_uint2(c.z, c.w);
+      }
+    }
+    __syncwarp();
   }
 };
 
 // ---------------------------------------------------------------- gradient
 
-// What was kept is read and dGU and Y are written through shared memory by the
-// tensor-memory accelerator, chunk by chunk, every warp its own 32 rows x 32
-// features: a row is a lane, so direct accesses would touch 32 lines an
-// instruction (16384 x 14336 through 4096: 1946 us so, %STAGED% staged).  A warp's
-// first chunk of a tile is loaded while the tile's products are formed; the
-// chunks' [gate, up] lie side by side in one box ([row][gate, up][32 features]),
-// and dG and dU replace what they came from.
-// Codes with F % 16 != 0, whose rows the accelerator cannot address, are loaded
-// directly (VIA false).
+// What was kept is read and dGU and Y are written through shared memory, chunk
+// by chunk, every warp its own 32 rows x 32 features: a row is a lane, so direct
+// accesses would touch 32 lines an instruction (16384 x 14336 through 4096: 1946 us
+// so).  In, copies of the tensor-memory accelerator bring a chunk's G and U; a
+// warp's first chunk of a tile comes while the tile's products are formed.  dG and dU replace what they came from and go out
+// by ordinary stores, four lanes a row: as copies of the accelerator, whose rows
+// are of 64 bytes, they took its time from the operands' (1455 us; the products
+// alone 969).  Codes with F % 16 != 0, whose rows the accelerator cannot address,
+// are loaded directly (VIA false).
 template <int W, bool CODES, bool VIA>
 struct GatedGradOp {
   using Params = GatedParams;
-  struct Maps { CUtensorMap kept, dgu, y; };
+  struct Maps { CUtensorMap kept; };
   static constexpr int kW = W, kARows = kTileM, kStg = W == 128 ? 4 : 5, kBufs = W == 128 ? 2 : 4, kSplit = 1;
   static constexpr int NC = W / 2, kChunk = 32;        // features a warp takes, and at a time
   static constexpr int kPair = 32 * 2 * kChunk * 2;    // bytes of a chunk of dG and dU (and of G and U in bf16)
@@ -175,10 +228,11 @@ struct GatedGradOp {
     const int quarter = warp & 3, w = warp - pairs::kFirstEpiWarp, sub = w >> 2;
     const uint32_t empty0 = ptx::mapa(ptx::smem_addr(&ss->tmem_empty[0]), 0);
     const int NB = (p.F + codes::kBlock - 1) / codes::kBlock;
-    // Both buffers have 128 and 64 bytes a row, and a lane touches its own row's alone.
-    uint8_t* both = epi + w * (kPair + kOne);  // [row][gate, up][32] bf16, 64-byte swizzle
-    uint8_t* one = both + kPair;               // [row][32] bf16, 64-byte swizzle; or codes [row][gate, up][32], 32-byte swizzle
+    // A lane computes its own row's bytes of each alone.
+    uint8_t* both = epi + w * (kPair + kOne);  // [gate, up][row][32] bf16, 64-byte swizzle
+    uint8_t* one = both + kPair;               // [row][32] bf16, 64-byte swizzle; or codes [gate, up][row][32], 32-byte swizzle
     uint64_t* bar = &ss->epi[w];
+    const uint64_t pol = evict_first_policy();  // (what streams through should not displace the operands in L2)
     uint32_t acc = 0, ph = 0, kept_ph = 0;
     auto origin = [&](int tile, int& row0, int& f0) {
       int tm, tn;
@@ -191,7 +245,9 @@ struct GatedGradOp {
       const bool any = row0 < p.T && f < p.F;
       if (VIA && any && lane == 0) {
         ptx::mbar_arrive_expect_tx(bar, CODES ? kOne : kPair);
-        ptx::tma_load_3d(&maps.kept, bar, CODES ? one : both, f, 0, row0);
+        uint8_t* to = CODES ? one : both;
+        ptx::tma_load_3d(&maps.kept, bar, to, f, 0, row0);
+        ptx::tma_load_3d(&maps.kept, bar, to + (CODES ? kOne : kPair) / 2, f, 1, row0);
       }
       return VIA && any;
     };
@@ -222,9 +278,10 @@ struct GatedGradOp {
           if (CODES) {
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-              gc[h] = *reinterpret_cast<const uint4*>(one + sw32(2 * lane, h));
-              uc[h] = *reinterpret_cast<const uint4*>(one + sw32(2 * lane + 1, h));
+              gc[h] = *reinterpret_cast<const uint4*>(one + sw32(lane, h));
+              uc[h] = *reinterpret_cast<const uint4*>(one + kOne / 2 + sw32(lane, h));
             }
+            __syncwarp();  // before Y goes over them
           }
         } else {
 #pragma unroll
@@ -245,14 +302,22 @@ struct GatedGradOp {
         pairs::tmem_load<kChunk>(taddr + c, da);
         if (p.act == kActSilu) gradients<kActSilu>(da, gc, uc, gs, us, both, one, lane);
         else gradients<kActGeluTanh>(da, gc, uc, gs, us, both, one, lane);
-        ptx::fence_proxy_async_smem();
         __syncwarp();
-        if (lane == 0) {
-          ptx::tma_store_3d(&maps.dgu, both, f, 0, row0);
-          if (p.Y != nullptr) ptx::tma_store_2d(&maps.y, one, f, row0);
-          ptx::bulk_commit_group();
-          ptx::bulk_wait_group_read0();  // before either buffer is filled again
+        // Out, four lanes a row: 64 contiguous bytes of eight rows a store.
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int r = 8 * i + (lane >> 2), q = lane & 3;
+          if (row0 + r < p.T && f + 8 * q < p.F) {
+            const int64_t at = static_cast<int64_t>(row0 + r) * 2 * p.F + f + 8 * q;
+            uint16_t* out = static_cast<uint16_t*>(p.dGU) + at;
+            st_stream(out, *reinterpret_cast<const uint4*>(both + sw64(r, q)), pol);
+            st_stream(out + p.F, *reinterpret_cast<const uint4*>(both + kPair / 2 + sw64(r, q)), pol);
+            if (p.Y != nullptr)
+              st_stream(static_cast<uint16_t*>(p.Y) + static_cast<int64_t>(row0 + r) * p.F + f + 8 * q,
+                        *reinterpret_cast<const uint4*>(one + sw64(r, q)), pol);
+          }
         }
+        ptx::fence_proxy_async_smem();  // before a copy fills the buffers again
         __syncwarp();
         // The next chunk: this tile's, or else the next tile's first.
         int next_row = row0, next_f = f + kChunk;
@@ -269,10 +334,7 @@ struct GatedGradOp {
         ph ^= 1u;
       }
     }
-    if (lane == 0) {
-      if (loaded) pairs::wait(bar, kept_ph, p, ss, false);  // (a load begun before the block gave up)
-      ptx::bulk_wait_group0();
-    }
+    if (loaded && lane == 0) pairs::wait(bar, kept_ph, p, ss, false);  // (a load begun before the block gave up)
     __syncwarp();
   }
 
@@ -287,13 +349,13 @@ struct GatedGradOp {
         decode8(q & 1 ? make_uint2(gc[q >> 1].z, gc[q >> 1].w) : make_uint2(gc[q >> 1].x, gc[q >> 1].y), gs, g);
         decode8(q & 1 ? make_uint2(uc[q >> 1].z, uc[q >> 1].w) : make_uint2(uc[q >> 1].x, uc[q >> 1].y), us, u);
       } else {
-        unpack_bf16x8(*reinterpret_cast<const uint4*>(both + sw64(2 * lane, q)), g);
-        unpack_bf16x8(*reinterpret_cast<const uint4*>(both + sw64(2 * lane + 1, q)), u);
+        unpack_bf16x8(*reinterpret_cast<const uint4*>(both + sw64(lane, q)), g);
+        unpack_bf16x8(*reinterpret_cast<const uint4*>(both + kPair / 2 + sw64(lane, q)), u);
       }
 #pragma unroll
       for (int j = 0; j < 8; ++j) gated_gradient<ACT>(da[8 * q + j], g[j], u[j], g[j], u[j], y[j]);
-      *reinterpret_cast<uint4*>(both + sw64(2 * lane, q)) = pack_rne_bf16x8(g);
-      *reinterpret_cast<uint4*>(both + sw64(2 * lane + 1, q)) = pack_rne_bf16x8(u);
+      *reinterpret_cast<uint4*>(both + sw64(lane, q)) = pack_rne_bf16x8(g);
+      *reinterpret_cast<uint4*>(both + kPair / 2 + sw64(lane, q)) = pack_rne_bf16x8(u);
       *reinterpret_cast<uint4*>(one + sw64(lane, q)) = pack_rne_bf16x8(y);
     }
   }
@@ -324,16 +386,16 @@ cudaError_t launch_gated(int width, const CUtensorMap& x, const CUtensorMap& w, 
 }
 
 template <int W>
-static cudaError_t run_grad(const CUtensorMap& dy, const CUtensorMap& w, const CUtensorMap& kept, const CUtensorMap& dgu,
-                            const CUtensorMap& y, const GatedParams& p, int pairs_n, cudaStream_t s) {
-  if (p.codes == nullptr) return pairs::launch<GatedGradOp<W, false, true>>(dy, w, {kept, dgu, y}, p, pairs_n, s);
-  if (p.F % 16 == 0) return pairs::launch<GatedGradOp<W, true, true>>(dy, w, {kept, dgu, y}, p, pairs_n, s);
-  return pairs::launch<GatedGradOp<W, true, false>>(dy, w, {kept, dgu, y}, p, pairs_n, s);
+static cudaError_t run_grad(const CUtensorMap& dy, const CUtensorMap& w, const CUtensorMap& kept, const GatedParams& p,
+                            int pairs_n, cudaStream_t s) {
+  if (p.codes == nullptr) return pairs::launch<GatedGradOp<W, false, true>>(dy, w, {kept}, p, pairs_n, s);
+  if (p.F % 16 == 0) return pairs::launch<GatedGradOp<W, true, true>>(dy, w, {kept}, p, pairs_n, s);
+  return pairs::launch<GatedGradOp<W, true, false>>(dy, w, {kept}, p, pairs_n, s);
 }
 
 cudaError_t launch_gated_grad(int width, const CUtensorMap& dy, const CUtensorMap& w, const CUtensorMap& kept,
-                              const CUtensorMap& dgu, const CUtensorMap& y, const GatedParams& p, int pairs_n, cudaStream_t s) {
-  return width == 128 ? run_grad<128>(dy, w, kept, dgu, y, p, pairs_n, s) : run_grad<64>(dy, w, kept, dgu, y, p, pairs_n, s);
+                              const GatedParams& p, int pairs_n, cudaStream_t s) {
+  return width == 128 ? run_grad<128>(dy, w, kept, p, pairs_n, s) : run_grad<64>(dy, w, kept, p, pairs_n, s);
 }
 
 }  // namespace forge
