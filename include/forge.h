@@ -437,7 +437,8 @@ typedef enum forge_act { FORGE_ACT_SILU = 0, FORGE_ACT_GELU_TANH = 1 } forge_act
  * kept of them are rounded from there.  Kept for the gradient, one or none:
  *   gu        bf16 [T x 2F]: row t is G[t], then U[t]
  *   gu_codes  E4M3 codes [T x 2F] with gu_scale [T x 2 x ceil(F / 128)]: the
- *             format of forge_quantize_e4m3 over the [2T x F] matrix
+ *             format of forge_quantize_e4m3 over the [2T x F] matrix, of the
+ *             float32 G and U (a scale carries the error of their K-term sums)
  * F % 8 == 0, K % 8 == 0; T, 2F and K within 31 bits; T == 0 or F == 0 does
  * nothing, K == 0 gives zeros.  An infinite G or U gives what the formula
  * does (inf * 0 is NaN).  The outputs overlap neither the inputs nor each other. */
@@ -484,7 +485,7 @@ FORGE_API forge_status_t forge_gated_dgrad(const forge_gated_grad_t* grad, void*
  *           one that holds a value that is not finite
  *   code  = E4M3(x / scale), to the nearest (x / scale is formed to within
  *           three float32 roundings)
- * cols % 8 == 0. */
+ * cols % 8 == 0; rows * cols within 40 bits.  The outputs overlap no input. */
 FORGE_API forge_status_t forge_quantize_e4m3(const void* x, int32_t x_dtype, void* codes, float* scale,
                                              int64_t rows, int64_t cols, int32_t block_rows, void* stream);
 /* And back: x = code * scale, a float32 product rounded once to x_dtype. */
@@ -494,6 +495,9 @@ FORGE_API forge_status_t forge_dequantize_e4m3(const void* codes, const float* s
 /* Y = X W^T of values in that format:
  *   Y[t, n] = sum_b x_scale[t, b] w_scale[n / 128, b] sum_{k in b} Xq[t, k] Wq[n, k]
  * with the inner sums and the outer one in float32 and one rounding to bf16.
+ * Scales are 0, positive or NaN, as forge_quantize_e4m3 writes them; their
+ * product may leave float32's range where the sum does not.  NaN scales and
+ * codes give NaN in their row of Y, or in their columns.  Y overlaps no input.
  * N % 8 == 0, K % 16 == 0; T, N and K within 31 bits; K == 0 gives zeros. */
 typedef struct forge_linear_e4m3 {
   int64_t T, N, K;

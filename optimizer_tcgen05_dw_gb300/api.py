@@ -647,6 +647,14 @@ def forge_rmsnorm_bwd(dy, h, w, rstd, dx, dw, workspace, dh=None, stream=None):
     _check(lib().forge_rmsnorm_bwd(ctypes.byref(p), _stream(stream)))
 
 
+def _here(*tensors):
+    """Every tensor given lies on the current device, whose stream the call goes to."""
+    dev = torch.cuda.current_device()
+    for t in tensors:
+        if t is not None and t.get_device() != dev:
+            raise ValueError(f"tensors must be on the current device, cuda:{dev}; got one on {t.device}")
+
+
 def _act(act):
     if act not in ACT_KINDS:
         raise ValueError(f"act: expected one of {', '.join(ACT_KINDS)}, got {act!r}")
@@ -677,6 +685,7 @@ def forge_gated_linear(X, W, Y, act: str = "silu", gu=None, gu_codes=None, gu_sc
     _need(W, "W", torch.bfloat16, (2 * F, K))
     _need(Y, "Y", torch.bfloat16, (T, F))
     _kept(T, F, gu, gu_codes, gu_scale)
+    _here(X, W, Y, gu, gu_codes, gu_scale)
     g = ForgeGated(T, F, K, _act(act), X.data_ptr(), W.data_ptr(), Y.data_ptr(), _ptr(gu), _ptr(gu_codes), _ptr(gu_scale))
     _check(lib().forge_gated_linear(ctypes.byref(g), _stream(stream)))
 
@@ -697,6 +706,7 @@ def forge_gated_dgrad(dY, Wd, dGU, act: str = "silu", gu=None, gu_codes=None, gu
     _kept(T, F, gu, gu_codes, gu_scale)
     if Y is not None:
         _need(Y, "Y", torch.bfloat16, (T, F))
+    _here(dY, Wd, dGU, gu, gu_codes, gu_scale, Y)
     g = ForgeGatedGrad(T, F, N, _act(act), dY.data_ptr(), Wd.data_ptr(), _ptr(gu), _ptr(gu_codes), _ptr(gu_scale),
                        dGU.data_ptr(), _ptr(Y))
     _check(lib().forge_gated_dgrad(ctypes.byref(g), _stream(stream)))
@@ -713,6 +723,7 @@ def _coded(codes, scale, x, block_rows):
     _need(codes, "codes", torch.float8_e4m3fn, shape)
     _need(scale, "scale", torch.float32, (rows if block_rows == 1 else (rows + CODE_BLOCK - 1) // CODE_BLOCK,
                                           (cols + CODE_BLOCK - 1) // CODE_BLOCK))
+    _here(x, codes, scale)
     return rows, cols, G_FP32 if x.dtype == torch.float32 else G_BF16
 
 
@@ -745,6 +756,7 @@ def forge_linear_e4m3(Xq, x_scale, Wq, w_scale, Y, stream=None):
     _need(Wq, "Wq", torch.float8_e4m3fn, (N, K))
     _need(w_scale, "w_scale", torch.float32, (blocks(N), blocks(K)))
     _need(Y, "Y", torch.bfloat16, (T, N))
+    _here(Xq, x_scale, Wq, w_scale, Y)
     g = ForgeLinearE4m3(T, N, K, Xq.data_ptr(), x_scale.data_ptr(), Wq.data_ptr(), w_scale.data_ptr(), Y.data_ptr())
     _check(lib().forge_linear_e4m3(ctypes.byref(g), _stream(stream)))
 

@@ -120,8 +120,9 @@ forge_status_t check_codes(int64_t rows, int64_t cols, int32_t x_dtype, int32_t 
   if (cols % 8 != 0) return fail(FORGE_ERR_INVALID_ARG, "cols must be a multiple of 8 (cols=%lld)", (long long)cols);
   if (x_dtype != FORGE_G_FP32 && x_dtype != FORGE_G_BF16) return fail(FORGE_ERR_INVALID_ARG, "x_dtype %d", x_dtype);
   if (block_rows != 1 && block_rows != kBlock) return fail(FORGE_ERR_INVALID_ARG, "block_rows must be 1 or 128 (got %d)", block_rows);
-  if (rows > kMost || cols > kMost || ceil_div(rows, kBlock) * ceil_div(cols, kBlock) > kMost)
-    return fail(FORGE_ERR_UNSUPPORTED, "rows, cols and the 128 x 128 blocks must fit in 31 bits");
+  if (rows > kMost || cols > kMost || ceil_div(rows, kBlock) * ceil_div(cols, kBlock) > kMost ||
+      (rows > 0 && cols > (int64_t{1} << 40) / rows))
+    return fail(FORGE_ERR_UNSUPPORTED, "rows, cols and the 128 x 128 blocks must fit in 31 bits, rows * cols in 40");
   return FORGE_OK;
 }
 

@@ -56,7 +56,7 @@ def test_gated_gradient_refusals(L, change, status, word):
 @pytest.mark.parametrize("change,status,word", [
     (dict(rows=-1), 1, "negative"), (dict(cols=-8), 1, "negative"), (dict(cols=12), 1, "multiple of 8"), (dict(dt=2), 1, "x_dtype"),
     (dict(block=64), 1, "block_rows"), (dict(rows=1 << 31), 2, "31 bits"), (dict(cols=1 << 31), 2, "31 bits"),
-    (dict(rows=1 << 30, cols=1 << 30), 2, "31 bits"), (dict(x=None), 1, "x is NULL"), (dict(x=FAKE + 8), 1, "x must be"),
+    (dict(rows=1 << 30, cols=1 << 30), 2, "31 bits"), (dict(rows=1 << 21, cols=1 << 20, block=1), 2, "in 40"), (dict(x=None), 1, "x is NULL"), (dict(x=FAKE + 8), 1, "x must be"),
     (dict(codes=None), 1, "codes is NULL"), (dict(codes=FAKE + 8), 1, "codes must be"), (dict(scale=None), 1, "scale is NULL"),
     (dict(scale=FAKE + 1), 1, "scale must be 4-byte")])
 def test_codes_refusals(L, change, status, word):
@@ -121,6 +121,24 @@ def test_the_binding_refuses_what_the_library_could_not_see():
         api.forge_dequantize_e4m3(e(4, 8), f(4, 1), f(8, 4).t())
     with pytest.raises(TypeError, match="Xq: expected"):
         api.forge_linear_e4m3(torch.zeros((4, 16), dtype=torch.uint8), f(4, 1), e(8, 16), f(1, 1), b(4, 8))
+
+
+def test_tensors_of_another_device_are_refused(monkeypatch):
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 1)
+    t = torch.zeros(4)  # (on the host: device -1)
+    with pytest.raises(ValueError, match="current device, cuda:1"):
+        api._here(None, t)
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: -1)
+    api._here(t, None)
+    calls = []
+    monkeypatch.setattr(api, "_here", lambda *a: calls.append(len(a)) or (_ for _ in ()).throw(ValueError("elsewhere")))
+    b, e, f = (lambda *n, d=d: _cuda(torch.zeros(n).to(d)) for d in (torch.bfloat16, torch.float8_e4m3fn, torch.float32))
+    for call in (lambda: api.forge_gated_linear(b(4, 8), b(16, 8), b(4, 8)), lambda: api.forge_gated_dgrad(b(4, 8), b(8, 16), b(4, 32), gu=b(4, 32)),
+                 lambda: api.forge_quantize_e4m3(f(4, 8), e(4, 8), f(4, 1)), lambda: api.forge_dequantize_e4m3(e(4, 8), f(4, 1), b(4, 8)),
+                 lambda: api.forge_linear_e4m3(e(4, 16), f(4, 1), e(8, 16), f(1, 1), b(4, 8))):
+        with pytest.raises(ValueError, match="elsewhere"):
+            call()
+    assert calls == [6, 7, 3, 3, 5]
 
 
 class _cuda(torch.Tensor):
