@@ -26,17 +26,9 @@ __device__ __forceinline__ float max_nan(float a, float b) {
   return r;
 }
 
-// a / 448, correctly rounded where it is a normal number (a finite): the rounded
-// product with 1 / 448 is within an ulp, its remainder exact in one fused
-// operation, and one more brings the quotient to the nearest.
-__device__ __forceinline__ float over_448(float a) {
-  constexpr float r = 1.f / kE4M3Max;
-  const float q = a * r;
-  return fmaf(fmaf(-kE4M3Max, q, a), r, q);
-}
 __device__ __forceinline__ float block_scale(float amax) {
   const float a = amax + (amax - amax);  // an infinite maximum is no scale
-  return a > 0.f ? fmaxf(over_448(a), 0x1p-126f) : a;
+  return a > 0.f ? fmaxf(__fdiv_rn(a, kE4M3Max), 0x1p-126f) : a;
 }
 __device__ __forceinline__ float inverse_scale(float scale) { return scale == 0.f ? 0.f : __frcp_rn(scale); }
 
