@@ -1,8 +1,8 @@
 // The gated product and the product of block-scaled codes for a few token rows
 // (decoding).  The weights are read once for a handful of tokens, so the floor
 // is that read and what matters is to spread it evenly and keep it streaming:
-// a block takes the weight rows of 8 (gated: gate and up) or 16 features, its
-// eight warps share the reduction, and the warp-level matrix instruction takes
+// a block takes the weight rows of 8 (gated: gate and up), 16 or 32 features, its
+// 8 or 16 warps share the reduction, and the warp-level matrix instruction takes
 // the weights from the registers they were loaded to (each is used once: staging
 // it through shared memory for a larger instruction would only lengthen its way).
 // The instruction's k order is free as long as both operands agree: a lane loads
@@ -50,34 +50,31 @@ __device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1,
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-// Four codes as two pairs of halves, codes 1 and 3 first, then 0 and 2, each
-// 2^-8 of its value: sign, four exponent and three mantissa bits move to their
-// places in a half (bias 15 for 7; numbers smaller than normal come out right
-// too).  Of NaN's seven set bits this makes 0x3F80, the largest magnitude there
-// is: `top` keeps the largest seen.
-__device__ __forceinline__ void halves4(uint32_t w, uint32_t& odd, uint32_t& even, uint32_t& top) {
-  constexpr uint32_t kMag = 0x3F803F80u, kSign = 0x80008000u;
-  const uint32_t mo = (w >> 1) & kMag, me = (w << 7) & kMag;
-  top = __vmaxu2(top, __vmaxu2(mo, me));
-  odd = mo | (w & kSign);
-  even = me | ((w << 8) & kSign);
+// Four codes, in order, as two pairs of halves, each 2^-8 of its value: sign,
+// four exponent and three mantissa bits move to their places in a half (bias 15
+// for 7; numbers smaller than normal come out right too).  Of NaN's seven set
+// bits this makes 0x3F80, the largest magnitude there is: `top` keeps the
+// largest seen.
+__device__ __forceinline__ uint32_t halves2(uint32_t high, uint32_t& top) {  // two codes, each the high byte of a half
+  const uint32_t mag = (high >> 1) & 0x3F803F80u;
+  top = __vmaxu2(top, mag);
+  return mag | (high & 0x80008000u);
 }
 __device__ __forceinline__ void halves16(uint4 c, uint32_t (&h)[8], uint32_t& top) {
-  halves4(c.x, h[0], h[1], top);
-  halves4(c.y, h[2], h[3], top);
-  halves4(c.z, h[4], h[5], top);
-  halves4(c.w, h[6], h[7], top);
+  const uint32_t w[4] = {c.x, c.y, c.z, c.w};
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    h[2 * j] = halves2(__byte_perm(w[j], 0, 0x1404), top);
+    h[2 * j + 1] = halves2(__byte_perm(w[j], 0, 0x3424), top);
+  }
 }
-// The same by the conversion instruction: values themselves, in order.
+// The same by the conversion instruction: the values themselves.
 __device__ __forceinline__ void converted16(uint4 c, uint32_t (&h)[8]) {
   const uint32_t w[4] = {c.x, c.y, c.z, c.w};
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
-    asm("{\n\t.reg .b16 lo, hi;\n\t.reg .b32 x;\n\tmov.b32 {lo, hi}, %2;\n\tcvt.rn.f16x2.e4m3x2 %1, lo;\n\tcvt.rn.f16x2.e4m3x2 %0, hi;\n\t}"
+    asm("{\n\t.reg .b16 lo, hi;\n\tmov.b32 {lo, hi}, %2;\n\tcvt.rn.f16x2.e4m3x2 %0, lo;\n\tcvt.rn.f16x2.e4m3x2 %1, hi;\n\t}"
         : "=r"(h[2 * j]), "=r"(h[2 * j + 1]) : "r"(w[j]));
-    const uint32_t a = h[2 * j], b = h[2 * j + 1];  // codes 2, 3 and 0, 1 -> 1, 3 and 0, 2
-    h[2 * j] = __byte_perm(b, a, 0x7632);
-    h[2 * j + 1] = __byte_perm(b, a, 0x5410);
   }
 }
 __device__ __forceinline__ bool has_nan(uint32_t top) { return (top & 0xFFFFu) == 0x3F80u || (top >> 16) == 0x3F80u; }
@@ -133,36 +130,44 @@ __global__ void __launch_bounds__(kThreads) gated_few_kernel(const uint16_t* W, 
 
 // ---------------------------------------------------------------- codes
 
-// Features 16 blockIdx.x .. of up to 8 NT tokens; a warp takes a block of 128
-// of the reduction at a time, and its sum meets the block's two scales.  The
+// Features 16 MT blockIdx.x .. of up to 8 NT tokens; a warp takes a block of
+// 128 of the reduction at a time, and its sum meets the block's two scales.  The
 // codes are multiplied as halves: the warp-level instruction on E4M3 itself ran
 // at a fraction of that one's rate (5 rows of 4096 x 14336: 33 us and more).
 // Weights are converted by the instruction for it and tokens by integer
-// operations, to share the time between the two pipes (all converted 22.6 us, all
-// by integers 26, so 17.9); the next block's loads are under way meanwhile.
-template <int NT>
-__global__ void __launch_bounds__(kThreads, 2) product_few_kernel(const uint8_t* W, const uint8_t* X, const ProductParams p,
-                                                               const int K) {
-  constexpr int kTok = 8 * NT;
-  __shared__ float s_sum[kWarps * kTok * 16];
+// operations, to share the time between the two pipes; the tokens' serve MT
+// instructions, and the next block's loads, 2 MT KB a warp, are under way meanwhile
+// (5 rows of 4096 x 14336: 14.7 us; MT = 1 in twice as many blocks of eight warps 18.2).
+constexpr int kCodeWarps = 16, kCodeThreads = 32 * kCodeWarps;
+template <int NT, int MT>
+__global__ void __launch_bounds__(kCodeThreads, 1) product_few_kernel(const uint8_t* W, const uint8_t* X, const ProductParams p,
+                                                                   const int K) {
+  constexpr int kTok = 8 * NT, kFeat = 16 * MT;
+  __shared__ float s_sum[kCodeWarps * kTok * kFeat];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, q = lane & 3;
-  const int f0 = blockIdx.x * 16, V = K >> 4;
-  const uint4* w0 = reinterpret_cast<const uint4*>(W + static_cast<int64_t>(min(f0 + g, p.N - 1)) * K) + q;
-  const uint4* w1 = reinterpret_cast<const uint4*>(W + static_cast<int64_t>(min(f0 + g + 8, p.N - 1)) * K) + q;
+  const int f0 = blockIdx.x * kFeat, V = K >> 4;
+  const uint4* w[MT][2];
+#pragma unroll
+  for (int m = 0; m < MT; ++m)
+#pragma unroll
+    for (int r = 0; r < 2; ++r)
+      w[m][r] = reinterpret_cast<const uint4*>(W + static_cast<int64_t>(min(f0 + 16 * m + 8 * r + g, p.N - 1)) * K) + q;
   const float* sw = p.w_scale + static_cast<int64_t>(f0 / codes::kBlock) * p.num_kb;
   const uint4* x[NT];
   const float* sx[NT][2];
-  float acc[NT][4];
+  float acc[MT][NT][4];
 #pragma unroll
   for (int i = 0; i < NT; ++i) {
     x[i] = reinterpret_cast<const uint4*>(X + static_cast<int64_t>(min(8 * i + g, p.T - 1)) * K) + q;
 #pragma unroll
     for (int j = 0; j < 2; ++j) sx[i][j] = p.x_scale + static_cast<int64_t>(min(8 * i + 2 * q + j, p.T - 1)) * p.num_kb;
 #pragma unroll
-    for (int j = 0; j < 4; ++j) acc[i][j] = 0.f;
+    for (int m = 0; m < MT; ++m)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) acc[m][i][j] = 0.f;
   }
   struct Block {
-    uint4 a0[2], a1[2], t[NT][2];
+    uint4 a[MT][2][2], t[NT][2];
     float ws, xs[NT][2];
   };
   Block ahead;
@@ -178,8 +183,10 @@ __global__ void __launch_bounds__(kThreads, 2) product_few_kernel(const uint8_t*
     for (int h = 0; h < 2; ++h) {
       const int v = at * 8 + h * 4;
       const bool there = in && v + q < V;
-      o.a0[h] = there ? ld_once(w0 + v) : zero;
-      o.a1[h] = there ? ld_once(w1 + v) : zero;
+#pragma unroll
+      for (int m = 0; m < MT; ++m)
+#pragma unroll
+        for (int r = 0; r < 2; ++r) o.a[m][r][h] = there ? ld_once(w[m][r] + v) : zero;
 #pragma unroll
       for (int i = 0; i < NT; ++i) o.t[i][h] = there ? x[i][v] : zero;
     }
@@ -189,25 +196,30 @@ __global__ void __launch_bounds__(kThreads, 2) product_few_kernel(const uint8_t*
       for (int j = 0; j < 2; ++j) o.xs[i][j] = sx[i][j][at];
   };
   load(ahead, warp);
-  for (int b = warp; b < p.num_kb; b += kWarps) {
+  for (int b = warp; b < p.num_kb; b += kCodeWarps) {
     const Block o = ahead;
-    load(ahead, b + kWarps);
-    float c[NT][4];
+    load(ahead, b + kCodeWarps);
+    float c[MT][NT][4];
 #pragma unroll
-    for (int i = 0; i < NT; ++i)
+    for (int m = 0; m < MT; ++m)
 #pragma unroll
-      for (int j = 0; j < 4; ++j) c[i][j] = 0.f;
+      for (int i = 0; i < NT; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) c[m][i][j] = 0.f;
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-      uint32_t r0[8], r1[8];
-      converted16(o.a0[h], r0);
-      converted16(o.a1[h], r1);
+      uint32_t t[NT][8];
 #pragma unroll
-      for (int i = 0; i < NT; ++i) {
-        uint32_t t[8];
-        halves16(o.t[i][h], t, top_t[i]);
+      for (int i = 0; i < NT; ++i) halves16(o.t[i][h], t[i], top_t[i]);
 #pragma unroll
-        for (int k = 0; k < 8; k += 2) mma_f16(c[i], r0[k], r1[k], r0[k + 1], r1[k + 1], t[k], t[k + 1]);
+      for (int m = 0; m < MT; ++m) {
+        uint32_t r0[8], r1[8];
+        converted16(o.a[m][0][h], r0);
+        converted16(o.a[m][1][h], r1);
+#pragma unroll
+        for (int i = 0; i < NT; ++i)
+#pragma unroll
+          for (int k = 0; k < 8; k += 2) mma_f16(c[m][i], r0[k], r1[k], r0[k + 1], r1[k + 1], t[i][k], t[i][k + 1]);
       }
     }
 #pragma unroll
@@ -216,8 +228,11 @@ __global__ void __launch_bounds__(kThreads, 2) product_few_kernel(const uint8_t*
       for (int j = 0; j < 2; ++j) {
         const codes::Factor f = codes::factor(o.xs[i][j], o.ws);
         const float part = f.p * 256.f;  // the tokens were 2^-8 of their values
-        acc[i][j] = fmaf(c[i][j] * part, f.f, acc[i][j]);
-        acc[i][j + 2] = fmaf(c[i][j + 2] * part, f.f, acc[i][j + 2]);
+#pragma unroll
+        for (int m = 0; m < MT; ++m) {
+          acc[m][i][j] = fmaf(c[m][i][j] * part, f.f, acc[m][i][j]);
+          acc[m][i][j + 2] = fmaf(c[m][i][j + 2] * part, f.f, acc[m][i][j + 2]);
+        }
       }
   }
   // A NaN code among this warp's makes its token's sums NaN: the token is with
@@ -227,30 +242,34 @@ __global__ void __launch_bounds__(kThreads, 2) product_few_kernel(const uint8_t*
     const uint32_t nan_t = __ballot_sync(0xFFFFFFFFu, has_nan(top_t[i]));
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      if (((nan_t >> (4 * (2 * q + (j & 1)))) & 0xFu) != 0) acc[i][j] = __uint_as_float(0x7FC00000u);
+      if (((nan_t >> (4 * (2 * q + (j & 1)))) & 0xFu) != 0)
+#pragma unroll
+        for (int m = 0; m < MT; ++m) acc[m][i][j] = __uint_as_float(0x7FC00000u);
     }
   }
   // [warp][token][feature]
 #pragma unroll
-  for (int i = 0; i < NT; ++i)
+  for (int m = 0; m < MT; ++m)
 #pragma unroll
-    for (int j = 0; j < 4; ++j)
-      s_sum[(warp * kTok + 8 * i + 2 * q + (j & 1)) * 16 + g + 8 * (j >> 1)] = acc[i][j];
+    for (int i = 0; i < NT; ++i)
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        s_sum[(warp * kTok + 8 * i + 2 * q + (j & 1)) * kFeat + 16 * m + g + 8 * (j >> 1)] = acc[m][i][j];
   __syncthreads();
-  for (int o = threadIdx.x; o < kTok * 16; o += kThreads) {
-    const int t = o / 16, f = f0 + o % 16;
+  for (int o = threadIdx.x; o < kTok * kFeat; o += kCodeThreads) {
+    const int t = o / kFeat, f = f0 + o % kFeat;
     if (t >= p.T || f >= p.N) continue;
     float sum = 0.f;
 #pragma unroll
-    for (int w = 0; w < kWarps; ++w) sum += s_sum[w * kTok * 16 + o];
+    for (int i = 0; i < kCodeWarps; ++i) sum += s_sum[i * kTok * kFeat + o];
     static_cast<uint16_t*>(p.Y)[static_cast<int64_t>(t) * p.N + f] = bf16_bits(sum);
   }
 }
 
-template <int NT>
+template <int NT, int MT>
 cudaError_t run_product(const void* W, const void* X, const ProductParams& p, int K, cudaStream_t s) {
-  const unsigned grid = static_cast<unsigned>((p.N + 15) / 16);
-  product_few_kernel<NT><<<grid, kThreads, 0, s>>>(static_cast<const uint8_t*>(W), static_cast<const uint8_t*>(X), p, K);
+  const unsigned grid = static_cast<unsigned>((p.N + 16 * MT - 1) / (16 * MT));
+  product_few_kernel<NT, MT><<<grid, kCodeThreads, 0, s>>>(static_cast<const uint8_t*>(W), static_cast<const uint8_t*>(X), p, K);
   return cudaGetLastError();
 }
 
@@ -262,8 +281,10 @@ cudaError_t launch_gated_few(const void* W, const void* X, const GatedParams& p,
   return cudaGetLastError();
 }
 
-cudaError_t launch_product_few(const void* W, const void* X, const ProductParams& p, int K, cudaStream_t s) {
-  return p.T <= 8 ? run_product<1>(W, X, p, K, s) : run_product<2>(W, X, p, K, s);
+// Blocks of 32 features, or of 16 where all of them have an SM each.
+cudaError_t launch_product_few(const void* W, const void* X, const ProductParams& p, int K, int num_sms, cudaStream_t s) {
+  if ((p.N + 15) / 16 <= num_sms) return p.T <= 8 ? run_product<1, 1>(W, X, p, K, s) : run_product<2, 1>(W, X, p, K, s);
+  return p.T <= 8 ? run_product<1, 2>(W, X, p, K, s) : run_product<2, 2>(W, X, p, K, s);
 }
 
 }  // namespace forge

@@ -84,16 +84,6 @@ forge_status_t check_tiles(int64_t rows, int64_t cols, int64_t narrowest) {
     return fail(FORGE_ERR_UNSUPPORTED, "too many output tiles (%lld x %lld)", (long long)rows, (long long)cols);
   return FORGE_OK;
 }
-// A tensor [T x 2F] as [T x 2 x F], in boxes of 32 features of one half of 32
-// rows (so that a ragged end of the first half is an end).
-forge_status_t halves_map(CUtensorMap* m, const void* base, CUtensorMapDataType dtype, int esize, int64_t T, int64_t F,
-                          CUtensorMapSwizzle swizzle) {
-  const cuuint64_t dims[3] = {static_cast<cuuint64_t>(F), 2, static_cast<cuuint64_t>(T)};
-  const cuuint64_t strides[2] = {static_cast<cuuint64_t>(F) * esize, static_cast<cuuint64_t>(F) * 2 * esize};
-  const cuuint32_t box[3] = {32, 1, 32};
-  return tensor_map_nd(m, base, dtype, 3, dims, strides, box, swizzle);
-}
-
 // Token rows of a copy of the A operand.
 uint32_t box_rows(int64_t T) { return T <= kShortRows ? kShortRows : kTileM; }
 int pairs_of(const PairParams& p, const DeviceInfo& d) { return p.num_tiles < d.num_sms / 2 ? p.num_tiles : d.num_sms / 2; }
@@ -215,11 +205,7 @@ forge_status_t forge_gated_dgrad(const forge_gated_grad_t* g, void* stream) {
     st = tensor_map(&mw, g->Wd, kBf16, 2, F, N, 64, kBlockK, CU_TENSOR_MAP_SWIZZLE_128B);
   }
   if (st != FORGE_OK) return st;
-  CUtensorMap kept = my;
-  if (g->gu != nullptr) st = halves_map(&kept, g->gu, kBf16, 2, T, F, CU_TENSOR_MAP_SWIZZLE_64B);
-  else if (F % 16 == 0) st = halves_map(&kept, g->gu_codes, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, T, F, CU_TENSOR_MAP_SWIZZLE_32B);
-  if (st != FORGE_OK) return st;
-  const cudaError_t e = launch_gated_grad(width, my, mw, kept, p, pairs_of(p, d), static_cast<cudaStream_t>(stream));
+  const cudaError_t e = launch_gated_grad(width, my, mw, p, pairs_of(p, d), static_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? FORGE_OK : cuda_fail(e, "gated gradient launch");
 }
 
@@ -282,7 +268,7 @@ forge_status_t forge_linear_e4m3(const forge_linear_e4m3_t* lin, void* stream) {
   p.w_scale = lin->w_scale;
   p.Y = lin->Y;
   if (T <= kFewProduct && p.skip_loads == 0) {
-    const cudaError_t e = launch_product_few(lin->Wq, lin->Xq, p, static_cast<int>(K), s);
+    const cudaError_t e = launch_product_few(lin->Wq, lin->Xq, p, static_cast<int>(K), d.num_sms, s);
     return e == cudaSuccess ? FORGE_OK : cuda_fail(e, "block-scaled product launch");
   }
   CUtensorMap mx, mw;

@@ -24,9 +24,6 @@ namespace forge {
 
 namespace {
 
-// Byte offset of 16-byte chunk c of row r in a box of 32-byte rows stored with the 32-byte swizzle.
-__device__ __forceinline__ uint32_t sw32(int r, int c) { return static_cast<uint32_t>(r * 32 + ((c ^ ((r >> 2) & 1)) << 4)); }
-
 constexpr int kQuarterBarrier = 2;  // + 0 .. 3: the four warps of a tensor-memory quarter
 
 // ---------------------------------------------------------------- forward
@@ -197,135 +194,141 @@ struct GatedOp {
 
 // ---------------------------------------------------------------- gradient
 
-// What was kept is read and dGU and Y are written through shared memory, chunk
-// by chunk, every warp its own 32 rows x 32 features: a row is a lane, so direct
-// accesses would touch 32 lines an instruction (16384 x 14336 through 4096: 1946 us
-// so).  In, copies of the tensor-memory accelerator bring a chunk's G and U; a
-// warp's first chunk of a tile comes while the tile's products are formed.  dG and dU replace what they came from and go out
-// by ordinary stores, four lanes a row: as copies of the accelerator, whose rows
-// are of 64 bytes, they took its time from the operands' (1455 us; the products
-// alone 969).  Codes with F % 16 != 0, whose rows the accelerator cannot address,
-// are loaded directly (VIA false).
-template <int W, bool CODES, bool VIA>
+// A row is a lane of the accumulator, so direct accesses would touch 32 lines an
+// instruction (16384 x 14336 through 4096: 1946 us so).  What was kept comes in
+// and dG, dU and Y go out four lanes a row, 64 contiguous bytes of eight rows an
+// instruction, and every warp turns its own 32 rows x 32 features between the two
+// in 2 KB of shared memory, one tensor after the other.  Copies of the
+// tensor-memory accelerator would turn them too, but they take its time from the
+// operands', and larger buffers, which the ring is better used for (what was kept
+// by copies, 6 KB a warp and 4 stages: 1318 us; 4 KB and 5 stages: 1240; so, 6
+// stages: 1146, the products alone 969).
+// A warp's first chunk of a tile is loaded before its products are there, and the
+// other asked into L2 (in registers there is no room for it: the spills of that
+// cost more, 1372 us).
+template <int W, bool CODES>
 struct GatedGradOp {
   using Params = GatedParams;
-  struct Maps { CUtensorMap kept; };
-  static constexpr int kW = W, kARows = kTileM, kStg = W == 128 ? 4 : 5, kBufs = W == 128 ? 2 : 4, kSplit = 1;
+  struct Maps { int unused; };
+  static constexpr int kW = W, kARows = kTileM, kStg = W == 128 ? 6 : 8, kBufs = W == 128 ? 2 : 4, kSplit = 1;
   static constexpr int NC = W / 2, kChunk = 32;        // features a warp takes, and at a time
-  static constexpr int kPair = 32 * 2 * kChunk * 2;    // bytes of a chunk of dG and dU (and of G and U in bf16)
-  static constexpr int kOne = 32 * kChunk * 2;         // of Y (and of G's and U's codes together)
-  static constexpr int kEpiBytes = pairs::kEpiWarps * (kPair + kOne);
+  static constexpr int kTurn = 32 * kChunk * 2;        // bytes of a chunk of one tensor in bf16
+  static constexpr int kLoads = CODES ? 4 : 8;         // 16-byte vectors a lane loads of a chunk
+  static constexpr int kEpiBytes = pairs::kEpiWarps * kTurn;
   static constexpr bool kMoreRegs = false, kFp8 = false, kBMajorMN = true, kBlockwise = false;
 
   static __device__ __forceinline__ int b_row(int tn, int rank, const Params&) { return (2 * tn + rank) * W; }
-  static __device__ __forceinline__ void init_barriers(pairs::Shared* ss) {
-    for (int i = 0; i < pairs::kEpiWarps; ++i) ptx::mbar_init(&ss->epi[i], 1);
-  }
+  static __device__ __forceinline__ void init_barriers(pairs::Shared*) {}
   static __device__ __forceinline__ void helper(const Params&, pairs::Shared*, uint8_t*, int, int, uint32_t) {}
 
-  static __device__ __forceinline__ void epilogue(const Maps& maps, const Params& p, pairs::Shared* ss, uint8_t* epi,
-                                                  int warp, int lane, uint32_t rank) {
+  // This lane's vectors of what was kept for the chunk at (row0, f): of rows
+  // 8 i + lane / 4, eight features of G (vectors 0-3) and of U (4-7); or in codes
+  // sixteen, of G in its even lanes' pairs and of U in the others'.
+  static __device__ __forceinline__ void load(uint4 (&v)[kLoads], const Params& p, int row0, int f, int lane) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int r = row0 + 8 * i + (lane >> 2), q = lane & 3;
+      v[i] = make_uint4(0, 0, 0, 0);
+      if constexpr (CODES) {
+        const int at = f + 16 * (q & 1);
+        const uint8_t* from = static_cast<const uint8_t*>(p.codes) + (static_cast<int64_t>(r) * 2 + (q >> 1)) * p.F + at;
+        if (r < p.T && at < p.F) {  // (F % 8 == 0: eight codes at a time)
+          const uint2 a = __ldcs(reinterpret_cast<const uint2*>(from));
+          v[i].x = a.x;
+          v[i].y = a.y;
+        }
+        if (r < p.T && at + 8 < p.F) {
+          const uint2 a = __ldcs(reinterpret_cast<const uint2*>(from + 8));
+          v[i].z = a.x;
+          v[i].w = a.y;
+        }
+      } else {
+        v[i + 4] = v[i];
+        if (r < p.T && f + 8 * q < p.F) {
+          const uint16_t* from = static_cast<const uint16_t*>(p.gu) + static_cast<int64_t>(r) * 2 * p.F + f + 8 * q;
+          v[i] = __ldcs(reinterpret_cast<const uint4*>(from));
+          v[i + 4] = __ldcs(reinterpret_cast<const uint4*>(from + p.F));
+        }
+      }
+    }
+  }
+  static __device__ __forceinline__ void prefetch_l2(const void* at) { asm volatile("prefetch.global.L2 [%0];" ::"l"(at)); }
+  // 32 rows of four vectors: from four lanes a row to a row a lane.
+  static __device__ __forceinline__ void turn(uint8_t* buf, const uint4* in, uint4* out, int lane) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) *reinterpret_cast<uint4*>(buf + sw64(8 * i + (lane >> 2), lane & 3)) = in[i];
+    __syncwarp();
+#pragma unroll
+    for (int q = 0; q < 4; ++q) out[q] = *reinterpret_cast<const uint4*>(buf + sw64(lane, q));
+    __syncwarp();
+  }
+  // And back, to memory: rows of `to`, ld elements apart.
+  static __device__ __forceinline__ void store(uint8_t* buf, const uint4* v, uint16_t* to, int64_t ld, const Params& p, int row0,
+                                               int f, int lane, uint64_t pol) {
+#pragma unroll
+    for (int q = 0; q < 4; ++q) *reinterpret_cast<uint4*>(buf + sw64(lane, q)) = v[q];
+    __syncwarp();
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int r = 8 * i + (lane >> 2), q = lane & 3;
+      if (row0 + r < p.T && f + 8 * q < p.F)
+        st_stream(to + (row0 + r) * ld + f + 8 * q, *reinterpret_cast<const uint4*>(buf + sw64(r, q)), pol);
+    }
+    __syncwarp();
+  }
+
+  static __device__ __forceinline__ void epilogue(const Maps&, const Params& p, pairs::Shared* ss, uint8_t* epi, int warp,
+                                                  int lane, uint32_t rank) {
     const int quarter = warp & 3, w = warp - pairs::kFirstEpiWarp, sub = w >> 2;
     const uint32_t empty0 = ptx::mapa(ptx::smem_addr(&ss->tmem_empty[0]), 0);
     const int NB = (p.F + codes::kBlock - 1) / codes::kBlock;
-    // A lane computes its own row's bytes of each alone.
-    uint8_t* both = epi + w * (kPair + kOne);  // [gate, up][row][32] bf16, 64-byte swizzle
-    uint8_t* one = both + kPair;               // [row][32] bf16, 64-byte swizzle; or codes [gate, up][row][32], 32-byte swizzle
-    uint64_t* bar = &ss->epi[w];
+    uint8_t* buf = epi + w * kTurn;
     const uint64_t pol = evict_first_policy();  // (what streams through should not displace the operands in L2)
-    uint32_t acc = 0, ph = 0, kept_ph = 0;
-    auto origin = [&](int tile, int& row0, int& f0) {
+    uint32_t acc = 0, ph = 0;
+    for (int tile = pair_id(); tile < p.num_tiles; tile += num_pairs()) {
       int tm, tn;
       tile_coords_of(tile, p.tiles_m, p.tiles_n, tm, tn);
-      row0 = tm * kPairM + static_cast<int>(rank) * kTileM + quarter * 32;
-      f0 = tn * 2 * W + sub * NC;
-    };
-    // Begins the load of what was kept for the chunk at (row0, f); whether there is any of it.
-    auto load = [&](int row0, int f) -> bool {
-      const bool any = row0 < p.T && f < p.F;
-      if (VIA && any && lane == 0) {
-        ptx::mbar_arrive_expect_tx(bar, CODES ? kOne : kPair);
-        uint8_t* to = CODES ? one : both;
-        ptx::tma_load_3d(&maps.kept, bar, to, f, 0, row0);
-        ptx::tma_load_3d(&maps.kept, bar, to + (CODES ? kOne : kPair) / 2, f, 1, row0);
-      }
-      return VIA && any;
-    };
-    bool loaded = false;  // a load is under way
-    for (int tile = pair_id(); tile < p.num_tiles; tile += num_pairs()) {
-      int row0, f0;
-      origin(tile, row0, f0);
-      if (!loaded) loaded = load(row0, f0);
-      if (!pairs::warp_wait(&ss->tmem_full[acc], ph, p, ss, lane)) break;
-      ptx::tc_fence_after();
+      const int row0 = tm * kPairM + static_cast<int>(rank) * kTileM + quarter * 32, f0 = tn * 2 * W + sub * NC;
+      const int64_t row = row0 + lane;
       const uint32_t taddr = ss->tmem_base + (static_cast<uint32_t>(quarter * 32) << 16) + acc * (kTmemCols / kBufs) +
                              static_cast<uint32_t>(sub * NC);
-      const int64_t row = row0 + lane;
-      bool ok = true;
+      bool ready = false;  // the accumulator is
 #pragma unroll 1
-      for (int c = 0; c < NC && row0 < p.T && f0 + c < p.F; c += kChunk) {
-        const int f = f0 + c;
+      for (int f = f0; f < f0 + NC && row0 < p.T && f < p.F; f += kChunk) {
         float gs = 0.f, us = 0.f;
         if (CODES && row < p.T) {
           gs = p.scale[row * 2 * NB + f / codes::kBlock];
           us = p.scale[(row * 2 + 1) * NB + f / codes::kBlock];
         }
-        uint4 gc[2], uc[2];  // CODES: this row's
-        if (VIA) {
-          if (!(ok = pairs::warp_wait(bar, kept_ph, p, ss, lane))) break;
-          kept_ph ^= 1u;
-          loaded = false;
-          if (CODES) {
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              gc[h] = *reinterpret_cast<const uint4*>(one + sw32(lane, h));
-              uc[h] = *reinterpret_cast<const uint4*>(one + kOne / 2 + sw32(lane, h));
+        uint4 kept[kLoads], rows[kLoads];
+        load(kept, p, row0, f, lane);
+        if (!ready) {
+          if (row < p.T && f + kChunk < min(f0 + NC, p.F)) {
+            const int64_t at = row * 2 * p.F + f + kChunk;
+            if (CODES) {
+              prefetch_l2(static_cast<const uint8_t*>(p.codes) + at);
+              prefetch_l2(static_cast<const uint8_t*>(p.codes) + at + p.F);
+            } else {
+              prefetch_l2(static_cast<const uint16_t*>(p.gu) + at);
+              prefetch_l2(static_cast<const uint16_t*>(p.gu) + at + p.F);
             }
-            __syncwarp();  // before Y goes over them
           }
-        } else {
-#pragma unroll
-          for (int h = 0; h < 4; ++h) {
-            uint2 a = make_uint2(0, 0), b = a;
-            if (row < p.T && f + 8 * h < p.F) {
-              const uint8_t* at = static_cast<const uint8_t*>(p.codes) + row * 2 * p.F + f + 8 * h;
-              a = *reinterpret_cast<const uint2*>(at);
-              b = *reinterpret_cast<const uint2*>(at + p.F);
-            }
-            (h & 1 ? gc[h >> 1].z : gc[h >> 1].x) = a.x;
-            (h & 1 ? gc[h >> 1].w : gc[h >> 1].y) = a.y;
-            (h & 1 ? uc[h >> 1].z : uc[h >> 1].x) = b.x;
-            (h & 1 ? uc[h >> 1].w : uc[h >> 1].y) = b.y;
-          }
+          if (!pairs::warp_wait(&ss->tmem_full[acc], ph, p, ss, lane)) return;
+          ptx::tc_fence_after();
+          ready = true;
         }
+#pragma unroll
+        for (int i = 0; i < kLoads; i += 4) turn(buf, kept + i, rows + i, lane);
         float da[kChunk];
-        pairs::tmem_load<kChunk>(taddr + c, da);
-        if (p.act == kActSilu) gradients<kActSilu>(da, gc, uc, gs, us, both, one, lane);
-        else gradients<kActGeluTanh>(da, gc, uc, gs, us, both, one, lane);
-        __syncwarp();
-        // Out, four lanes a row: 64 contiguous bytes of eight rows a store.
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int r = 8 * i + (lane >> 2), q = lane & 3;
-          if (row0 + r < p.T && f + 8 * q < p.F) {
-            const int64_t at = static_cast<int64_t>(row0 + r) * 2 * p.F + f + 8 * q;
-            uint16_t* out = static_cast<uint16_t*>(p.dGU) + at;
-            st_stream(out, *reinterpret_cast<const uint4*>(both + sw64(r, q)), pol);
-            st_stream(out + p.F, *reinterpret_cast<const uint4*>(both + kPair / 2 + sw64(r, q)), pol);
-            if (p.Y != nullptr)
-              st_stream(static_cast<uint16_t*>(p.Y) + static_cast<int64_t>(row0 + r) * p.F + f + 8 * q,
-                        *reinterpret_cast<const uint4*>(one + sw64(r, q)), pol);
-          }
-        }
-        ptx::fence_proxy_async_smem();  // before a copy fills the buffers again
-        __syncwarp();
-        // The next chunk: this tile's, or else the next tile's first.
-        int next_row = row0, next_f = f + kChunk;
-        const bool more = c + kChunk < NC && next_f < p.F;
-        if (!more && tile + num_pairs() < p.num_tiles) origin(tile + num_pairs(), next_row, next_f);
-        if (more || tile + num_pairs() < p.num_tiles) loaded = load(next_row, next_f);
+        pairs::tmem_load<kChunk>(taddr + (f - f0), da);
+        uint4 dg[4], du[4], y[4];
+        if (p.act == kActSilu) gradients<kActSilu>(da, rows, gs, us, dg, du, y);
+        else gradients<kActGeluTanh>(da, rows, gs, us, dg, du, y);
+        store(buf, dg, static_cast<uint16_t*>(p.dGU), int64_t{2} * p.F, p, row0, f, lane, pol);
+        store(buf, du, static_cast<uint16_t*>(p.dGU) + p.F, int64_t{2} * p.F, p, row0, f, lane, pol);
+        if (p.Y != nullptr) store(buf, y, static_cast<uint16_t*>(p.Y), p.F, p, row0, f, lane, pol);
       }
-      if (!ok) break;
+      if (!ready && !pairs::warp_wait(&ss->tmem_full[acc], ph, p, ss, lane)) return;  // nothing of it is this warp's
       ptx::tc_fence_before();
       __syncwarp();
       if (lane == 0) ptx::mbar_arrive_cluster_tmem(empty0 + acc * 8u);
@@ -334,29 +337,28 @@ struct GatedGradOp {
         ph ^= 1u;
       }
     }
-    if (loaded && lane == 0) pairs::wait(bar, kept_ph, p, ss, false);  // (a load begun before the block gave up)
-    __syncwarp();
   }
 
-  // A lane's 32 features: dG and dU over G and U, and Y.
+  // A lane's 32 features, G in the first half of `rows` and U in the second: dG, dU and Y.
   template <int ACT>
-  static __device__ __forceinline__ void gradients(const float (&da)[kChunk], const uint4 (&gc)[2], const uint4 (&uc)[2], float gs,
-                                                   float us, uint8_t* both, uint8_t* one, int lane) {
+  static __device__ __forceinline__ void gradients(const float (&da)[kChunk], const uint4 (&rows)[kLoads], float gs, float us,
+                                                   uint4 (&dg)[4], uint4 (&du)[4], uint4 (&out)[4]) {
 #pragma unroll
-    for (int q = 0; q < kChunk / 8; ++q) {
+    for (int q = 0; q < 4; ++q) {
       float g[8], u[8], y[8];
-      if (CODES) {
-        decode8(q & 1 ? make_uint2(gc[q >> 1].z, gc[q >> 1].w) : make_uint2(gc[q >> 1].x, gc[q >> 1].y), gs, g);
-        decode8(q & 1 ? make_uint2(uc[q >> 1].z, uc[q >> 1].w) : make_uint2(uc[q >> 1].x, uc[q >> 1].y), us, u);
+      if constexpr (CODES) {
+        const uint4 a = rows[q >> 1], b = rows[2 + (q >> 1)];
+        decode8(q & 1 ? make_uint2(a.z, a.w) : make_uint2(a.x, a.y), gs, g);
+        decode8(q & 1 ? make_uint2(b.z, b.w) : make_uint2(b.x, b.y), us, u);
       } else {
-        unpack_bf16x8(*reinterpret_cast<const uint4*>(both + sw64(lane, q)), g);
-        unpack_bf16x8(*reinterpret_cast<const uint4*>(both + kPair / 2 + sw64(lane, q)), u);
+        unpack_bf16x8(rows[q], g);
+        unpack_bf16x8(rows[4 + q], u);
       }
 #pragma unroll
       for (int j = 0; j < 8; ++j) gated_gradient<ACT>(da[8 * q + j], g[j], u[j], g[j], u[j], y[j]);
-      *reinterpret_cast<uint4*>(both + sw64(lane, q)) = pack_rne_bf16x8(g);
-      *reinterpret_cast<uint4*>(both + kPair / 2 + sw64(lane, q)) = pack_rne_bf16x8(u);
-      *reinterpret_cast<uint4*>(one + sw64(lane, q)) = pack_rne_bf16x8(y);
+      dg[q] = pack_rne_bf16x8(g);
+      du[q] = pack_rne_bf16x8(u);
+      out[q] = pack_rne_bf16x8(y);
     }
   }
 
@@ -386,16 +388,14 @@ cudaError_t launch_gated(int width, const CUtensorMap& x, const CUtensorMap& w, 
 }
 
 template <int W>
-static cudaError_t run_grad(const CUtensorMap& dy, const CUtensorMap& w, const CUtensorMap& kept, const GatedParams& p,
-                            int pairs_n, cudaStream_t s) {
-  if (p.codes == nullptr) return pairs::launch<GatedGradOp<W, false, true>>(dy, w, {kept}, p, pairs_n, s);
-  if (p.F % 16 == 0) return pairs::launch<GatedGradOp<W, true, true>>(dy, w, {kept}, p, pairs_n, s);
-  return pairs::launch<GatedGradOp<W, true, false>>(dy, w, {kept}, p, pairs_n, s);
+static cudaError_t run_grad(const CUtensorMap& dy, const CUtensorMap& w, const GatedParams& p, int pairs_n, cudaStream_t s) {
+  if (p.codes == nullptr) return pairs::launch<GatedGradOp<W, false>>(dy, w, {}, p, pairs_n, s);
+  return pairs::launch<GatedGradOp<W, true>>(dy, w, {}, p, pairs_n, s);
 }
 
-cudaError_t launch_gated_grad(int width, const CUtensorMap& dy, const CUtensorMap& w, const CUtensorMap& kept,
-                              const GatedParams& p, int pairs_n, cudaStream_t s) {
-  return width == 128 ? run_grad<128>(dy, w, kept, p, pairs_n, s) : run_grad<64>(dy, w, kept, p, pairs_n, s);
+cudaError_t launch_gated_grad(int width, const CUtensorMap& dy, const CUtensorMap& w, const GatedParams& p, int pairs_n,
+                              cudaStream_t s) {
+  return width == 128 ? run_grad<128>(dy, w, p, pairs_n, s) : run_grad<64>(dy, w, p, pairs_n, s);
 }
 
 }  // namespace forge

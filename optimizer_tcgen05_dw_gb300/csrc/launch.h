@@ -195,10 +195,8 @@ cudaError_t launch_gated(int width, const CUtensorMap& x, const CUtensorMap& w, 
 // few_rows.cu: the forward of at most kFewGated rows, without codes.
 constexpr int64_t kFewGated = 8;
 cudaError_t launch_gated_few(const void* W, const void* X, const GatedParams& p, int K, cudaStream_t s);
-// kept: gu, or gu_codes, as [T x 2 x F] in boxes of 32 features x 1 x 32 rows
-// (64-byte swizzle; codes 32-byte; any valid map for codes with F % 16 != 0).
-cudaError_t launch_gated_grad(int width, const CUtensorMap& dy, const CUtensorMap& w, const CUtensorMap& kept,
-                              const GatedParams& p, int pairs, cudaStream_t s);
+cudaError_t launch_gated_grad(int width, const CUtensorMap& dy, const CUtensorMap& w, const GatedParams& p, int pairs,
+                              cudaStream_t s);
 
 // The product of block-scaled codes (product.cu); num_kb blocks of 128.
 struct ProductParams : PairParams {
@@ -212,7 +210,7 @@ cudaError_t launch_product(int width, const CUtensorMap& x, const CUtensorMap& w
                            const ProductParams& p, int pairs, cudaStream_t s);
 // few_rows.cu: the product of at most kFewProduct rows.
 constexpr int64_t kFewProduct = 16;
-cudaError_t launch_product_few(const void* W, const void* X, const ProductParams& p, int K, cudaStream_t s);
+cudaError_t launch_product_few(const void* W, const void* X, const ProductParams& p, int K, int num_sms, cudaStream_t s);
 
 // Values to E4M3 codes in blocks of 128 and back (codes.cu).
 struct CodesParams {

@@ -79,6 +79,14 @@ def test_normal_data(T, N, K):
     assert (off <= want.abs() * 2.0 ** -8 + size * ((K / 32 + K / 128 + 4) * 2.0 ** -23)).all()
 
 
+@pytest.mark.parametrize("N,K", [(2432, 2064), (2440, 272), (4104, 1040)])
+@pytest.mark.parametrize("T", [1, 7, 8, 9, 16, 17, 32])
+def test_exact_sums_of_few_rows(T, N, K):
+    """On either side of the rows, and of the features (16 for each of 152 SMs), at which another form takes over."""
+    a = _whole((T, K), 1), _powers((T, blocks(K)), 2), _whole((N, K), 3), _powers((blocks(N), blocks(K)), 4)
+    assert torch.equal(_product(*a), _exact(*a)[0].float().to(B16))
+
+
 def test_factors_out_of_float32s_range():
     """Scales whose product is not a normal float32, though the values are."""
     T, N, K = 8, 128, 512
@@ -104,6 +112,23 @@ def test_values_that_are_not_finite():
     bad = torch.isnan(_product(xq, xs, wq, ws))
     want = torch.zeros_like(bad)
     want[3], want[70], want[:, 256:] = True, True, True
+    assert torch.equal(bad, want)
+
+
+@pytest.mark.parametrize("T", [6, 13])
+def test_values_that_are_not_finite_in_few_rows(T):
+    """The same in the products of a few rows; codes of either sign, in each place of a word."""
+    xq, xs, wq, ws = _random(T, 2568, 2064)
+    for t, k in ((0, 3), (2, 130), (5, 2061)):
+        xq.view(torch.uint8)[t, k] = 0x7F if t else 0xFF
+    wq.view(torch.uint8)[2567, 17], wq.view(torch.uint8)[40, 2062] = 0xFF, 0x7F
+    ws[3, 1] = float("nan")
+    xs[T - 2, 16] = float("nan")
+    bad = torch.isnan(_product(xq, xs, wq, ws))
+    want = torch.zeros_like(bad)
+    want[[0, 2, 5, T - 2]] = True
+    want[:, [2567, 40]] = True
+    want[:, 384:512] = True
     assert torch.equal(bad, want)
 
 
