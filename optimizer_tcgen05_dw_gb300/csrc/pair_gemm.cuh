@@ -254,16 +254,6 @@ done:
   __syncwarp();
 }
 
-// Four bytes global -> shared, without a register on the way, and an arrival on
-// `bar` (counted in its expected arrivals) when this thread's copies so far are there.
-__device__ __forceinline__ void copy4(uint32_t to, const float* from) {
-  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(to), "l"(from) : "memory");
-}
-__device__ __forceinline__ void arrive_when_copied(uint64_t* bar) {
-  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(ptx::smem_addr(bar)) : "memory");
-}
-__device__ __forceinline__ void copies_wait() { asm volatile("cp.async.wait_all;" ::: "memory"); }
-
 // NC consecutive fp32 columns of this warp's 32 tensor-memory lanes.
 template <int NC>
 __device__ __forceinline__ void tmem_load(uint32_t taddr, float (&v)[NC]) {

@@ -17,10 +17,10 @@ namespace {
 
 // An epilogue warp holds 32 token rows (the lanes of its quarter of tensor
 // memory) x W / 2 columns of the sum in registers.  What it does besides folding is
-// kept small, as it is this loop that the tensor cores wait for: the scales come
-// through shared memory, kGroup stages at a time, by asynchronous copies of the
-// two helper warps (a lane's loads of its own row, a line each, took 300 ns and
-// more every few stages; registers to wait in there are none).
+// kept small, as it is this loop that the tensor cores wait for: the factors, a
+// product of two scales each, come through shared memory from the two helper
+// warps, kGroup stages at a time and up to kSlots of these ahead (16384 x 14336 x
+// 4096: 790 us; 832 where those copied the scales and the epilogue multiplied them).
 // At W = 128 a stage is multiplied in two halves (kSplit), each with accumulators
 // of its own, so that four are under way: an accumulator's way through commit,
 // epilogue and back is longer than the instructions of two.
@@ -35,8 +35,9 @@ struct ProductOp {
   static constexpr bool kStaged = W == 128 && AROWS == kTileM;
   static constexpr int kStage = kStaged ? 32 * LD * 2 : 0;     // bytes a warp stages its rows in
   static constexpr int kGroup = 4, kSlots = 4;                 // stages in a slot of scales, slots
-  static constexpr int kStageFloats = kTileM + kBlk;           // a stage's scales: 128 rows', W's blocks'
-  static constexpr int kSlotFloats = kGroup * kStageFloats;
+  static constexpr int kStageFloats = kBlk * kTileM;           // a stage's factors: [W's block][row]
+  static constexpr int kWide = kBlk * 4;                       // a slot's flags: [W's block][quarter of the rows]
+  static constexpr int kSlotFloats = kGroup * kStageFloats + kWide;
   static constexpr int kEpiBytes = kEpiWarps * kStage + ((kSlots * kSlotFloats * 4 + 127) & ~127);
   static constexpr bool kMoreRegs = true, kFp8 = true, kBMajorMN = false, kBlockwise = true;
 
@@ -44,18 +45,19 @@ struct ProductOp {
 
   static __device__ __forceinline__ void init_barriers(pairs::Shared* ss) {
     for (int i = 0; i < kSlots; ++i) {
-      ptx::mbar_init(&ss->epi[i], 64);                  // a slot's scales are there: both helper warps' lanes
+      ptx::mbar_init(&ss->epi[i], 64);                  // a slot's factors are there: both helper warps' lanes
       ptx::mbar_init(&ss->epi[kSlots + i], kEpiWarps);  // and have been read
     }
   }
-  static __device__ __forceinline__ float* scales(uint8_t* epi) { return reinterpret_cast<float*>(epi + kEpiWarps * kStage); }
+  static __device__ __forceinline__ float* factors(uint8_t* epi) { return reinterpret_cast<float*>(epi + kEpiWarps * kStage); }
 
-  // Helper warp 2 + i copies the scales of rows 64 i .. 64 i + 63, two a lane.
-  // Rows and columns past the end repeat the last one's; nothing of theirs is stored.
+  // Helper warp 2 + i forms the factors of rows 64 i .. 64 i + 63, two a lane, and
+  // says of each quarter of the tile's rows whether some factor in a slot is not
+  // an ordinary number.  Rows and columns past the end repeat the last one's;
+  // nothing of theirs is stored.
   static __device__ __forceinline__ void helper(const Params& p, pairs::Shared* ss, uint8_t* epi, int warp, int lane,
                                                 uint32_t rank) {
     const int row = (warp - 2) * 64 + lane;
-    const uint32_t out = ptx::smem_addr(scales(epi)) + row * 4;
     int slot = 0;
     uint32_t ph = 0;
     for (int tile = pair_id(); tile < p.num_tiles; tile += num_pairs()) {
@@ -64,29 +66,47 @@ struct ProductOp {
       const int row0 = tm * kPairM + static_cast<int>(rank) * kTileM + row;
       const float* sx0 = p.x_scale + static_cast<int64_t>(min(row0, p.T - 1)) * p.num_kb;
       const float* sx1 = p.x_scale + static_cast<int64_t>(min(row0 + 32, p.T - 1)) * p.num_kb;
-      const float* sw = p.w_scale + static_cast<int64_t>(min(tn * 2 * W + (lane % kBlk) * W, p.N - 1) / codes::kBlock) * p.num_kb;
-      for (int kb = 0; kb < p.num_kb; kb += kGroup) {
-        if (!pairs::warp_wait(&ss->epi[kSlots + slot], ph ^ 1u, p, ss, lane)) {
-          pairs::copies_wait();
-          return;
-        }
-        const uint32_t to = out + slot * kSlotFloats * 4;
+      const float* sw[kBlk];
 #pragma unroll
-        for (int j = 0; j < kGroup; ++j)
-          if (kb + j < p.num_kb) {
-            pairs::copy4(to + j * kStageFloats * 4, sx0 + kb + j);
-            pairs::copy4(to + (j * kStageFloats + 32) * 4, sx1 + kb + j);
+      for (int b = 0; b < kBlk; ++b)
+        sw[b] = p.w_scale + static_cast<int64_t>(min(tn * 2 * W + b * W, p.N - 1) / codes::kBlock) * p.num_kb;
+      for (int kb = 0; kb < p.num_kb; kb += kGroup) {
+        if (!pairs::warp_wait(&ss->epi[kSlots + slot], ph ^ 1u, p, ss, lane)) return;
+        float* to = factors(epi) + slot * kSlotFloats;
+        uint32_t odd = 0;  // bit 2 b + i: some factor of this lane's row i with block b is
+#pragma unroll 1
+        for (int j = 0; j < kGroup; j += 2) {  // (two stages at a time: the warp has 32 registers)
+          float x[2][2], ws[2][kBlk];
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const int at = min(kb + j + h, p.num_kb - 1);
+            x[h][0] = sx0[at];
+            x[h][1] = sx1[at];
+#pragma unroll
+            for (int b = 0; b < kBlk; ++b) ws[h][b] = sw[b][at];
           }
-        if (warp == 2 && lane < kGroup * kBlk && kb + lane / kBlk < p.num_kb)
-          pairs::copy4(out + (slot * kSlotFloats + (lane / kBlk) * kStageFloats + kTileM + lane % kBlk - lane) * 4, sw + kb + lane / kBlk);
-        pairs::arrive_when_copied(&ss->epi[slot]);
+#pragma unroll
+          for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int b = 0; b < kBlk; ++b)
+#pragma unroll
+              for (int i = 0; i < 2; ++i) {
+                const float f = x[h][i] * ws[h][b];
+                // (blocks of zeros, as padding rows have, are ordinary: their factor is 0 itself)
+                if (!((f > 0x1p-100f && f < 0x1p100f) || x[h][i] == 0.f || ws[h][b] == 0.f)) odd |= 1u << (2 * b + i);
+                to[(j + h) * kStageFloats + b * kTileM + 32 * i + row] = f;
+              }
+        }
+        odd = __reduce_or_sync(0xFFFFFFFFu, odd);
+        if (lane < 2 * kBlk)
+          to[kGroup * kStageFloats + (lane >> 1) * 4 + (warp - 2) * 2 + (lane & 1)] = (odd >> lane) & 1u ? 1.f : 0.f;
+        ptx::mbar_arrive(&ss->epi[slot]);
         if (++slot == kSlots) {
           slot = 0;
           ph ^= 1u;
         }
       }
     }
-    pairs::copies_wait();
   }
 
   // acc += v f; where some lane's factor is not an ordinary number, in two parts.
@@ -115,7 +135,8 @@ struct ProductOp {
     const uint32_t tbase = ss->tmem_base + (static_cast<uint32_t>(quarter * 32) << 16) +
                            static_cast<uint32_t>(kSplit == 2 ? blk * NC : sub * NC);
     uint8_t* stage = epi + w * kStage;
-    const float* own = scales(epi) + quarter * 32 + lane;
+    const float* own = factors(epi) + blk * kTileM + quarter * 32 + lane;
+    const float* flag = factors(epi) + kGroup * kStageFloats + blk * 4 + quarter;
     uint32_t buf = half, ph = 0, slot_ph = 0;
     int slot = 0;
     for (int tile = pair_id(); tile < p.num_tiles; tile += num_pairs()) {
@@ -129,18 +150,10 @@ struct ProductOp {
 #pragma unroll 1
       for (int kb0 = 0; kb0 < p.num_kb; kb0 += kGroup) {
         if (!pairs::warp_wait(&ss->epi[slot], slot_ph, p, ss, lane)) return;
-        const float* at = own + slot * kSlotFloats;
-        const float* w_at = scales(epi) + slot * kSlotFloats + kTileM + blk;
         float f[kGroup];
-        bool mine = true;
 #pragma unroll
-        for (int j = 0; j < kGroup; ++j) {
-          const float xs = at[j * kStageFloats], ws = w_at[j * kStageFloats];
-          f[j] = xs * ws;
-          // (blocks of zeros, as padding rows have, are ordinary: their factor is 0 itself)
-          mine = mine && ((f[j] > 0x1p-100f && f[j] < 0x1p100f) || xs == 0.f || ws == 0.f || kb0 + j >= p.num_kb);
-        }
-        const bool wide = !__all_sync(0xFFFFFFFFu, mine);
+        for (int j = 0; j < kGroup; ++j) f[j] = own[slot * kSlotFloats + j * kStageFloats];
+        const bool wide = flag[slot * kSlotFloats] != 0.f;
         __syncwarp();  // the slot has been read
         if (lane == 0) ptx::mbar_arrive(&ss->epi[kSlots + slot]);
         if (++slot == kSlots) {
