@@ -438,7 +438,7 @@ typedef enum forge_act { FORGE_ACT_SILU = 0, FORGE_ACT_GELU_TANH = 1 } forge_act
  *   gu        bf16 [T x 2F]: row t is G[t], then U[t]
  *   gu_codes  E4M3 codes [T x 2F] with gu_scale [T x 2 x ceil(F / 128)]: the
  *             format of forge_quantize_e4m3 over the [2T x F] matrix, of the
- *             float32 G and U (a scale carries the error of their K-term sums)
+ *             float32 G and U (a scale carries the error of their sums)
  * F % 8 == 0, K % 8 == 0; T, 2F and K within 31 bits; T == 0 or F == 0 does
  * nothing, K == 0 gives zeros.  An infinite G or U gives what the formula
  * does (inf * 0 is NaN).  The outputs overlap neither the inputs nor each other. */

@@ -46,9 +46,9 @@ constexpr int kLeastWidth = 32;
 // token operand is loaded and read again for each, and its stages are short):
 // 62 and 54 where the widest costs 100.  us at widths 128, 64 and 32 (product:
 // codes; else the gated forward, of 2 F rows of weights):
-//   300 x 14336 x 4096   68  85 150      128 x 14336 x 4096   55  50  79
-//   24 x 2048 x 4096     27  21  22      product 33 x 4096 x 14336  60  41  37
-//   product 1531 x 5120 x 17408  139 179 257
+//   300 x 14336 x 4096   66  78 137      128 x 14336 x 4096   52  48  72
+//   24 x 2048 x 4096     25  19  21      product 33 x 4096 x 14336  58  38  37
+//   product 1531 x 5120 x 17408  135 166 261      product 300 x 14336 x 4096  40  38  58
 // `halves`: B halves side by side in a tile's output columns (2), or on top of
 // each other (1: gate and up).
 int pick_width(int64_t rows, int64_t cols, int halves, int least, int pairs) {

@@ -39,7 +39,14 @@ struct GatedOp {
   static constexpr bool kRows = W == 128 && AROWS == kTileM;  // outputs meet in shared memory, to leave by rows
   static constexpr int kOut = kRows ? 32 * 32 * 2 : 0;        // a warp's bytes of it: 32 rows x 32 bf16
   static constexpr int kEpiBytes = pairs::kEpiWarps * kOut + (CODES ? 2 * 4 * kTileM * 4 : 0);
-  static constexpr bool kMoreRegs = W == 128, kFp8 = false, kBMajorMN = false, kBlockwise = false;
+  static constexpr bool kMoreRegs = W == 128, kFp8 = false, kBMajorMN = false;
+  // The tensor cores' sums are truncated, 1e-9 of a sum for each of its terms on
+  // average: nothing beside bf16, but the scales of the codes are float32.  So
+  // these are summed over 64 kFold terms at a time, and the sums in registers
+  // (mean error of a scale at K = 5120: -5.0e-6 in one sum, -6.2e-7 so;
+  // 4099 x 17408 tokens and features 800 us either way, 838 with kFold = 8: the
+  // tensor cores then wait for the outputs of the tile before).
+  static constexpr int kFold = CODES ? 12 : 0;
 
   // rank 0: gate rows, rank 1: up rows of the same features (rows of another
   // half past a ragged end give columns that are not stored)
@@ -60,25 +67,41 @@ struct GatedOp {
       tile_coords_of(tile, p.tiles_m, p.tiles_n, tm, tn);
       const int64_t row = static_cast<int64_t>(tm) * kPairM + static_cast<int>(rank) * kTileM + r;
       const int f0 = tn * W + sub * NC;
-      const bool ok = pairs::warp_wait(&ss->tmem_full[acc], ph, p, ss, lane);
-      if (CODES) {  // the quarter's warps meet below: they stop together
-        if (ptx::bar_red_or(kQuarterBarrier + quarter, 128, !ok)) return;
+      float g[NC], u[NC];
+      // Hands the accumulator on after reading columns of it with `take`.
+      auto read = [&](auto&& take) -> bool {
+        if (!pairs::warp_wait(&ss->tmem_full[acc], ph, p, ss, lane)) return false;
+        ptx::tc_fence_after();
+        take(ss->tmem_base + (static_cast<uint32_t>(quarter * 32) << 16) + acc * (kTmemCols / kBufs) +
+             static_cast<uint32_t>(sub * NC));
+        ptx::tc_fence_before();
+        __syncwarp();
+        if (lane == 0) ptx::mbar_arrive_cluster_tmem(empty0 + acc * 8u);
+        if (++acc == kBufs) {
+          acc = 0;
+          ph ^= 1u;
+        }
+        return true;
+      };
+      bool ok = read([&](uint32_t at) {
+        pairs::tmem_load<NC>(at, g);
+        pairs::tmem_load<NC>(at + W, u);
+      });
+      if constexpr (CODES) {
+        for (int kb = kFold; ok && kb < p.num_kb; kb += kFold)
+          ok = read([&](uint32_t at) {
+            float v[NC];
+            pairs::tmem_load<NC>(at, v);
+#pragma unroll
+            for (int j = 0; j < NC; ++j) g[j] += v[j];
+            pairs::tmem_load<NC>(at + W, v);
+#pragma unroll
+            for (int j = 0; j < NC; ++j) u[j] += v[j];
+          });
+        if (ptx::bar_red_or(kQuarterBarrier + quarter, 128, !ok)) return;  // the quarter's warps meet below: they stop together
         __syncwarp();
       } else if (!ok) {
         return;
-      }
-      ptx::tc_fence_after();
-      const uint32_t taddr = ss->tmem_base + (static_cast<uint32_t>(quarter * 32) << 16) + acc * (kTmemCols / kBufs) +
-                             static_cast<uint32_t>(sub * NC);
-      float g[NC], u[NC];
-      pairs::tmem_load<NC>(taddr, g);
-      pairs::tmem_load<NC>(taddr + W, u);
-      ptx::tc_fence_before();
-      __syncwarp();
-      if (lane == 0) ptx::mbar_arrive_cluster_tmem(empty0 + acc * 8u);
-      if (++acc == kBufs) {
-        acc = 0;
-        ph ^= 1u;
       }
       float gs = 0.f, us = 0.f;
       if (CODES) {
@@ -215,7 +238,8 @@ struct GatedGradOp {
   static constexpr int kTurn = 32 * kChunk * 2;        // bytes of a chunk of one tensor in bf16
   static constexpr int kLoads = CODES ? 4 : 8;         // 16-byte vectors a lane loads of a chunk
   static constexpr int kEpiBytes = pairs::kEpiWarps * kTurn;
-  static constexpr bool kMoreRegs = false, kFp8 = false, kBMajorMN = true, kBlockwise = false;
+  static constexpr bool kMoreRegs = false, kFp8 = false, kBMajorMN = true;
+  static constexpr int kFold = 0;
 
   static __device__ __forceinline__ int b_row(int tn, int rank, const Params&) { return (2 * tn + rank) * W; }
   static __device__ __forceinline__ void init_barriers(pairs::Shared*) {}

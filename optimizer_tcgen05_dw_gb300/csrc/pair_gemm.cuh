@@ -16,8 +16,8 @@
 //   Op::Params                    with PairParams as its base
 //   kW, kFp8, kBMajorMN           columns of B per CTA; E4M3 operands; B stored
 //                                 with its columns contiguous
-//   kBlockwise                    the accumulator is handed over after every
-//                                 stage (and starts from zero), not after a tile
+//   kFold                         stages after which the accumulator is handed over
+//                                 (and starts from zero), 0: after a tile
 //   kEpiBytes, kMoreRegs          the epilogue's shared memory; whether it takes
 //                                 registers from the first warpgroup
 //   kStg, kBufs                   ring stages, accumulators
@@ -114,7 +114,7 @@ struct Layout {
   static_assert(Op::kStg <= kMaxStages && Op::kBufs <= kMaxBufs, "barrier arrays");
   static constexpr int kBufCols = kTmemCols / Op::kBufs;  // tensor-memory columns of an accumulator
   static_assert(kBufCols * Op::kSplit >= 2 * Op::kW && Op::kBufs % Op::kSplit == 0, "accumulators");
-  static_assert(Op::kSplit == 1 || (Op::kBlockwise && !Op::kBMajorMN), "halves of a stage");
+  static_assert(Op::kSplit == 1 || (Op::kFold == 1 && !Op::kBMajorMN), "halves of a stage");
   static constexpr int kThreads = 32 * (kFirstEpiWarp + kEpiWarps);
   // 65536 registers give 640 threads 96 each, five warpgroups 480; kMoreRegs:
   // the first keeps 32 and the epilogue's take 112 (32 + 4 x 112 = 480).
@@ -214,7 +214,7 @@ __device__ __forceinline__ void issue_stage(uint32_t d, uint32_t alo, uint32_t b
 template <class Op>
 __device__ __forceinline__ void mma(const typename Op::Params& p, uint8_t* smA, uint8_t* smB, Shared* ss, int lane) {
   using L = Layout<Op>;
-  constexpr int STG = Op::kStg, BK = L::kBK;
+  constexpr int STG = Op::kStg, BK = L::kBK, kFold = Op::kFold > 0 ? Op::kFold : 1 << 30;
   constexpr uint32_t idesc = Op::kFp8 ? ptx::idesc_e4m3_f32(kPairM, 2 * Op::kW / Op::kSplit)
                                       : ptx::idesc_bf16_f32(kPairM, 2 * Op::kW, false, Op::kBMajorMN);
   // 8-row (or 8-column-atom) groups 1 KiB apart; B stored by columns: atoms of
@@ -226,15 +226,15 @@ __device__ __forceinline__ void mma(const typename Op::Params& p, uint8_t* smA, 
   uint32_t s = 0, ph = 0, acc = 0, aph = 0;
   for (int tile = pair_id(); tile < p.num_tiles; tile += num_pairs()) {
     for (int kb = 0; kb < p.num_kb; ++kb) {
-      const bool last = Op::kBlockwise || kb == p.num_kb - 1;
+      const bool first = kb % kFold == 0, last = kb % kFold == kFold - 1 || kb == p.num_kb - 1;
 #pragma unroll
       for (uint32_t h = 0; h < Op::kSplit; ++h) {
-        if ((Op::kBlockwise || kb == 0) && !warp_wait(&ss->tmem_empty[acc], aph ^ 1u, p, ss, lane)) goto done;
+        if (first && !warp_wait(&ss->tmem_empty[acc], aph ^ 1u, p, ss, lane)) goto done;
         if (h == 0 && !warp_wait(&ss->full[s], ph, p, ss, lane)) goto done;
         ptx::tc_fence_after();
         issue_stage<Op::kFp8, Op::kBMajorMN ? 2048 / 16 : 2>(
             tmem + acc * L::kBufCols, alo + s * (L::kAStage / 16), blo + s * (L::kB / 16) + h * (L::kB / Op::kSplit / 16), hi,
-            idesc, Op::kBlockwise || kb == 0 ? 0u : 1u, empty0 + s * 8u, full0 + acc * 8u, h == Op::kSplit - 1 ? 1u : 0u,
+            idesc, first ? 0u : 1u, empty0 + s * 8u, full0 + acc * 8u, h == Op::kSplit - 1 ? 1u : 0u,
             last ? 1u : 0u);
         if (last && ++acc == Op::kBufs) {
           acc = 0;

@@ -34,12 +34,13 @@ struct ProductOp {
   static constexpr int kBlk = W == 128 ? 2 : 1;                // blocks of W's scales they lie in
   static constexpr bool kStaged = W == 128 && AROWS == kTileM;
   static constexpr int kStage = kStaged ? 32 * LD * 2 : 0;     // bytes a warp stages its rows in
-  static constexpr int kGroup = 4, kSlots = 4;                 // stages in a slot of scales, slots
+  static constexpr int kGroup = 4, kSlots = 4;                 // stages in a slot of factors, slots
   static constexpr int kStageFloats = kBlk * kTileM;           // a stage's factors: [W's block][row]
   static constexpr int kWide = kBlk * 4;                       // a slot's flags: [W's block][quarter of the rows]
   static constexpr int kSlotFloats = kGroup * kStageFloats + kWide;
   static constexpr int kEpiBytes = kEpiWarps * kStage + ((kSlots * kSlotFloats * 4 + 127) & ~127);
-  static constexpr bool kMoreRegs = true, kFp8 = true, kBMajorMN = false, kBlockwise = true;
+  static constexpr bool kMoreRegs = true, kFp8 = true, kBMajorMN = false;
+  static constexpr int kFold = 1;
 
   static __device__ __forceinline__ int b_row(int tn, int rank, const Params&) { return (2 * tn + rank) * W; }
 

@@ -118,6 +118,17 @@ def test_kept_projections_of_exact_sums(T, F, K):
     assert torch.equal(outs[2][2].view(torch.uint8).reshape(-1), codes.view(torch.uint8).view(-1))
 
 
+def test_scales_of_long_sums():
+    """Scales are float32, so their sums are cut: 768 terms an instruction of 16 at a time (48 u, were each a
+    truncation), the cuts added with half a u each and the division half of one.  Terms of one sign lose most."""
+    T, F, K = 33, 264, 8200
+    X, W = inputs.normal((T, K), 1.0, 1, device="cuda").abs(), inputs.normal((2 * F, K), 0.02, 2, device="cuda").abs()
+    scale = forward(X, W, "silu", "e4m3")[3].double().view(2 * T, -1)
+    sums = (X.double() @ W.double().t()).view(2 * T, F)
+    most = torch.stack([c.amax(1) for c in sums.split(128, 1)], 1) / 448
+    assert ((scale - most).abs() <= most * ((48 + K / 768 + 2) * U)).all()
+
+
 def gradient(dY, Wd, kind, gu=None, codes=None, scale=None, want_y=True, inplace=False):
     T, F = dY.shape[0], Wd.shape[1]
     dGU = gu if inplace else guarded(T, 2 * F)
