@@ -523,7 +523,9 @@ FORGE_API forge_status_t forge_set_wait_limit_ns(uint64_t ns);
 
 /* Test hook for the failure path: while nonzero, the tensor-core kernels'
  * load-issuing warp issues nothing (and the token-contiguous norm sends its
- * cluster nothing), so the consumers' bounded waits expire.
+ * cluster nothing), so the consumers' bounded waits expire.  At 2 the gated
+ * products and the product of codes load what each CTA pair's first tile needs,
+ * so that the waits expire with results on their way out.
  * Never set it outside tests. */
 FORGE_API forge_status_t forge_debug_skip_loads(int32_t enable);
 

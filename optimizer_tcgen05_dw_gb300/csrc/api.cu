@@ -61,7 +61,7 @@ static std::atomic<int32_t> g_skip_loads{0};
 static std::atomic<int32_t> g_step_fusion{1};
 
 uint64_t wait_limit_ns() { return g_wait_limit_ns.load(); }
-bool skip_loads() { return g_skip_loads.load() != 0; }
+int skip_loads() { return g_skip_loads.load(); }
 
 // ---------------------------------------------------------------- per device
 
@@ -972,7 +972,7 @@ forge_status_t forge_set_wait_limit_ns(uint64_t ns) {
 }
 
 forge_status_t forge_debug_skip_loads(int32_t enable) {
-  g_skip_loads.store(enable ? 1 : 0);
+  g_skip_loads.store(enable == 2 ? 2 : enable != 0);
   return FORGE_OK;
 }
 

@@ -74,7 +74,7 @@ void set_tiles(PairParams* p, int64_t rows, int64_t cols, int64_t wide, int64_t 
   p->tiles_n = static_cast<int32_t>(tn);
   p->num_tiles = static_cast<int32_t>(tm * tn);
   p->num_kb = static_cast<int32_t>(stages);
-  p->skip_loads = skip_loads() ? 1 : 0;
+  p->skip_loads = skip_loads();
   p->wait_limit_ns = wait_limit_ns();
   p->status = d.status;
 }

@@ -29,7 +29,7 @@ forge_status_t device_info(DeviceInfo* out);
 forge_status_t check_device(const DeviceInfo& d);
 
 uint64_t wait_limit_ns();
-bool skip_loads();
+int skip_loads();
 
 forge_status_t tensor_map(CUtensorMap* m, const void* base, CUtensorMapDataType dtype, int esize,
                           int64_t inner, int64_t outer, uint32_t box_inner, uint32_t box_outer,

@@ -150,7 +150,7 @@ struct ProductOp {
       for (int i = 0; i < NC; ++i) acc[i] = 0.f;
 #pragma unroll 1
       for (int kb0 = 0; kb0 < p.num_kb; kb0 += kGroup) {
-        if (!pairs::warp_wait(&ss->epi[slot], slot_ph, p, ss, lane)) return;
+        if (!pairs::warp_wait(&ss->epi[slot], slot_ph, p, ss, lane)) goto drain;
         float f[kGroup];
 #pragma unroll
         for (int j = 0; j < kGroup; ++j) f[j] = own[slot * kSlotFloats + j * kStageFloats];
@@ -164,7 +164,7 @@ struct ProductOp {
 #pragma unroll
         for (int j = 0; j < kGroup; ++j) {
           if (kb0 + j >= p.num_kb) break;
-          if (!pairs::warp_wait(&ss->tmem_full[buf], ph, p, ss, lane)) return;
+          if (!pairs::warp_wait(&ss->tmem_full[buf], ph, p, ss, lane)) goto drain;
           ptx::tc_fence_after();
           const uint32_t taddr = tbase + buf * kBufCols;
 #pragma unroll
@@ -210,7 +210,9 @@ struct ProductOp {
         }
       }
     }
+  drain:  // (after a wait that ran out too: the copies under way read this block's shared memory)
     if (kStaged && lane == 0) ptx::bulk_wait_group0();
+    __syncwarp();
   }
 };
 
