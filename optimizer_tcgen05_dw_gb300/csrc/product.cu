@@ -173,6 +173,7 @@ struct ProductOp {
             pairs::tmem_load<LD>(taddr + c * LD, v);
             if (c == NC / LD - 1) {  // all of it is in registers
               ptx::tc_fence_before();
+              __syncwarp();  // (every lane's reads, not only lane 0's, come before the arrival)
               if (lane == 0) ptx::mbar_arrive_cluster_tmem(empty0 + buf * 8u);
             }
             if (!wide) fold(acc + c * LD, v, f[j]);
