@@ -32,7 +32,7 @@ LIBS = {
     "libforge_testkit.so": ["testkit.cu"],
 }
 HEADERS = ["codes.cuh", "common.h", "elem.cuh", "gate.cuh", "host.h", "launch.h", "optim.cuh", "pair_gemm.cuh", "ptx.cuh",
-           "tc_grouped.cuh", "tc_kernel.cuh"]
+           "tc_grouped.cuh", "tc_kernel.cuh", "widths.h"]
 
 
 def nvcc() -> str:

@@ -2,10 +2,12 @@
 // device Philox4x32-10 of optim.cuh, and cuRAND's Philox4_32_10 generator, on
 // caller-given (counter, key) pairs so the two can be compared with each other
 // and with the CPU oracle; and holds SMs for a bounded time, so that a test
-// can launch a kernel that does not find the whole device free.
+// can launch a kernel that does not find the whole device free; and says which
+// width of tiles the pair kernels take for a shape.
 #include <curand_kernel.h>
 
 #include "optim.cuh"
+#include "widths.h"
 
 namespace {
 
@@ -67,6 +69,11 @@ __attribute__((visibility("default"))) int forge_testkit_hold_sms(int blocks, un
   if (e != cudaSuccess) return static_cast<int>(e);
   hold_kernel<<<blocks, 32, static_cast<size_t>(smem), static_cast<cudaStream_t>(stream)>>>(ns);
   return static_cast<int>(cudaGetLastError());
+}
+
+__attribute__((visibility("default"))) int forge_testkit_pick_width(long long rows, long long cols, int halves, int least,
+                                                                     int pairs) {
+  return forge::pick_width(rows, cols, halves, least, pairs);
 }
 
 __attribute__((visibility("default"))) int forge_testkit_philox(const uint32_t* in, uint32_t* out,
