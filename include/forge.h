@@ -439,6 +439,9 @@ typedef enum forge_act { FORGE_ACT_SILU = 0, FORGE_ACT_GELU_TANH = 1 } forge_act
  *   gu_codes  E4M3 codes [T x 2F] with gu_scale [T x 2 x ceil(F / 128)]: the
  *             format of forge_quantize_e4m3 over the [2T x F] matrix, of the
  *             float32 G and U (a scale carries the error of their sums)
+ * The sums are formed in pieces that depend on the shape and on what is kept
+ * (with codes they are cut every 768 terms), so the last bit of an output may
+ * differ with either; for one shape and kind the outputs repeat bit for bit.
  * F % 8 == 0, K % 8 == 0; T, 2F and K within 31 bits; T == 0 or F == 0 does
  * nothing, K == 0 gives zeros.  An infinite G or U gives what the formula
  * does (inf * 0 is NaN).  The outputs overlap neither the inputs nor each other. */
@@ -483,8 +486,10 @@ FORGE_API forge_status_t forge_gated_dgrad(const forge_gated_grad_t* grad, void*
  *   scale = max|x| / 448, at least 2^-126 (so that small blocks lose codes, not
  *           the scale's bits); 0 for a block of zeros; NaN, with NaN codes, for
  *           one that holds a value that is not finite
- *   code  = E4M3(x / scale), to the nearest (x / scale is formed to within
- *           three float32 roundings)
+ *   code  = E4M3(x * r) with r = 1 / scale, both rounded to float32, then to
+ *           the nearest, ties to even: x / scale to within 2^-23 of itself, so
+ *           where that lies as close to the middle between two codes, ties of
+ *           448 x / max|x| among them, it may be either one
  * cols % 8 == 0; rows * cols within 40 bits.  The outputs overlap no input. */
 FORGE_API forge_status_t forge_quantize_e4m3(const void* x, int32_t x_dtype, void* codes, float* scale,
                                              int64_t rows, int64_t cols, int32_t block_rows, void* stream);
