@@ -144,7 +144,7 @@ struct ProductOp {
       int tm, tn;
       tile_coords_of(tile, p.tiles_m, p.tiles_n, tm, tn);
       const int row0 = tm * kPairM + static_cast<int>(rank) * kTileM + quarter * 32, col0 = tn * 2 * W + first;
-      const bool live = row0 < p.T && col0 < p.N;  // else the warp hands the accumulators on unread
+      const bool live = row0 < p.T && col0 < p.N;  // else nothing of the warp's is stored
       float acc[NC];
 #pragma unroll
       for (int i = 0; i < NC; ++i) acc[i] = 0.f;
