@@ -3,9 +3,10 @@
 // block whose largest magnitude is below 448 * 2^-126 then uses only the lower
 // codes), 0 for a block of zeros, NaN for one that holds a value that is not
 // finite.  A code is E4M3(x r), to the nearest, ties to even, with r the float32
-// reciprocal of the scale (one division a block).  Reciprocal and product are rounded once each, so
-// x r is x / scale to within 2^-23 of itself, and the code differs from that of
-// the quotient only where this lies that close to the middle between two codes.
+// reciprocal of the scale (one division a block).  Reciprocal and product are
+// rounded once each, so x r is x / scale to within 2^-23 of itself, and the code
+// differs from that of the quotient only where this lies that close to the
+// middle between two codes.
 // (5 in 10^4 of 17 M bf16 values did, every one an exact tie of 448 x / max|x|:
 // the two codes are equally near, and a quantiser that divides takes the other.)
 #pragma once
