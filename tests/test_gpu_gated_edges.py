@@ -1,4 +1,4 @@
-"""The gate where its sigmoid leaves float32's normal range.
+"""The gate where its sigmoid leaves float32's normal range, and values that are not finite.
 
 Bounds: e = exp(-|z|) carries 2^-22 and |z| 2^-23 of itself, at most 2^-16 for |z| < 110, z of the tanh form four
 float32 roundings of itself, at most 2^-15 of e; what follows adds a few 2^-24: 2^-14 of the value in all.  Below
@@ -8,7 +8,7 @@ value, or half a step of its numbers below 2^-126, 2^-134."""
 import pytest
 import torch
 
-from optimizer_tcgen05_dw_gb300 import api
+from optimizer_tcgen05_dw_gb300 import api, inputs
 from optimizer_tcgen05_dw_gb300.build import build
 from test_gpu_codes import B16, blocks
 from test_gpu_gated import ACTS, act, decoded, forward, gradient
@@ -68,3 +68,28 @@ def test_small_gates_gradient(kind, keep):
     close(dGU[:, F:], a, g.abs())
     close(Y, a * u, (g * u).abs())
     close(dGU[:, :F], slope * u, (1 + 40 * g.abs()) * u.abs())
+
+
+@pytest.mark.parametrize("keep", ["none", "bf16", "e4m3"])
+@pytest.mark.parametrize("T", [5, 24, 40, 300])
+def test_values_that_are_not_finite_stay_where_they_are(T, keep):
+    """A NaN in a token spoils its row, a NaN in a weight its feature, and repeating the call gives the same bits."""
+    F, K = 264, 136
+    X, W = inputs.normal((T, K), 1.0, 1, device="cuda"), inputs.normal((2 * F, K), 0.1, 2, device="cuda")
+    X[T - 1, 7], X[1, K - 1], W[33, 70], W[F + 200, 0] = (float("nan"),) * 4
+    Y, gu, codes, scale = forward(X, W, "silu", keep)
+    bad = torch.zeros((T, F), dtype=torch.bool, device="cuda")
+    bad[T - 1] = bad[1] = True
+    bad[:, 33] = bad[:, 200] = True
+    assert torch.equal(torch.isnan(Y), bad)
+    if keep == "bf16":
+        both = torch.zeros((T, 2 * F), dtype=torch.bool, device="cuda")
+        both[T - 1] = both[1] = True
+        both[:, 33] = both[:, F + 200] = True
+        assert torch.equal(torch.isnan(gu), both)
+    if keep == "e4m3":
+        rows = torch.isnan(scale)
+        assert rows[T - 1].all() and rows[1].all() and rows[:, 0, 0].all() and rows[:, 1, 1].all()
+        assert not rows[0, 0, 1:].any() and not rows[0, 1, 0] and not rows[0, 1, 2]
+    for a, b in zip((Y, gu, codes, scale), forward(X, W, "silu", keep)):
+        assert a is None or torch.equal(a.view(torch.uint8), b.view(torch.uint8))

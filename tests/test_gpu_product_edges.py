@@ -1,5 +1,6 @@
-"""The product of E4M3 codes where a wait runs out with results on their way to
-memory: what was finished arrives whole, and nothing else is written."""
+"""The product of E4M3 codes at its edges: a wait that runs out with results on their
+way to memory (what was finished arrives whole, and nothing else is written), and
+factors of two scales that float32 does not hold."""
 
 import pytest
 import torch
@@ -52,3 +53,24 @@ def test_results_under_way_when_a_wait_runs_out(N):
                 assert (got == 9).all(), (t, n)
     assert done == pairs  # of 9 x 20
     assert torch.equal(_product(*a), want)
+
+
+@pytest.mark.parametrize("T,N", [(5, 264), (13, 2568), (24, 14344), (24, 9656), (24, 4104), (33, 4104), (300, 4104), (2049, 4936)])
+def test_factors_out_of_float32s_range(T, N):
+    """Scales whose product is no ordinary float32, though the values are, in every other row, so that a warp has
+    both; at each width of the tiles.  One block of the reduction at a time, the others zero."""
+    K = 528
+    xq, wq = _whole((T, K), 1), _whole((N, K), 2)
+    scales = ((2.0 ** -120, 2.0 ** -10), (2.0 ** 20, 2.0 ** -20), (2.0 ** 70, 2.0 ** 45), (2.0 ** -90, 2.0 ** -42), (2.0 ** -126, 2.0 ** 3))
+    xs = torch.tensor([[s[0] for s in scales]] * T, device="cuda")
+    xs[1::2] = 1.0
+    ws = torch.tensor([[s[1] for s in scales]] * blocks(N), device="cuda")
+    for b in range(len(scales)):
+        x = torch.zeros_like(xq.float())
+        x[:, b * 128:(b + 1) * 128] = xq.float()[:, b * 128:(b + 1) * 128]
+        x = x.to(xq.dtype)
+        want = _exact(x, xs, wq, ws)[0]
+        assert want.abs().max() < 2.0 ** 127
+        got = _product(x, xs, wq, ws)
+        assert torch.equal(got, want.float().to(B16)), b
+        assert torch.equal(got, _product(x, xs, wq, ws))
